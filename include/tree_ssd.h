@@ -467,6 +467,181 @@ tsv_status tree_ssd_snapshot_commit(const tsv_shape* s, const float* states, flo
                                     const int32_t* accepted_len, int32_t max_path_len, int32_t* tree_status,
                                     void* stream);
 
+/* ------------------------------------------------------------------------
+ * Sequences around the tree: the prompt scan and the single-token step, which
+ * make and advance the state h0 that a tree is verified from. The recurrence
+ * is that of tree_ssd_verify; along a sequence every token has the one before
+ * it as its parent.
+ * ------------------------------------------------------------------------ */
+
+/* Per-item status bit: seq_start is not 0 <= seq_start[0] <= seq_start[1] <=
+ * ... <= n_tokens. The array describes one packing, so the bit is set for
+ * every sequence of the call and nothing is written for any of them. */
+#define TSV_ST_BAD_SEQ 32
+
+typedef struct {
+    int32_t n_seqs;   /* sequences >= 0 (0: nothing to do) */
+    int32_t n_tokens; /* rows of the packed arrays >= 0 */
+    int32_t n_heads;  /* H in [1, 65535] */
+    int32_t head_dim; /* P in [1, 256] */
+    int32_t d_state;  /* N in [1, 256] */
+    int32_t n_groups; /* G >= 1, H % G == 0; head h uses group h / (H / G) */
+    int32_t in_dtype; /* tsv_dtype of x, dt, B, C, y */
+    int32_t flags;    /* TSV_FLAG_FORCE_GENERIC or 0 */
+} tsv_seq_shape;
+
+/*
+ * tree_ssd_prefill -- one SSD layer over packed prompts of any lengths: for
+ * each sequence q, its tokens t = seq_start[q] .. seq_start[q+1] - 1 in order
+ * and each head h, from the state h_inout[q][h],
+ *   H <- exp(dt_t A_h) H + dt_t x_t (outer) B_t,   y_t = H C_t + D_h x_t,
+ * and the state after the last token is written back to h_inout.
+ *
+ *   x      [n_tokens][H][P]  in_dtype   dt [n_tokens][H]  in_dtype (positive)
+ *   A, D   [H]               float
+ *   B, C   [n_tokens][G][N]  in_dtype
+ *   h_inout [n_seqs][H][P][N] float     read, then overwritten
+ *   seq_start [n_seqs + 1]   int32      rows of each sequence
+ *   y      [n_tokens][H][P]  in_dtype   rows of no sequence are left as they were
+ *   seq_status [n_seqs]      int32      optional; TSV_ST_BAD_SEQ or 0
+ *   workspace  device memory of at least the bytes that
+ *              tree_ssd_prefill_workspace gives (16-byte aligned; NULL where
+ *              that is 0), in use until the stream passes this call: calls
+ *              that may overlap need one each
+ * An empty sequence keeps its state. A long sequence is cut into segments that
+ * run side by side, each from the state that the ones before it leave.
+ *
+ * Arithmetic: bf16 inputs with P == 64 and N in {64, 128} take an MFMA kernel
+ * over chunks of 64 tokens: scores and decays in fp32, their masked product
+ * rounded once to bf16 as the operand of the product with x; the state held in
+ * fp32, read out as a bf16 high and low part (16 bits), and updated with
+ * weighted inputs split into three bf16 parts (24 bits). Per-token log decays
+ * below -128 count as -128 (exp of both is 0 in fp32). Other inputs run the
+ * recurrence token by token in fp32.
+ * TSV_E_SHAPE for negative sizes, TSV_E_NULL also for a missing workspace.
+ */
+tsv_status tree_ssd_prefill(const tsv_seq_shape* s, const void* x, const void* dt, const float* A,
+                            const void* B, const void* C, const float* D, float* h_inout,
+                            const int32_t* seq_start, void* y, int32_t* seq_status, void* workspace,
+                            uint64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that tree_ssd_prefill needs for this shape (host only). */
+tsv_status tree_ssd_prefill_workspace(const tsv_seq_shape* s, uint64_t* bytes);
+
+/*
+ * tree_ssd_step -- one token of each item, without a tree: the state is
+ * advanced in place and read out in one pass over it,
+ *   H <- exp(dt A_h) H + dt x (outer) B,   y = H C + D_h x.
+ * What tree_ssd_verify and tree_ssd_commit of a one-node tree give, with the
+ * state read once. s->n_nodes must be 1 (0: nothing to do; TSV_E_SHAPE
+ * otherwise); x, y [Bt][H][P], dt [Bt][H], B, C [Bt][G][N] in in_dtype, A, D
+ * [H], h_inout [Bt][H][P][N] float. fp32 arithmetic. Not idempotent.
+ */
+tsv_status tree_ssd_step(const tsv_shape* s, const void* x, const void* dt, const float* A,
+                         const void* B, const void* C, const float* D, float* h_inout, void* y,
+                         void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention layers of a hybrid model beside its SSM layers: the nodes of a
+ * packed tree (or one new token) attend to a paged key-value cache and to
+ * their ancestors, and the accepted path's rows, or prompts' rows, enter the
+ * cache.
+ *
+ * The cache: k_cache, v_cache [n_pages][n_kv_heads][page_size][head_dim] in
+ * cache_dtype. Position p of item b is row p % page_size of page
+ * page_table[b][p / page_size]; cache_len[b] positions are filled. A cache in
+ * TSV_E4M3 (OCP e4m3, 1 sign, 4 exponent and 3 mantissa bits, largest value
+ * 448) has a scale for each row and head, k_scale, v_scale
+ * [n_pages][n_kv_heads][page_size] float: an element stands for byte * scale.
+ * Scales are NULL for other caches. Pages may be shared by items as long as no
+ * call writes to a shared position.
+ * ------------------------------------------------------------------------ */
+
+/* cache_dtype of a cache in 8 bits, beside the tsv_dtype values */
+#define TSV_E4M3 2
+
+/* Per-item status bit: cache_len (with the rows to write) is not in
+ * [0, max_pages * page_size], or a page index that the call uses is not in
+ * [0, n_pages) */
+#define TSV_ST_BAD_CACHE 64
+
+typedef struct {
+    int32_t batch;       /* Bt >= 0 (0: nothing to do) */
+    int32_t n_nodes;     /* T in [0, 1024]; tree_attn_append: rows of k and v */
+    int32_t n_heads;     /* query heads H >= 1 */
+    int32_t n_kv_heads;  /* Hk >= 1, H % Hk == 0; head h reads key head h / (H / Hk) */
+    int32_t head_dim;    /* D in [1, 256] */
+    int32_t n_pages;     /* pages of the pool >= 0 */
+    int32_t page_size;   /* positions per page, in [1, 65536] */
+    int32_t max_pages;   /* row length of page_table >= 0; max_pages * page_size < 2^31 */
+    int32_t in_dtype;    /* tsv_dtype of q, k, v, o */
+    int32_t cache_dtype; /* in_dtype or TSV_E4M3 (TSV_E_UNSUPPORTED for other pairs) */
+    int32_t flags;       /* TSV_FLAG_FORCE_GENERIC or 0 */
+    float scale;         /* factor of the scores, usually head_dim^-1/2 (finite) */
+} tsv_attn_shape;
+
+/*
+ * tree_attn_verify -- attention of every node of a packed tree: node i of item
+ * b attends to the cache's positions 0 .. cache_len[b] - 1 and to the nodes on
+ * its root path, itself included,
+ *   o_i = sum_j softmax_j(scale q_i . k_j) v_j.
+ * A tree of one node is plain decoding: the new token's own k and v beside the
+ * cache. The cache is not written (tree_attn_commit does that).
+ *
+ *   q, o   [Bt][T][H][D]    in_dtype
+ *   k, v   [Bt][T][Hk][D]   in_dtype   the nodes' own keys and values
+ *   parent [Bt][T]          int32      as for tree_ssd_verify
+ *   page_table [Bt][max_pages] int32, cache_len [Bt] int32
+ *   tree_status [Bt]        optional; bits 1|2 and TSV_ST_BAD_CACHE
+ *   workspace  as for tree_ssd_prefill, with tree_attn_verify_workspace
+ * Items with a status bit keep their o. The work is split over the cache's
+ * length by the lengths found on the device, so short and long items may share
+ * a batch; a second launch joins the parts.
+ *
+ * Arithmetic: fp32 scores, maxima, sums and accumulators. bf16 inputs with D
+ * 64 or 128 use bf16 MFMA; the softmax weights (times the scale of an 8-bit
+ * value row) are rounded once to bf16 for the product with v. Other shapes and
+ * fp32 inputs use fp32 throughout.
+ */
+tsv_status tree_attn_verify(const tsv_attn_shape* s, const void* q, const void* k, const void* v,
+                            const int32_t* parent, const void* k_cache, const void* v_cache,
+                            const float* k_scale, const float* v_scale, const int32_t* page_table,
+                            const int32_t* cache_len, void* o, int32_t* tree_status, void* workspace,
+                            uint64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that tree_attn_verify needs for this shape (host only). */
+tsv_status tree_attn_verify_workspace(const tsv_attn_shape* s, uint64_t* bytes);
+
+/*
+ * tree_attn_commit -- the accepted path's keys and values enter the cache: row
+ * accepted[b][i] of k and v goes to position cache_len[b] + i, i <
+ * accepted_len[b]. The layers of a model share cache_len, so it is read only;
+ * the caller adds accepted_len to it after the last layer.
+ *   k, v, parent, page_table, cache_len as for tree_attn_verify; accepted,
+ *   accepted_len, max_path_len and tree_status as for tree_ssd_commit, with
+ *   TSV_ST_BAD_CACHE. Items with a status bit are not written.
+ * Rows are stored as they are, or for TSV_E4M3 with
+ *   scale = max(max|row| / 448, 2^-126),  byte = row / scale rounded to even;
+ * a row with a NaN or an infinity reads back as NaN.
+ */
+tsv_status tree_attn_commit(const tsv_attn_shape* s, const void* k, const void* v, const int32_t* parent,
+                            const int32_t* accepted, const int32_t* accepted_len, int32_t max_path_len,
+                            const int32_t* page_table, const int32_t* cache_len, void* k_cache,
+                            void* v_cache, float* k_scale, float* v_scale, int32_t* tree_status,
+                            void* stream);
+
+/*
+ * tree_attn_append -- packed prompts' keys and values enter the cache: row
+ * seq_start[b] + i of k and v [n_nodes][Hk][D] goes to position cache_len[b] +
+ * i of item b. seq_start [Bt + 1] and seq_status (TSV_ST_BAD_SEQ and
+ * TSV_ST_BAD_CACHE) as for tree_ssd_prefill; storage as for tree_attn_commit;
+ * cache_len is read only.
+ */
+tsv_status tree_attn_append(const tsv_attn_shape* s, const void* k, const void* v, const int32_t* seq_start,
+                            const int32_t* page_table, const int32_t* cache_len, void* k_cache,
+                            void* v_cache, float* k_scale, float* v_scale, int32_t* seq_status,
+                            void* stream);
+
 /* Static, human-readable name of a tsv_status value. */
 const char* tree_ssd_status_string(int32_t status);
 

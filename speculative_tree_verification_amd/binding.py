@@ -7,8 +7,10 @@ for device memory and streams only. There is no fallback: if the library is
 missing, importing this module raises.
 
 Entry points mirror include/tree_ssd.h: ``verify``, ``commit``,
-``commit_layers``, ``accept_greedy``, ``tree_info``, and for the gated delta
-rule ``gdn_verify`` and ``gdn_commit``.
+``commit_layers``, ``accept_greedy``, ``tree_info``, for the gated delta rule
+``gdn_verify`` and ``gdn_commit``, for sequences around the tree ``prefill``
+and ``step``, and for a hybrid model's attention layers ``attn_verify``,
+``attn_commit`` and ``attn_append``.
 """
 from __future__ import annotations
 
@@ -35,10 +37,14 @@ EXPORTS = ("tree_ssd_verify", "tree_ssd_commit", "tree_ssd_commit_layers", "tree
            "tree_ssd_tree_info", "tree_ssd_status_string", "tree_ssd_abi_version", "tree_gdn_verify",
            "tree_gdn_commit", "tree_ssd_unroll_plan", "tree_ssd_unroll_gather", "tree_ssd_seq_scan",
            "tree_ssd_snapshot_verify", "tree_ssd_snapshot_commit", "tree_ssd_accept_stochastic",
-           "tree_ssd_commit_layers_static")
+           "tree_ssd_commit_layers_static", "tree_ssd_prefill", "tree_ssd_prefill_workspace", "tree_ssd_step",
+           "tree_attn_verify", "tree_attn_verify_workspace", "tree_attn_commit", "tree_attn_append")
 STATIC_MAX_LAYERS = 1024  # TSV_STATIC_MAX_LAYERS
 ST_OVER_CAPACITY = 8
 ST_BAD_TOKEN = 16
+ST_BAD_SEQ = 32
+ST_BAD_CACHE = 64
+TSV_E4M3 = 2
 
 
 class Shape(ctypes.Structure):
@@ -47,6 +53,19 @@ class Shape(ctypes.Structure):
                 ("d_state", ctypes.c_int32), ("n_groups", ctypes.c_int32),
                 ("in_dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
                 ("heads_per_block", ctypes.c_int32)]
+
+
+class SeqShape(ctypes.Structure):
+    """tsv_seq_shape"""
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_tokens", "n_heads", "head_dim", "d_state", "n_groups",
+                                              "in_dtype", "flags")]
+
+
+class AttnShape(ctypes.Structure):
+    """tsv_attn_shape"""
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "n_nodes", "n_heads", "n_kv_heads", "head_dim", "n_pages",
+                                              "page_size", "max_pages", "in_dtype", "cache_dtype", "flags")] + \
+        [("scale", ctypes.c_float)]
 
 
 class CommitLayer(ctypes.Structure):
@@ -106,6 +125,17 @@ def _load():
     L.tree_ssd_snapshot_verify.restype = ctypes.c_int
     L.tree_ssd_snapshot_commit.argtypes = [ctypes.POINTER(Shape)] + [_VP] * 5 + [ctypes.c_int32, _VP, _VP]
     L.tree_ssd_snapshot_commit.restype = ctypes.c_int
+    u64 = ctypes.c_uint64
+    L.tree_ssd_prefill.argtypes = [ctypes.POINTER(SeqShape)] + [_VP] * 11 + [u64, _VP]
+    L.tree_ssd_prefill_workspace.argtypes = [ctypes.POINTER(SeqShape), ctypes.POINTER(u64)]
+    L.tree_ssd_step.argtypes = [ctypes.POINTER(Shape)] + [_VP] * 9
+    L.tree_attn_verify.argtypes = [ctypes.POINTER(AttnShape)] + [_VP] * 13 + [u64, _VP]
+    L.tree_attn_verify_workspace.argtypes = [ctypes.POINTER(AttnShape), ctypes.POINTER(u64)]
+    L.tree_attn_commit.argtypes = [ctypes.POINTER(AttnShape)] + [_VP] * 5 + [ctypes.c_int32] + [_VP] * 8
+    L.tree_attn_append.argtypes = [ctypes.POINTER(AttnShape)] + [_VP] * 11
+    for f in (L.tree_ssd_prefill, L.tree_ssd_prefill_workspace, L.tree_ssd_step, L.tree_attn_verify,
+              L.tree_attn_verify_workspace, L.tree_attn_commit, L.tree_attn_append):
+        f.restype = ctypes.c_int
     return L
 
 
@@ -862,3 +892,239 @@ class PreparedSnapshot:
         rc = lib.tree_ssd_snapshot_commit(ctypes.byref(self.cshape), _ptr(self.states), _ptr(h), *self.commit_tail)
         if rc != 0:
             raise TreeSSDError(rc, "tree_ssd_snapshot_commit")
+
+
+# ---- sequences around the tree, and the paged cache of attention layers
+class _Launch:
+    """What one call needs of torch: the tensors' device made current (the
+    library launches on the current device), and the stream, also as the one
+    that buffers made here belong to."""
+
+    def __init__(self, dev, stream):
+        if dev.type != "cuda":
+            raise ValueError(f"tensors must be on a GPU, got {dev}")
+        self.device = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+        if stream is None:
+            self.stream, self.alloc = torch.cuda.current_stream(dev), None
+        else:
+            self.stream, self.alloc = stream, _on_stream(stream)
+
+    def __enter__(self):
+        if self.device is not None:
+            self.device.__enter__()
+        if self.alloc is not None:
+            self.alloc.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.alloc is not None:
+            self.alloc.__exit__(*exc)
+        if self.device is not None:
+            self.device.__exit__(*exc)
+
+
+def _workspace(query, shape, given, dev):
+    """(tensor or None, bytes) of at least what ``query`` says, made here if not given."""
+    need = ctypes.c_uint64()
+    rc = query(ctypes.byref(shape), ctypes.byref(need))
+    if rc != 0:
+        raise TreeSSDError(rc, query.__name__)
+    if given is not None:
+        if given.device != dev or not given.is_contiguous():
+            raise ValueError("workspace must be contiguous and on the tensors' device")
+        size = given.numel() * given.element_size()
+        if size < need.value:
+            raise ValueError(f"workspace has {size} bytes, {need.value} are needed")
+        return given, size
+    if need.value == 0:
+        return None, 0
+    return torch.empty(need.value, dtype=torch.uint8, device=dev), need.value
+
+
+def prefill_workspace_bytes(n_seqs, n_tokens, n_heads, head_dim, d_state, n_groups=1, dtype=torch.bfloat16) -> int:
+    """Bytes of workspace a ``prefill`` of these sizes needs."""
+    shape = SeqShape(n_seqs, n_tokens, n_heads, head_dim, d_state, n_groups,
+                     TSV_BF16 if dtype == torch.bfloat16 else TSV_F32, 0)
+    need = ctypes.c_uint64()
+    rc = lib.tree_ssd_prefill_workspace(ctypes.byref(shape), ctypes.byref(need))
+    if rc != 0:
+        raise TreeSSDError(rc, "tree_ssd_prefill_workspace")
+    return need.value
+
+
+def prefill(x, dt, A, B, C, D, h, seq_start, y=None, seq_status=None, workspace=None, stream=None,
+            force_generic: bool = False):
+    """y [L,H,P] of one SSD layer over packed prompts, and h [n,H,P,N] advanced
+    over them in place (tree_ssd_prefill): x [L,H,P], dt [L,H], B, C [L,G,N],
+    seq_start [n+1] int32. ``workspace`` (a tensor of at least
+    ``prefill_workspace_bytes``) is made here if not given; calls that may
+    overlap need one each."""
+    L, H, P = x.shape
+    G, N = B.shape[1], B.shape[2]
+    n, dev, io = h.shape[0], x.device, x.dtype
+    _check(x, "x", (L, H, P), io, dev)
+    _check(dt, "dt", (L, H), io, dev)
+    _check(A, "A", (H,), torch.float32, dev)
+    _check(B, "B", (L, G, N), io, dev)
+    _check(C, "C", (L, G, N), io, dev)
+    _check(D, "D", (H,), torch.float32, dev)
+    _check(h, "h", (n, H, P, N), torch.float32, dev)
+    _check(seq_start, "seq_start", (n + 1,), torch.int32, dev)
+    if seq_status is not None:
+        _check(seq_status, "seq_status", (n,), torch.int32, dev)
+    shape = SeqShape(n, L, H, P, N, G, _dtype_code(x), TSV_FLAG_FORCE_GENERIC if force_generic else 0)
+    with _Launch(dev, stream) as s:
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _check(y, "y", (L, H, P), io, dev)
+        ws, size = _workspace(lib.tree_ssd_prefill_workspace, shape, workspace, dev)
+        rc = lib.tree_ssd_prefill(ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(h),
+                                  _ptr(seq_start), _ptr(y), _ptr(seq_status), _ptr(ws) if ws is not None else None,
+                                  size, s)
+    if rc != 0:
+        raise TreeSSDError(rc, "tree_ssd_prefill")
+    return y
+
+
+def step(x, dt, A, B, C, D, h, y=None, stream=None):
+    """y [Bt,H,P] of one token of each item, and h [Bt,H,P,N] advanced by it in
+    place (tree_ssd_step): x [Bt,H,P], dt [Bt,H], B, C [Bt,G,N]."""
+    Bt, H, P = x.shape
+    G, N = B.shape[1], B.shape[2]
+    dev, io = x.device, x.dtype
+    _check(x, "x", (Bt, H, P), io, dev)
+    _check(dt, "dt", (Bt, H), io, dev)
+    _check(A, "A", (H,), torch.float32, dev)
+    _check(B, "B", (Bt, G, N), io, dev)
+    _check(C, "C", (Bt, G, N), io, dev)
+    _check(D, "D", (H,), torch.float32, dev)
+    _check(h, "h", (Bt, H, P, N), torch.float32, dev)
+    shape = Shape(Bt, 1, H, P, N, G, _dtype_code(x), 0, 0)
+    with _Launch(dev, stream) as s:
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _check(y, "y", (Bt, H, P), io, dev)
+        rc = lib.tree_ssd_step(ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(h),
+                               _ptr(y), s)
+    if rc != 0:
+        raise TreeSSDError(rc, "tree_ssd_step")
+    return y
+
+
+def _attn_shape(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, batch, rows, n_heads, scale,
+                force_generic) -> AttnShape:
+    """Checks what every attention call has of the cache, and fills tsv_attn_shape."""
+    dev = k.device
+    n_pages, Hk, page_size, D = k_cache.shape
+    if k.shape[-2:] != (Hk, D):
+        raise ValueError(f"k: heads and head_dim {tuple(k.shape[-2:])} != the cache's {(Hk, D)}")
+    e4m3 = k_cache.dtype == torch.float8_e4m3fn
+    if not e4m3 and k_cache.dtype != k.dtype:
+        raise TypeError(f"k_cache: dtype {k_cache.dtype} is neither {k.dtype} nor torch.float8_e4m3fn")
+    _check(k_cache, "k_cache", (n_pages, Hk, page_size, D), k_cache.dtype, dev)
+    _check(v_cache, "v_cache", (n_pages, Hk, page_size, D), k_cache.dtype, dev)
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if e4m3:
+            if t is None:
+                raise ValueError(f"{name} is needed with an e4m3 cache")
+            _check(t, name, (n_pages, Hk, page_size), torch.float32, dev)
+        elif t is not None:
+            raise ValueError(f"{name} goes with an e4m3 cache only")
+    _check(page_table, "page_table", (batch, page_table.shape[1]), torch.int32, dev)
+    _check(cache_len, "cache_len", (batch,), torch.int32, dev)
+    io = _dtype_code(k)
+    return AttnShape(batch, rows, n_heads, Hk, D, n_pages, page_size, page_table.shape[1], io,
+                     TSV_E4M3 if e4m3 else io, TSV_FLAG_FORCE_GENERIC if force_generic else 0, scale)
+
+
+def attn_verify(q, k, v, parent, k_cache, v_cache, page_table, cache_len, k_scale=None, v_scale=None,
+                scale: Optional[float] = None, o=None, tree_status=None, workspace=None, stream=None,
+                force_generic: bool = False):
+    """o [Bt,T,H,D]: every tree node's attention over the paged cache and its
+    ancestors (tree_attn_verify). q [Bt,T,H,D], k, v [Bt,T,Hk,D], caches
+    [n_pages,Hk,page_size,D] in q's dtype or float8_e4m3fn with k_scale,
+    v_scale [n_pages,Hk,page_size]. ``scale`` defaults to D**-0.5. One node per
+    item is plain decoding."""
+    Bt, T, H, D = q.shape
+    dev, io = q.device, q.dtype
+    Hk = k.shape[2]
+    _check(q, "q", (Bt, T, H, D), io, dev)
+    _check(k, "k", (Bt, T, Hk, D), io, dev)
+    _check(v, "v", (Bt, T, Hk, D), io, dev)
+    _check(parent, "parent", (Bt, T), torch.int32, dev)
+    if tree_status is not None:
+        _check(tree_status, "tree_status", (Bt,), torch.int32, dev)
+    shape = _attn_shape(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, T, H,
+                        D ** -0.5 if scale is None else float(scale), force_generic)
+    with _Launch(dev, stream) as s:
+        if o is None:
+            o = torch.empty_like(q)
+        else:
+            _check(o, "o", (Bt, T, H, D), io, dev)
+        ws, size = _workspace(lib.tree_attn_verify_workspace, shape, workspace, dev)
+        rc = lib.tree_attn_verify(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(parent), _ptr(k_cache),
+                                  _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(cache_len),
+                                  _ptr(o), _ptr(tree_status), _ptr(ws) if ws is not None else None, size, s)
+    if rc != 0:
+        raise TreeSSDError(rc, "tree_attn_verify")
+    return o
+
+
+def attn_verify_workspace_bytes(batch, n_nodes, n_heads, n_kv_heads, head_dim, page_size, max_pages,
+                                dtype=torch.bfloat16, cache_dtype=None) -> int:
+    """Bytes of workspace an ``attn_verify`` of these sizes needs."""
+    io = TSV_BF16 if dtype == torch.bfloat16 else TSV_F32
+    shape = AttnShape(batch, n_nodes, n_heads, n_kv_heads, head_dim, 1, page_size, max_pages, io,
+                      TSV_E4M3 if cache_dtype == torch.float8_e4m3fn else io, 0, 1.0)
+    need = ctypes.c_uint64()
+    rc = lib.tree_attn_verify_workspace(ctypes.byref(shape), ctypes.byref(need))
+    if rc != 0:
+        raise TreeSSDError(rc, "tree_attn_verify_workspace")
+    return need.value
+
+
+def attn_commit(k, v, parent, accepted, accepted_len, k_cache, v_cache, page_table, cache_len, k_scale=None,
+                v_scale=None, tree_status=None, stream=None):
+    """Write the accepted paths' rows of k, v [Bt,T,Hk,D] into the cache behind
+    its cache_len positions (tree_attn_commit; cache_len is not changed)."""
+    Bt, T, Hk, D = k.shape
+    dev, io = k.device, k.dtype
+    Lmax = accepted.shape[1]
+    _check(k, "k", (Bt, T, Hk, D), io, dev)
+    _check(v, "v", (Bt, T, Hk, D), io, dev)
+    _check(parent, "parent", (Bt, T), torch.int32, dev)
+    _check(accepted, "accepted", (Bt, Lmax), torch.int32, dev)
+    _check(accepted_len, "accepted_len", (Bt,), torch.int32, dev)
+    if tree_status is not None:
+        _check(tree_status, "tree_status", (Bt,), torch.int32, dev)
+    shape = _attn_shape(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, T, Hk, 1.0, False)
+    with _Launch(dev, stream) as s:
+        rc = lib.tree_attn_commit(ctypes.byref(shape), _ptr(k), _ptr(v), _ptr(parent), _ptr(accepted),
+                                  _ptr(accepted_len), int(Lmax), _ptr(page_table), _ptr(cache_len), _ptr(k_cache),
+                                  _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(tree_status), s)
+    if rc != 0:
+        raise TreeSSDError(rc, "tree_attn_commit")
+
+
+def attn_append(k, v, seq_start, k_cache, v_cache, page_table, cache_len, k_scale=None, v_scale=None,
+                seq_status=None, stream=None):
+    """Write packed prompts' rows k, v [L,Hk,D] (seq_start [Bt+1] int32) into
+    the cache behind its cache_len positions (tree_attn_append; cache_len is
+    not changed)."""
+    L, Hk, D = k.shape
+    dev, io = k.device, k.dtype
+    Bt = cache_len.shape[0]
+    _check(k, "k", (L, Hk, D), io, dev)
+    _check(v, "v", (L, Hk, D), io, dev)
+    _check(seq_start, "seq_start", (Bt + 1,), torch.int32, dev)
+    if seq_status is not None:
+        _check(seq_status, "seq_status", (Bt,), torch.int32, dev)
+    shape = _attn_shape(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, L, Hk, 1.0, False)
+    with _Launch(dev, stream) as s:
+        rc = lib.tree_attn_append(ctypes.byref(shape), _ptr(k), _ptr(v), _ptr(seq_start), _ptr(page_table),
+                                  _ptr(cache_len), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                  _ptr(seq_status), s)
+    if rc != 0:
+        raise TreeSSDError(rc, "tree_attn_append")

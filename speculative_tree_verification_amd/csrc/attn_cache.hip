@@ -1,0 +1,272 @@
+// attn_cache.hip -- rows of keys and values into the paged cache: the accepted
+// path of each item (tree_attn_commit) or packed prompts (tree_attn_append),
+// as they are or in 8 bits.
+//
+//   position p of item b is row p % page_size of page table[b][p / page_size];
+//   e4m3: scale = max(max|row| / 448, 2^-126), byte = row / scale to even.
+//
+// Bound by the rows' traffic (in: Hk D elements of k and of v each, out: the
+// same in the cache's type). A row of one head is held by LPR lanes with 8
+// elements each: one 16-byte load (bf16), a butterfly over the lanes for the
+// largest value, one store of 8 bytes (e4m3) or 16. The division is a true one,
+// so that the stored byte is the nearest to row / scale. A work-group first
+// checks everything that its rows' items need (path, lengths, pages), so that
+// an item with a status bit is left whole.
+#include "attn_common.hpp"
+
+namespace tsv {
+namespace {
+
+struct Quad {
+    float v[8];
+};
+
+template <typename TIO, bool VEC>
+__device__ __forceinline__ Quad load8(const TIO* p, int rem) {
+    Quad q;
+    if (VEC) {
+        if (sizeof(TIO) == 2) {
+            const uint4 u = gload((const uint4*)p);
+            const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                q.v[2 * i] = __uint_as_float(wd[i] << 16);
+                q.v[2 * i + 1] = __uint_as_float(wd[i] & 0xffff0000u);
+            }
+        } else {
+            const float4 a = gload((const float4*)p), b = gload((const float4*)p + 1);
+            q.v[0] = a.x; q.v[1] = a.y; q.v[2] = a.z; q.v[3] = a.w;
+            q.v[4] = b.x; q.v[5] = b.y; q.v[6] = b.z; q.v[7] = b.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q.v[i] = i < rem ? Elem<TIO>::ld(p, i) : 0.f;
+    }
+    return q;
+}
+
+// The cache's element: TIO, or a byte with a scale (E4M3)
+template <typename TIO, bool E4M3, bool VEC>
+__device__ __forceinline__ void store8(const CacheWriteArgs& a, bool value, size_t at, int d, int rem, const Quad& q,
+                                       float scale, bool finite) {
+    if (E4M3) {
+        uint32_t by[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) by[i] = finite ? e4m3_byte(q.v[i] / scale) : 0x7fu;
+        uint8_t* o = (uint8_t*)(value ? a.v_cache : a.k_cache) + at * a.D + d;
+        if (VEC) {
+            gstore((uint2*)o, make_uint2(by[0] | by[1] << 8 | by[2] << 16 | by[3] << 24,
+                                         by[4] | by[5] << 8 | by[6] << 16 | by[7] << 24));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < rem) o[i] = (uint8_t)by[i];
+        }
+        if (d == 0) (value ? a.v_scale : a.k_scale)[at] = scale;
+    } else {
+        TIO* o = (TIO*)(value ? a.v_cache : a.k_cache) + at * a.D + d;
+        if (VEC) {
+            if (sizeof(TIO) == 2) {
+                // bf16 values: the upper halves are exact
+                gstore((uint4*)o, make_uint4(__float_as_uint(q.v[0]) >> 16 | (__float_as_uint(q.v[1]) & 0xffff0000u),
+                                             __float_as_uint(q.v[2]) >> 16 | (__float_as_uint(q.v[3]) & 0xffff0000u),
+                                             __float_as_uint(q.v[4]) >> 16 | (__float_as_uint(q.v[5]) & 0xffff0000u),
+                                             __float_as_uint(q.v[6]) >> 16 | (__float_as_uint(q.v[7]) & 0xffff0000u)));
+            } else {
+                gstore((float4*)o, make_float4(q.v[0], q.v[1], q.v[2], q.v[3]));
+                gstore((float4*)o + 1, make_float4(q.v[4], q.v[5], q.v[6], q.v[7]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < rem) {
+                    if (sizeof(TIO) == 2)
+                        ((uint16_t*)o)[i] = (uint16_t)(__float_as_uint(q.v[i]) >> 16);
+                    else
+                        ((float*)o)[i] = q.v[i];
+                }
+        }
+    }
+}
+
+// Status bits of writing `count` rows at cache_len[b]: the same in all threads.
+// Acts as a barrier.
+__device__ __forceinline__ int check_pages(const CacheWriteArgs& a, int b, int count) {
+    const int room = a.max_pages * a.page_size, len = a.cache_len[b];
+    int bad = len < 0 || count < 0 || len > room || count > room - len;
+    if (!bad && count > 0) {
+        const int first = page_of(len, a.div), last = page_of(len + count - 1, a.div);
+        for (int i = first + threadIdx.x; i <= last; i += blockDim.x) {
+            const int pg = a.page_table[(size_t)b * a.max_pages + i];
+            bad |= pg < 0 || pg >= a.n_pages;
+        }
+    }
+    return __syncthreads_or(bad) ? kStBadCache : 0;
+}
+
+// Rows r0 .. r0 + n - 1 (at most kRows) with their source rows and destination
+// sequences and positions in LDS (position -1: not written): all heads, keys
+// and values.
+constexpr int kRows = 16;
+template <typename TIO, int LPR, bool E4M3, bool VEC>
+__device__ __forceinline__ void write_rows(const CacheWriteArgs& a, int n, const long long* s_src, const int* s_item,
+                                           const int* s_pos) {
+    const int lane = threadIdx.x % LPR, d = lane * 8, rem = a.D - d;
+    const int per = 256 / LPR, work = n * a.Hk * 2;
+    for (int u0 = 0; u0 < work; u0 += per) {
+        const int u = u0 + threadIdx.x / LPR;  // row, k or v, head: heads fastest
+        const bool in = u < work;
+        const int row = in ? u / (2 * a.Hk) : 0, hv = in ? u % (2 * a.Hk) : 0;
+        const bool value = hv >= a.Hk;
+        const int hk = value ? hv - a.Hk : hv;
+        const int pos = in ? s_pos[row] : -1;
+        Quad q;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q.v[i] = 0.f;
+        if (pos >= 0 && rem > 0)
+            q = load8<TIO, VEC>((const TIO*)(value ? a.v : a.k) + ((size_t)s_src[row] * a.Hk + hk) * a.D + d, rem);
+        float scale = 1.f;
+        bool finite = true;
+        if (E4M3) {
+            float top = 0.f;
+            int odd = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                top = fmaxf(top, fabsf(q.v[i]));
+                odd |= !(fabsf(q.v[i]) <= 3.402823466e38f);  // an infinity or a NaN, which fmaxf passes over
+            }
+#pragma unroll
+            for (int m = 1; m < LPR; m <<= 1) {
+                top = fmaxf(top, __shfl_xor(top, m, kWave));
+                odd |= __shfl_xor(odd, m, kWave);
+            }
+            finite = !odd;
+            scale = finite ? fmaxf(top / 448.f, 1.17549435e-38f) : __uint_as_float(0x7fc00000u);
+        }
+        if (pos >= 0 && rem > 0) {
+            const int page = page_of(pos, a.div);
+            const int pg = a.page_table[(size_t)s_item[row] * a.max_pages + page];
+            const size_t at = ((size_t)pg * a.Hk + hk) * a.page_size + (pos - page * a.page_size);
+            store8<TIO, E4M3, VEC>(a, value, at, d, rem, q, scale, finite);
+        }
+    }
+}
+
+template <typename TIO, int LPR, bool E4M3, bool VEC>
+__global__ __launch_bounds__(256) void append_kernel(CacheWriteArgs a, int row_blocks) {
+    __shared__ long long s_src[kRows];
+    __shared__ int s_item[kRows], s_pos[kRows], s_first;
+    const int tid = threadIdx.x;
+    // the packing, and the sequence of this block's first row: the sequences
+    // that end at or before it
+    const int r0 = blockIdx.x * kRows;
+    if (tid == 0) s_first = 0;
+    __syncthreads();
+    int bad = 0, before = 0;
+    for (int q = tid; q < a.batch; q += 256) {
+        const int lo = a.seq_start[q], hi = a.seq_start[q + 1];
+        bad |= lo < 0 || hi < lo || hi > a.T;
+        before += hi <= r0;
+    }
+    if (before) atomicAdd(&s_first, before);
+    bad = __syncthreads_or(bad);
+    if ((int)blockIdx.x >= row_blocks) {  // a block for each item's status
+        const int b = blockIdx.x - row_blocks;
+        const int st = bad ? kStBadSeqRows : check_pages(a, b, a.seq_start[b + 1] - a.seq_start[b]);
+        if (tid == 0) a.status[b] = st;
+        return;
+    }
+    if (bad) return;
+    const int n = min(kRows, a.T - r0);
+    if (tid < kRows) {
+        int q = s_first, pos = -1;
+        const int r = r0 + tid;
+        while (q < a.batch && a.seq_start[q + 1] <= r) ++q;
+        if (tid < n && q < a.batch && r >= a.seq_start[q]) pos = r - a.seq_start[q];  // + cache_len below
+        s_item[tid] = q < a.batch ? q : 0;
+        s_src[tid] = r;
+        s_pos[tid] = pos;
+    }
+    __syncthreads();
+    for (int i = 0; i < n; ++i) {
+        const int b = s_item[i];
+        if (s_pos[i] < 0 || (i > 0 && s_pos[i - 1] >= 0 && s_item[i - 1] == b)) continue;
+        const int st = check_pages(a, b, a.seq_start[b + 1] - a.seq_start[b]);
+        const int len = a.cache_len[b];
+        // thread i' owns row i': rows of item b start here
+        if (tid >= i && tid < n && s_item[tid] == b && s_pos[tid] >= 0) s_pos[tid] = st ? -2 : s_pos[tid] + len;
+        __syncthreads();
+    }
+    write_rows<TIO, LPR, E4M3, VEC>(a, n, s_src, s_item, s_pos);
+}
+
+template <typename TIO, int LPR, bool E4M3, bool VEC>
+__global__ __launch_bounds__(256) void commit_kernel(CacheWriteArgs a, int chunks) {
+    __shared__ long long s_src[kRows];
+    __shared__ int s_item[kRows], s_pos[kRows];
+    const int tid = threadIdx.x, b = blockIdx.x / chunks, c = blockIdx.x % chunks;
+    const int32_t* par = a.parent + (size_t)b * a.T;
+    int bits = 0;
+    for (int i = tid; i < a.T; i += 256) {
+        const int p = par[i];
+        bits |= i == 0 ? (p != -1 ? kStBadRoot : 0) : (p < 0 || p >= i ? kStBadParent : 0);
+    }
+    const int len = a.accepted_len[b];
+    const bool fits = len >= 0 && len <= a.Lmax && len <= a.T;
+    if (!fits) bits |= kStBadPath;
+    const int32_t* acc = a.accepted + (size_t)b * a.Lmax;
+    for (int i = tid; fits && i < len; i += 256) {
+        const int node = acc[i];
+        const int want = i == 0 ? -1 : acc[i - 1];
+        if (node < 0 || node >= a.T || (i == 0 ? node != 0 : par[node] != want)) bits |= kStBadPath;
+    }
+    int st = (__syncthreads_or(bits & kStBadRoot) ? kStBadRoot : 0) | (__syncthreads_or(bits & kStBadParent) ? kStBadParent : 0) |
+             (__syncthreads_or(bits & kStBadPath) ? kStBadPath : 0);
+    st |= check_pages(a, b, fits ? len : 0);
+    if (c == 0 && tid == 0 && a.status) a.status[b] = st;
+    if (st) return;
+    const int n = min(kRows, len - c * kRows);
+    if (n <= 0) return;
+    if (tid < kRows) {
+        const int i = c * kRows + tid;
+        s_item[tid] = b;
+        s_src[tid] = tid < n ? (long long)b * a.T + acc[i] : 0;
+        s_pos[tid] = tid < n ? a.cache_len[b] + i : -1;
+    }
+    __syncthreads();
+    write_rows<TIO, LPR, E4M3, VEC>(a, n, s_src, s_item, s_pos);
+}
+
+template <typename TIO, int LPR, bool E4M3, bool VEC>
+hipError_t launch_one(const CacheWriteArgs& a, hipStream_t stream) {
+    if (a.seq_start) {
+        const int blocks = (a.T + kRows - 1) / kRows;
+        const int all = blocks + (a.status ? a.batch : 0);
+        if (all > 0)
+            hipLaunchKernelGGL((append_kernel<TIO, LPR, E4M3, VEC>), dim3(all), dim3(256), 0, stream, a, blocks);
+    } else {
+        const int chunks = max(1, (min(a.Lmax, a.T) + kRows - 1) / kRows);
+        hipLaunchKernelGGL((commit_kernel<TIO, LPR, E4M3, VEC>), dim3((unsigned)((long long)a.batch * chunks)), dim3(256), 0,
+                           stream, a, chunks);
+    }
+    return hipGetLastError();
+}
+
+template <typename TIO, bool E4M3>
+hipError_t launch_type(const CacheWriteArgs& a, hipStream_t stream) {
+    // 8 elements at a time where rows and pointers allow it
+    const uintptr_t in = (uintptr_t)a.k | (uintptr_t)a.v, out = (uintptr_t)a.k_cache | (uintptr_t)a.v_cache;
+    const bool vec = a.D % 8 == 0 && in % 16 == 0 && out % (E4M3 ? 8 : 16) == 0;
+    if (a.D <= 64) return vec ? launch_one<TIO, 8, E4M3, true>(a, stream) : launch_one<TIO, 8, E4M3, false>(a, stream);
+    if (a.D <= 128) return vec ? launch_one<TIO, 16, E4M3, true>(a, stream) : launch_one<TIO, 16, E4M3, false>(a, stream);
+    return vec ? launch_one<TIO, 32, E4M3, true>(a, stream) : launch_one<TIO, 32, E4M3, false>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_cache_write(const CacheWriteArgs& a, bool bf16, bool e4m3, hipStream_t stream) {
+    if (bf16) return e4m3 ? launch_type<uint16_t, true>(a, stream) : launch_type<uint16_t, false>(a, stream);
+    return e4m3 ? launch_type<float, true>(a, stream) : launch_type<float, false>(a, stream);
+}
+
+}  // namespace tsv

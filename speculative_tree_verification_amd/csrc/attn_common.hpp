@@ -1,0 +1,150 @@
+// attn_common.hpp -- the paged cache and the split of an attention pass over it.
+#pragma once
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace tsv {
+
+constexpr int kStBadSeqRows = 32;
+constexpr int kStBadCache = 64;
+
+// n / page_size by a product: exact for 0 <= n < 2^31 (mul = floor(2^(31 + s) /
+// d) + 1 with 2^(s - 1) < d <= 2^s exceeds 2^(31 + s) / d by at most 2^s / d of
+// a unit, which stays below one part in n)
+inline PageDiv page_div(int d) {
+    int s = 0;
+    while ((1 << s) < d) ++s;
+    return PageDiv{(uint32_t)(((1ull << (31 + s)) / (uint32_t)d) + 1), 31 + s};
+}
+__device__ __forceinline__ int page_of(int n, PageDiv d) { return (int)(((uint64_t)(uint32_t)n * d.mul) >> d.shift); }
+
+// ---------------------------------------------------------------- the split
+// The cache positions of all items are cut into parts of `keys` positions (a
+// multiple of 64); an item has at least one part (it holds the tree's own
+// keys, with the last of the positions). `keys` follows from the lengths on
+// the device: the sum of all lengths, times the work-groups that read a
+// position (key heads, blocks of query rows), over the work-groups wanted. So
+// a batch of short items is not split, one long item is, and in a mixed batch
+// the long ones are: the parts are of equal length whatever the table's room.
+// Every work-group computes the same cut from cache_len. The number of parts
+// is at most `want` over the readers plus one for each item.
+constexpr int kAttnWant = 1024;  // about four work-groups for each of the 256 compute units
+constexpr int kAttnMinKeys = 256;
+
+struct AttnPlan {
+    int readers;   // work-groups that read one part
+    int min_keys;  // smallest part
+    int parts;     // upper bound of parts over all items
+    bool split;    // whether an item may have more than one
+};
+
+inline AttnPlan attn_plan(int batch, long long room, int readers, int min_keys) {
+    AttnPlan p;
+    p.readers = readers;
+    p.min_keys = min_keys;
+    p.split = room > min_keys;
+    p.parts = batch + (p.split ? kAttnWant / readers : 0);
+    return p;
+}
+
+// Partial results of a part, for each of the T * H rows: the unnormalised
+// output, and the running maximum (base 2) and sum of the softmax; and the part's
+// status bits.
+struct AttnWorkspace {
+    float* o;     // [parts][T * H][D]
+    float* ml;    // [parts][T * H][2]
+    int* bits;    // [parts]
+};
+inline uint64_t attn_workspace_bytes(const AttnPlan& p, int T, int H, int D) {
+    if (!p.split) return 0;
+    return (uint64_t)p.parts * (((uint64_t)T * H * (D + 2) + 1) + 3) / 4 * 4 * sizeof(float);
+}
+inline AttnWorkspace attn_workspace(void* ws, const AttnPlan& p, int T, int H, int D) {
+    AttnWorkspace w;
+    w.o = (float*)ws;
+    w.ml = ws ? w.o + (size_t)p.parts * T * H * D : nullptr;
+    w.bits = ws ? (int*)(w.ml + (size_t)p.parts * T * H * 2) : nullptr;
+    return w;
+}
+
+__device__ __forceinline__ int usable_len(int len, int room) { return len < 0 || len > room ? 0 : len; }
+
+struct Part {
+    int ok;        // 0: no such part
+    int item;
+    int k, n;      // index among the item's n parts
+    int base;      // the item's first part
+    int len;       // usable cache length
+    int bad_len;   // cache_len is out of range (its len is 0 then)
+    int keys;      // positions per part
+};
+
+// The part `want` (or, with by_item, part 0 of item `want`), the same in all
+// NT threads. Acts as a barrier. s_red: NT / 64 + 2 ints,
+// 8-byte aligned; s_out: one Part.
+template <int NT>
+__device__ __forceinline__ Part find_part(const int32_t* __restrict__ cache_len, int batch, int room, const AttnPlan& plan,
+                                          int want, bool by_item, int* s_red, Part* s_out) {
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    if (tid == 0) {
+        s_out->ok = 0;
+        s_red[0] = s_red[1] = 0;
+    }
+    __syncthreads();
+    int keys = 0x40000000;
+    if (plan.split) {
+        unsigned long long sum = 0;
+        for (int b = tid; b < batch; b += NT) sum += usable_len(cache_len[b], room);
+#pragma unroll
+        for (int m = 1; m < kWave; m <<= 1) sum += __shfl_xor(sum, m, kWave);
+        if (lane == 0) atomicAdd((unsigned long long*)s_red, sum);
+        __syncthreads();
+        sum = *(volatile unsigned long long*)s_red;
+        const unsigned long long want_keys = (sum * plan.readers + kAttnWant - 1) / kAttnWant;
+        keys = (int)min((want_keys + 63) / 64 * 64, 0x40000000ull);
+        keys = max(keys, plan.min_keys);
+        __syncthreads();
+    }
+    int run = 0;
+    for (int b0 = 0; b0 < batch; b0 += NT) {
+        const int b = b0 + tid;
+        const int raw = b < batch ? cache_len[b] : 0;
+        const int len = usable_len(raw, room);
+        const int cnt = b < batch ? max(1, (len + keys - 1) / keys) : 0;
+        int total;
+        const int base = run + block_exclusive_scan<NT>(cnt, s_red, &total);
+        if (b < batch && (by_item ? b == want : want >= base && want < base + cnt)) {
+            s_out->item = b;
+            s_out->k = by_item ? 0 : want - base;
+            s_out->n = cnt;
+            s_out->base = base;
+            s_out->len = len;
+            s_out->bad_len = raw != len;
+            s_out->keys = keys;
+            s_out->ok = 1;
+        }
+        run += total;
+    }
+    __syncthreads();
+    return *s_out;
+}
+
+// 8 e4m3 bytes -> 8 floats
+__device__ __forceinline__ void e4m3x8(uint2 u, float* f) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int wd = (int)(i ? u.y : u.x);
+        const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(wd, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(wd, true);
+        f[4 * i] = lo.x;
+        f[4 * i + 1] = lo.y;
+        f[4 * i + 2] = hi.x;
+        f[4 * i + 3] = hi.y;
+    }
+}
+__device__ __forceinline__ float e4m3_ld(const uint8_t* p) { return __builtin_amdgcn_cvt_f32_fp8((int)*p, 0); }
+// the byte nearest to f (|f| <= 448), ties to even
+__device__ __forceinline__ uint32_t e4m3_byte(float f) { return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f, f, 0, false) & 0xffu; }
+
+}  // namespace tsv

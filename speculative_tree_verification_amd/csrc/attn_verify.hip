@@ -1,0 +1,332 @@
+// attn_verify.hip -- attention of a packed tree's nodes over the paged cache:
+// the plain fp32 kernel (any head_dim up to 256, any types), the join of the
+// parts, and the choice of the kernel. The bf16 MFMA kernels are in
+// attn_mfma.hip.
+//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(scale log2(e) q_i . k_j - m_i)
+// over the cache's positions and node i's ancestors, in one pass with a running
+// maximum m_i and sum; parts of the cache (attn_common.hpp) are joined by
+//   o = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k,  m = max_k m_k.
+//
+// Plain kernel: a work-group takes kRows rows (node, query head) of one key
+// head and one part; its waves take 64 keys each in turn. Scores: a lane per
+// key, the rows' q from LDS (the same for all lanes). Values: lanes over the
+// head_dim, weights from LDS. Bound by the vector ALU (4 D operations per row
+// and key, no matrix instructions).
+#include "attn_common.hpp"
+
+namespace tsv {
+
+// Status bits of the tree, and each of `rows` rows' ancestors as bit words
+// (row i is node first + i); s_par: T ints. Acts as a barrier.
+template <int NT>
+__device__ int tree_words(const int32_t* __restrict__ parent, int T, int first, int rows, int words, int* s_par, uint32_t* s_anc) {
+    int bits = 0;
+    for (int i = threadIdx.x; i < T; i += NT) {
+        const int p = parent[i];
+        s_par[i] = p;
+        bits |= i == 0 ? (p != -1 ? kStBadRoot : 0) : (p < 0 || p >= i ? kStBadParent : 0);
+    }
+    for (int i = threadIdx.x; i < rows * words; i += NT) s_anc[i] = 0;
+    const int any = __syncthreads_or(bits);
+    if (any) return (__syncthreads_or(bits & kStBadRoot) ? kStBadRoot : 0) | (__syncthreads_or(bits & kStBadParent) ? kStBadParent : 0);
+    for (int i = threadIdx.x; i < rows; i += NT)
+        for (int j = first + i; j >= 0; j = s_par[j]) s_anc[i * words + j / 32] |= 1u << (j % 32);
+    __syncthreads();
+    return 0;
+}
+
+namespace {
+
+constexpr int kRows = 8;
+
+template <typename TC>
+__device__ __forceinline__ float elem(const TC* p, size_t i) {
+    if constexpr (sizeof(TC) == 1)
+        return e4m3_ld((const uint8_t*)p + i);
+    else
+        return Elem<TC>::ld(p, i);
+}
+
+// One wave's 64 keys: scores, running maximum, weights, products with v.
+// `key`: this lane's row in kp / vp (elements), -1: none; ks, vs: its scales.
+template <typename TC, int DV>
+__device__ __forceinline__ void plain_tile(const AttnArgs& a, const TC* kp, const TC* vp, long long key, float ks, float vs,
+                                           const uint32_t* s_anc, int words, int tree_key, const int* s_node,
+                                           const float (*s_q)[256], float (*s_p)[kWave], long long* s_off, int n,
+                                           float* m, float* l, float (*o)[DV]) {
+    const int lane = threadIdx.x & (kWave - 1), D = a.D;
+    float s[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) s[r] = 0.f;
+    if (key >= 0) {
+        for (int d = 0; d < D; ++d) {
+            const float kv = elem<TC>(kp, (size_t)key * D + d);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) s[r] = fmaf(s_q[r][d], kv, s[r]);
+        }
+    }
+    s_off[lane] = key;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        bool seen = key >= 0;
+        if (s_anc && seen) seen = s_anc[s_node[r] * words + tree_key / 32] >> (tree_key % 32) & 1;
+        const float sc = seen ? s[r] * ks * a.scale_log2 : -INFINITY;
+        float top = sc;
+#pragma unroll
+        for (int x = 1; x < kWave; x <<= 1) top = fmaxf(top, __shfl_xor(top, x, kWave));
+        // fmaxf passes over a NaN, which the weights then carry
+        const float mn = fmaxf(m[r], top), base = mn == -INFINITY ? 0.f : mn;
+        const float p = seen ? exp2f(sc - base) : 0.f, al = exp2f(m[r] - base);
+        float sum = p;
+#pragma unroll
+        for (int x = 1; x < kWave; x <<= 1) sum += __shfl_xor(sum, x, kWave);
+        l[r] = l[r] * al + sum;
+        m[r] = mn;
+#pragma unroll
+        for (int i = 0; i < DV; ++i) o[r][i] *= al;
+        s_p[r][lane] = p * vs;
+    }
+    wave_sync();
+    for (int j = 0; j < n; ++j) {
+        const long long at = s_off[j];
+        if (at < 0) continue;
+#pragma unroll
+        for (int i = 0; i < DV; ++i) {
+            const int d = lane + i * kWave;
+            if (d >= D) continue;
+            const float v = elem<TC>(vp, (size_t)at * D + d);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                // a key that row r does not see has weight 0, also where its value is not finite
+                const float p = s_p[r][j];
+                o[r][i] = p == 0.f ? o[r][i] : fmaf(p, v, o[r][i]);
+            }
+        }
+    }
+    wave_sync();
+}
+
+template <typename TIO, typename TC, int DV>
+__global__ __launch_bounds__(256) void attn_plain_kernel(AttnArgs a, AttnPlan plan, AttnWorkspace ws, int row_blocks) {
+    __shared__ __attribute__((aligned(8))) int s_red[6];
+    __shared__ Part s_part;
+    __shared__ float s_q[kRows][256], s_p[4][kRows][kWave], s_o[kRows][256], s_ml[4][kRows][2];
+    __shared__ long long s_off[4][kWave];
+    __shared__ int s_par[1024], s_node[kRows];
+    __shared__ uint32_t s_anc[kRows * 32];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int reader = blockIdx.x % plan.readers, hk = reader / row_blocks, rb = reader % row_blocks;
+    const Part pt = find_part<256>(a.cache_len, a.batch, a.room, plan, blockIdx.x / plan.readers, false, s_red, &s_part);
+    if (!pt.ok) return;
+    const int b = pt.item, T = a.T, H = a.H, D = a.D, g = H / a.Hk, R = T * g, row0 = rb * kRows;
+    const bool last = pt.k == pt.n - 1;
+    int st = pt.bad_len ? kStBadCache : 0;
+    const int first = row0 / g, nodes = min(R - 1, row0 + kRows - 1) / g - first + 1, words = (T + 31) / 32;
+    if (last) st |= tree_words<256>(a.parent + (size_t)b * T, T, first, nodes, words, s_par, s_anc);
+    for (int i = tid; i < kRows * D; i += 256) {
+        const int r = row0 + i / D;
+        s_q[i / D][i % D] = r < R ? Elem<TIO>::ld((const TIO*)a.q, (((size_t)b * T + r / g) * H + hk * g + r % g) * D + i % D) : 0.f;
+    }
+    if (tid < kRows) s_node[tid] = min(R - 1, row0 + tid) / g - first;
+    __syncthreads();
+    float m[kRows], l[kRows], o[kRows][DV];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < DV; ++i) o[r][i] = 0.f;
+    }
+    const int k0 = pt.k * pt.keys, k1 = last ? pt.len : min(pt.len, k0 + pt.keys);
+    int bad = 0;
+    for (int t0 = k0 + w * kWave; t0 < k1; t0 += 4 * kWave) {
+        const int pos = t0 + lane;
+        long long key = -1;
+        float ks = 1.f, vs = 1.f;
+        if (pos < k1) {
+            const int page = page_of(pos, a.div), pg = a.page_table[(size_t)b * a.max_pages + page];
+            if (pg < 0 || pg >= a.n_pages) {
+                bad = 1;
+            } else {
+                key = ((long long)pg * a.Hk + hk) * a.page_size + (pos - page * a.page_size);
+                if (a.k_scale) {
+                    ks = a.k_scale[key];
+                    vs = a.v_scale[key];
+                }
+            }
+        }
+        plain_tile<TC, DV>(a, (const TC*)a.k_cache, (const TC*)a.v_cache, key, ks, vs, nullptr, 0, 0, s_node, s_q, s_p[w],
+                           s_off[w], min(kWave, k1 - t0), m, l, o);
+    }
+    if (last && !st) {
+        for (int t0 = w * kWave; t0 < T; t0 += 4 * kWave) {
+            const int j = t0 + lane;
+            plain_tile<TIO, DV>(a, (const TIO*)a.k, (const TIO*)a.v, j < T ? ((long long)b * T + j) * a.Hk + hk : -1, 1.f, 1.f,
+                                s_anc, words, min(j, T - 1), s_node, s_q, s_p[w], s_off[w], min(kWave, T - t0), m, l, o);
+        }
+    }
+    st |= __syncthreads_or(bad) ? kStBadCache : 0;
+    // the four waves' parts
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+        if (lane == 0) {
+            s_ml[w][r][0] = m[r];
+            s_ml[w][r][1] = l[r];
+        }
+    __syncthreads();
+    float mt[kRows], lt[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        mt[r] = fmaxf(fmaxf(s_ml[0][r][0], s_ml[1][r][0]), fmaxf(s_ml[2][r][0], s_ml[3][r][0]));
+        const float base = mt[r] == -INFINITY ? 0.f : mt[r];
+        lt[r] = 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) lt[r] += s_ml[x][r][1] * exp2f(s_ml[x][r][0] - base);
+        const float al = exp2f(m[r] - base);
+#pragma unroll
+        for (int i = 0; i < DV; ++i) o[r][i] *= al;
+    }
+    for (int x = 0; x < 4; ++x) {
+        if (w == x) {
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                for (int i = 0; i < DV; ++i) {
+                    const int d = lane + i * kWave;
+                    s_o[r][d] = x == 0 ? o[r][i] : s_o[r][d] + o[r][i];
+                }
+        }
+        __syncthreads();
+    }
+    const int part = blockIdx.x / plan.readers;
+    if (reader == 0 && tid == 0) {
+        if (pt.n > 1)
+            ws.bits[part] = st;
+        else if (a.status)
+            a.status[b] = st;
+    }
+    if (pt.n == 1 && st) return;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        if (row0 + r >= R) break;
+        const int node = (row0 + r) / g, head = hk * g + (row0 + r) % g;
+        const size_t row = (size_t)node * H + head;
+        if (pt.n > 1) {
+            if (tid < D) ws.o[((size_t)part * T * H + row) * D + tid] = s_o[r][tid];
+            if (tid < 2) ws.ml[((size_t)part * T * H + row) * 2 + tid] = tid ? lt[r] : mt[r];
+        } else if (tid < D) {
+            Elem<TIO>::st((TIO*)a.o, ((size_t)b * T * H + row) * D + tid, s_o[r][tid] / lt[r]);
+        }
+    }
+}
+
+// A wave joins one row's parts.
+template <typename TIO, int DV>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnPlan plan, AttnWorkspace ws, int blocks) {
+    __shared__ __attribute__((aligned(8))) int s_red[6];
+    __shared__ Part s_part;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave;
+    const Part pt = find_part<256>(a.cache_len, a.batch, a.room, plan, blockIdx.x / blocks, true, s_red, &s_part);
+    if (pt.n < 2) return;
+    const int rows = a.T * a.H;
+    int st = 0;
+    for (int k = 0; k < pt.n; ++k) st |= ws.bits[pt.base + k];
+    const int rb = blockIdx.x % blocks;
+    if (rb == 0 && tid == 0 && a.status) a.status[pt.item] = st;
+    const int row = rb * 4 + w;
+    if (st || row >= rows) return;
+    const float* ml = ws.ml + ((size_t)pt.base * rows + row) * 2;
+    const float* po = ws.o + ((size_t)pt.base * rows + row) * a.D;
+    float m = -INFINITY;
+    for (int k = lane; k < pt.n; k += kWave) m = fmaxf(m, ml[(size_t)k * rows * 2]);
+#pragma unroll
+    for (int x = 1; x < kWave; x <<= 1) m = fmaxf(m, __shfl_xor(m, x, kWave));
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[DV];
+#pragma unroll
+    for (int i = 0; i < DV; ++i) o[i] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < pt.n; ++k) {
+        const float al = exp2f(ml[(size_t)k * rows * 2] - base);
+        l += al * ml[(size_t)k * rows * 2 + 1];
+#pragma unroll
+        for (int i = 0; i < DV; ++i) {
+            const int d = lane + i * kWave;
+            if (d < a.D) o[i] = fmaf(al, po[(size_t)k * rows * a.D + d], o[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < DV; ++i) {
+        const int d = lane + i * kWave;
+        if (d < a.D) Elem<TIO>::st((TIO*)a.o, ((size_t)pt.item * rows + row) * a.D + d, o[i] / l);
+    }
+}
+
+template <typename TIO, typename TC>
+void launch_plain(const AttnArgs& a, const AttnPlan& p, const AttnWorkspace& ws, int row_blocks, hipStream_t stream) {
+    const dim3 grid((unsigned)((long long)p.parts * p.readers));
+    if (a.D <= 64)
+        hipLaunchKernelGGL((attn_plain_kernel<TIO, TC, 1>), grid, dim3(256), 0, stream, a, p, ws, row_blocks);
+    else if (a.D <= 128)
+        hipLaunchKernelGGL((attn_plain_kernel<TIO, TC, 2>), grid, dim3(256), 0, stream, a, p, ws, row_blocks);
+    else
+        hipLaunchKernelGGL((attn_plain_kernel<TIO, TC, 4>), grid, dim3(256), 0, stream, a, p, ws, row_blocks);
+}
+
+template <typename TIO>
+void launch_join(const AttnArgs& a, const AttnPlan& p, const AttnWorkspace& ws, hipStream_t stream) {
+    const int blocks = (a.T * a.H + 3) / 4;
+    const dim3 grid((unsigned)((long long)a.batch * blocks));
+    if (a.D <= 64)
+        hipLaunchKernelGGL((attn_join_kernel<TIO, 1>), grid, dim3(256), 0, stream, a, p, ws, blocks);
+    else if (a.D <= 128)
+        hipLaunchKernelGGL((attn_join_kernel<TIO, 2>), grid, dim3(256), 0, stream, a, p, ws, blocks);
+    else
+        hipLaunchKernelGGL((attn_join_kernel<TIO, 4>), grid, dim3(256), 0, stream, a, p, ws, blocks);
+}
+
+AttnPlan plan_of(int batch, int T, int H, int Hk, long long room, int* row_blocks) {
+    *row_blocks = (T * (H / Hk) + kRows - 1) / kRows;
+    return attn_plan(batch, room, Hk * *row_blocks, kAttnMinKeys);
+}
+
+}  // namespace
+
+uint64_t attn_verify_workspace_bytes(const tsv_attn_shape* s) {
+    int rb;
+    const AttnPlan p = plan_of(s->batch, s->n_nodes, s->n_heads, s->n_kv_heads, (long long)s->max_pages * s->page_size, &rb);
+    return attn_workspace_bytes(p, s->n_nodes, s->n_heads, s->head_dim);
+}
+
+long long attn_verify_blocks(const tsv_attn_shape* s) {
+    int rb;
+    const AttnPlan p = plan_of(s->batch, s->n_nodes, s->n_heads, s->n_kv_heads, (long long)s->max_pages * s->page_size, &rb);
+    const long long join = (long long)s->batch * (((long long)s->n_nodes * s->n_heads + 3) / 4);
+    const long long parts = (long long)p.parts * p.readers;
+    return parts > join ? parts : join;
+}
+
+hipError_t launch_attn_verify(const AttnArgs& a, const tsv_attn_shape* s, void* workspace, hipStream_t stream) {
+    int row_blocks;
+    const AttnPlan p = plan_of(a.batch, a.T, a.H, a.Hk, a.room, &row_blocks);
+    const AttnWorkspace ws = attn_workspace(workspace, p, a.T, a.H, a.D);
+    const bool bf16 = s->in_dtype == TSV_BF16, e4m3 = s->cache_dtype == TSV_E4M3;
+    if (bf16 && e4m3)
+        launch_plain<uint16_t, uint8_t>(a, p, ws, row_blocks, stream);
+    else if (bf16)
+        launch_plain<uint16_t, uint16_t>(a, p, ws, row_blocks, stream);
+    else if (e4m3)
+        launch_plain<float, uint8_t>(a, p, ws, row_blocks, stream);
+    else
+        launch_plain<float, float>(a, p, ws, row_blocks, stream);
+    if (p.split) {
+        if (bf16)
+            launch_join<uint16_t>(a, p, ws, stream);
+        else
+            launch_join<float>(a, p, ws, stream);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace tsv

@@ -1,0 +1,113 @@
+// seq_common.hpp -- how the prompt scan cuts packed sequences into segments.
+//
+// The recurrence is sequential along a sequence, and one sequence has only
+// n_heads independent states: 80 work-groups on 256 compute units. A sequence
+// of more than `seg` tokens is therefore cut into segments of `seg` tokens:
+//   local    every segment but a sequence's last one forms the state it would
+//            leave from a zero state, and the sum of its log decays;
+//   combine  one pass over the segments of each sequence turns those into the
+//            state before each segment (H_k = exp(sum_k) H_{k-1} + local_k);
+//   scan     every segment runs from its own state and writes y.
+// Segments are numbered through all sequences ("slots"); a work-group finds
+// the sequence of its slot from seq_start, so the cut follows the lengths that
+// are on the device and the launch needs only an upper bound of the slots.
+#pragma once
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace tsv {
+
+constexpr int kStBadSeq = 32;
+
+// Largest and smallest sensible cut: `seg` tokens so that all (segment, head)
+// pairs are about four work-groups for each of the 256 compute units, a
+// multiple of the 64-token chunk and at least four chunks (below that the
+// second pass over the inputs costs more than the parallelism gives). One
+// segment for each sequence where no sequence can be longer than that.
+struct SeqPlan {
+    int seg;        // tokens per segment
+    int slots;      // upper bound of segments over all sequences
+    bool split;     // whether a sequence may have more than one
+};
+
+inline SeqPlan seq_plan(int n_seqs, int n_tokens, int n_heads) {
+    constexpr long long kWant = 1024;
+    long long seg = ((long long)n_tokens * n_heads + kWant - 1) / kWant;
+    seg = (seg + 63) / 64 * 64;
+    if (seg < 256) seg = 256;
+    if (seg > 0x7fffffc0LL) seg = 0x7fffffc0LL;
+    SeqPlan p;
+    p.seg = (int)seg;
+    p.slots = n_tokens / p.seg + (n_seqs < n_tokens ? n_seqs : n_tokens);
+    p.split = n_tokens > p.seg;
+    return p;
+}
+
+// The states of all slots, then the log-decay sums.
+struct SeqWorkspace {
+    float* state;  // [slots][H][P * N]
+    float* sum;    // [slots][H]
+};
+inline uint64_t seq_workspace_bytes(const SeqPlan& p, int H, int P, int N) {
+    return p.split ? (uint64_t)p.slots * H * ((uint64_t)P * N + 4) * sizeof(float) : 0;
+}
+inline SeqWorkspace seq_workspace(void* ws, const SeqPlan& p, int H, int P, int N) {
+    SeqWorkspace w;
+    w.state = (float*)ws;
+    w.sum = w.state ? w.state + (size_t)p.slots * H * P * N : nullptr;
+    return w;
+}
+
+struct Segment {
+    int ok;           // 0: no such slot, or seq_start is invalid
+    int seq, k, n;    // sequence, index among its n segments
+    int base;         // slot of the sequence's segment 0
+    int t0, t1;       // rows
+};
+
+// Whether seq_start is 0 <= start[0] <= ... <= start[n] <= n_tokens (the answer
+// is the same in all threads), and, for `want` >= 0, the segment of that slot,
+// or, with by_seq, segment 0 of that sequence. `s_red` and `s_out`: LDS scratch
+// of NT/64 ints and of one Segment. Acts as a barrier.
+template <int NT>
+__device__ __forceinline__ Segment find_segment(const int32_t* __restrict__ seq_start, int n_seqs, int n_tokens,
+                                                int seg, int want, bool by_seq, int* s_red, Segment* s_out) {
+    if (threadIdx.x == 0) s_out->ok = 0;
+    __syncthreads();
+    int run = 0, bad = 0;
+    for (int q0 = 0; q0 < n_seqs; q0 += NT) {
+        const int q = q0 + threadIdx.x;
+        int a = 0, b = 0;
+        if (q < n_seqs) {
+            a = seq_start[q];
+            b = seq_start[q + 1];
+        }
+        if (a < 0 || b < a || b > n_tokens) {
+            bad = 1;
+            b = a;
+        }
+        const int len = b - a;
+        const int cnt = len / seg + (len % seg != 0);
+        int total;
+        const int base = run + block_exclusive_scan<NT>(cnt, s_red, &total);
+        const bool mine = q < n_seqs && (by_seq ? q == want : want >= base && want < base + cnt);
+        if (mine) {
+            const int k = by_seq ? 0 : want - base;
+            s_out->seq = q;
+            s_out->k = k;
+            s_out->n = cnt;
+            s_out->base = base;
+            s_out->t0 = a + k * seg;
+            s_out->t1 = min(b, s_out->t0 + seg);
+            s_out->ok = 1;
+        }
+        run += total;
+    }
+    bad = __syncthreads_or(bad);
+    Segment r = *s_out;
+    if (bad) r.ok = 0;
+    return r;
+}
+
+}  // namespace tsv

@@ -1,0 +1,188 @@
+"""Refusals and workspace sizes of the prompt scan, the step and the paged
+cache's entry points: all before anything is enqueued (no GPU needed)."""
+import ctypes
+import glob
+import os
+import re
+
+import pytest
+
+from speculative_tree_verification_amd import binding as B
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+L = B.lib
+FAKE = ctypes.c_void_p(0x1000)  # never dereferenced: every call here returns before a launch
+OK, NULL, SHAPE, DTYPE, UNSUPPORTED = 0, 1, 2, 3, 4
+
+
+def seq(**kw):
+    v = dict(n_seqs=2, n_tokens=40, n_heads=8, head_dim=64, d_state=128, n_groups=1, in_dtype=1, flags=0)
+    v.update(kw)
+    return B.SeqShape(*v.values())
+
+
+def attn(**kw):
+    v = dict(batch=2, n_nodes=15, n_heads=8, n_kv_heads=2, head_dim=64, n_pages=9, page_size=16, max_pages=4, in_dtype=1,
+             cache_dtype=1, flags=0, scale=0.125)
+    v.update(kw)
+    return B.AttnShape(*v.values())
+
+
+def prefill(s, ptrs=None, ws=FAKE, size=1 << 62):
+    p = [FAKE] * 9 if ptrs is None else ptrs
+    return L.tree_ssd_prefill(ctypes.byref(s) if s is not None else None, *p, None, ws, size, None)
+
+
+def verify(s, ptrs=None, ws=FAKE, size=1 << 62):
+    p = [FAKE] * 11 if ptrs is None else ptrs
+    return L.tree_attn_verify(ctypes.byref(s) if s is not None else None, *p, None, ws, size, None)
+
+
+def commit(s, lmax=4, ptrs=None):
+    p = [FAKE] * 5 if ptrs is None else ptrs[:5]
+    r = [FAKE] * 6 if ptrs is None else ptrs[5:]
+    return L.tree_attn_commit(ctypes.byref(s), *p, lmax, *r, None, None)
+
+
+def append(s, ptrs=None):
+    p = [FAKE] * 9 if ptrs is None else ptrs
+    return L.tree_attn_append(ctypes.byref(s), *p, None, None)
+
+
+def test_declared_and_exported():
+    text = open(os.path.join(ROOT, "include", "tree_ssd.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = set(re.findall(r"\b(tree_(?:ssd|gdn|attn)_\w+)\s*\(", text))
+    assert names == set(B.EXPORTS)
+    for n in names:
+        assert hasattr(L, n), n
+
+
+@pytest.mark.parametrize("field,value,code", [
+    ("n_seqs", -1, SHAPE), ("n_tokens", -1, SHAPE), ("n_heads", 0, SHAPE), ("head_dim", 0, SHAPE), ("d_state", 0, SHAPE),
+    ("n_groups", 3, SHAPE), ("n_groups", 0, SHAPE), ("in_dtype", 2, DTYPE), ("head_dim", 257, UNSUPPORTED),
+    ("d_state", 257, UNSUPPORTED), ("n_heads", 70000, UNSUPPORTED)])
+def test_prefill_refuses_shapes(field, value, code):
+    assert prefill(seq(**{field: value})) == code
+    n = ctypes.c_uint64(7)
+    assert L.tree_ssd_prefill_workspace(ctypes.byref(seq(**{field: value})), ctypes.byref(n)) == code
+    assert n.value == 7
+
+
+def test_prefill_refuses_grids_past_31_bits():
+    assert prefill(seq(n_seqs=2 ** 31 - 1, n_tokens=2 ** 31 - 1, n_heads=4096, n_groups=1)) == UNSUPPORTED
+
+
+def test_prefill_null_and_workspace():
+    assert prefill(None) == NULL
+    for i in range(9):
+        p = [FAKE] * 9
+        p[i] = None
+        assert prefill(seq(), p) == NULL, i
+    assert prefill(seq(n_seqs=0), [None] * 9, None, 0) == OK
+    long = seq(n_tokens=100000)
+    need = B.prefill_workspace_bytes(2, 100000, 8, 64, 128)
+    assert need > 0
+    assert prefill(long, ws=None) == NULL
+    assert prefill(long, size=need - 1) == NULL
+    assert prefill(long, ws=ctypes.c_void_p(0x1008)) == SHAPE
+    assert L.tree_ssd_prefill_workspace(ctypes.byref(long), None) == NULL
+    # a prompt of at most one segment needs none
+    assert B.prefill_workspace_bytes(1, 256, 80, 64, 128) == 0
+
+
+@pytest.mark.parametrize("field,value,code", [
+    ("batch", -1, SHAPE), ("n_nodes", 2, SHAPE), ("n_nodes", -1, SHAPE), ("n_heads", 0, SHAPE), ("n_groups", 3, SHAPE),
+    ("in_dtype", 2, DTYPE), ("head_dim", 257, UNSUPPORTED), ("d_state", 300, UNSUPPORTED)])
+def test_step_refuses(field, value, code):
+    v = dict(batch=2, n_nodes=1, n_heads=8, head_dim=64, d_state=128, n_groups=1, in_dtype=1, flags=0, heads_per_block=0)
+    v[field] = value
+    assert L.tree_ssd_step(ctypes.byref(B.Shape(*v.values())), *[FAKE] * 8, None) == code
+
+
+def test_step_null_and_empty():
+    s = B.Shape(2, 1, 8, 64, 128, 1, 1, 0, 0)
+    assert L.tree_ssd_step(None, *[FAKE] * 8, None) == NULL
+    for i in range(8):
+        p = [FAKE] * 8
+        p[i] = None
+        assert L.tree_ssd_step(ctypes.byref(s), *p, None) == NULL, i
+    s.batch = 0
+    assert L.tree_ssd_step(ctypes.byref(s), *[None] * 8, None) == OK
+
+
+BAD_ATTN = [("batch", -1, SHAPE), ("n_nodes", -1, SHAPE), ("n_heads", 0, SHAPE), ("n_kv_heads", 3, SHAPE),
+            ("n_kv_heads", 0, SHAPE), ("head_dim", 0, SHAPE), ("n_pages", -1, SHAPE), ("max_pages", -1, SHAPE),
+            ("page_size", 0, SHAPE), ("page_size", 65537, SHAPE), ("max_pages", 2 ** 27, SHAPE),
+            ("scale", float("nan"), SHAPE), ("scale", float("inf"), SHAPE), ("in_dtype", 2, DTYPE), ("cache_dtype", 3, DTYPE),
+            ("cache_dtype", 0, UNSUPPORTED), ("head_dim", 257, UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("field,value,code", BAD_ATTN + [("n_nodes", 1025, SHAPE)])
+def test_attn_verify_and_commit_refuse_shapes(field, value, code):
+    assert verify(attn(**{field: value})) == code
+    assert commit(attn(**{field: value})) == code
+
+
+@pytest.mark.parametrize("field,value,code", BAD_ATTN)
+def test_attn_append_refuses_shapes(field, value, code):
+    assert append(attn(**{field: value})) == code
+
+
+def test_attn_null_and_workspace():
+    assert verify(None) == NULL
+    for i in range(11):
+        p = [FAKE] * 11
+        p[i] = None
+        scales = i in (6, 7)
+        assert verify(attn(cache_dtype=2), p, None, 0) == NULL, i
+        if not scales:
+            assert verify(attn(), p, None, 0) == NULL, i
+    long = attn(max_pages=4096)
+    need = B.attn_verify_workspace_bytes(2, 15, 8, 2, 64, 16, 4096)
+    assert need > 0
+    assert verify(long, ws=None) == NULL
+    assert verify(long, size=need - 1) == NULL
+    assert verify(long, ws=ctypes.c_void_p(0x1004)) == SHAPE
+    assert B.attn_verify_workspace_bytes(2, 15, 8, 2, 64, 16, 4) == 0  # 64 positions are not split
+    assert B.attn_verify_workspace_bytes(0, 15, 8, 2, 64, 16, 4096) == 0
+    for f, n in ((commit, 11), (append, 9)):
+        for i in range(n):
+            p = [FAKE] * n
+            p[i] = None
+            assert (f(attn(cache_dtype=2), ptrs=p)) == NULL, (f.__name__, i)
+
+
+def test_attn_commit_path_lengths():
+    assert commit(attn(), lmax=-1) == SHAPE
+    assert commit(attn(), lmax=1025) == SHAPE
+
+
+def test_attn_empty_calls_are_noops():
+    assert verify(attn(batch=0), [None] * 11, None, 0) == OK
+    assert verify(attn(n_nodes=0), [None] * 11, None, 0) == OK
+    assert commit(attn(batch=0), ptrs=[None] * 11) == OK
+    assert append(attn(batch=0), ptrs=[None] * 9) == OK
+
+
+def test_binding_refuses_before_the_library():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(4, 2, 8)
+    with pytest.raises(ValueError):  # a tensor that is not on a GPU
+        B.step(x, torch.zeros(4, 2), torch.zeros(2), torch.zeros(4, 1, 16), torch.zeros(4, 1, 16), torch.zeros(2),
+               torch.zeros(4, 2, 8, 16))
+    with pytest.raises(ValueError):  # a state of another shape
+        B.step(x, torch.zeros(4, 2), torch.zeros(2), torch.zeros(4, 1, 16), torch.zeros(4, 1, 16), torch.zeros(2),
+               torch.zeros(4, 2, 8, 15))
+    k, table, n = torch.zeros(3, 2, 8), torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    start = torch.tensor([0, 3], dtype=torch.int32)
+    c8 = torch.zeros(2, 2, 16, 8, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    with pytest.raises(ValueError, match="k_scale"):
+        B.attn_append(k, k, start, c8, c8, table, n)
+    with pytest.raises(TypeError, match="float8"):
+        B.attn_append(k, k, start, c8.view(torch.uint8), c8.view(torch.uint8), table, n)
+    c = torch.zeros(2, 2, 16, 8)
+    with pytest.raises(ValueError, match="contiguous"):
+        B.attn_append(k, k, start, c.transpose(0, 1), c, table, n)
+    with pytest.raises(ValueError, match="e4m3"):
+        B.attn_append(k, k, start, c, c, table, n, k_scale=torch.zeros(2, 2, 16))
