@@ -197,17 +197,17 @@ hipError_t launch_prefill(const PrefillArgs& a, bool bf16, bool mfma, int32_t* s
     if (a.n_tokens > 0) {
         const SeqPlan p = seq_plan(a.n_seqs, a.n_tokens, a.H);
         const SeqWorkspace ws = seq_workspace(workspace, p, a.H, a.P, a.N);
-        if (p.split) {
-            if (bf16)
-                launch_plain<uint16_t, true>(a, p, ws, stream);
+        const bool matrix = bf16 && mfma && prefill_mfma_supported(a);
+        for (int pass = p.split ? 0 : 1; pass < 2; ++pass) {
+            const bool local = pass == 0;
+            if (matrix)
+                launch_prefill_mfma(a, p, ws, local, stream);
+            else if (bf16)
+                local ? launch_plain<uint16_t, true>(a, p, ws, stream) : launch_plain<uint16_t, false>(a, p, ws, stream);
             else
-                launch_plain<float, true>(a, p, ws, stream);
-            launch_combine(a, p, ws, stream);
+                local ? launch_plain<float, true>(a, p, ws, stream) : launch_plain<float, false>(a, p, ws, stream);
+            if (local) launch_combine(a, p, ws, stream);
         }
-        if (bf16)
-            launch_plain<uint16_t, false>(a, p, ws, stream);
-        else
-            launch_plain<float, false>(a, p, ws, stream);
     }
     return hipGetLastError();
 }

@@ -59,6 +59,10 @@ inline SeqWorkspace seq_workspace(void* ws, const SeqPlan& p, int H, int P, int 
     return w;
 }
 
+// bf16 MFMA kernel (prefill_mfma.hip): P 64, N 64 or 128, 16-byte aligned tensors
+bool prefill_mfma_supported(const PrefillArgs& a);
+void launch_prefill_mfma(const PrefillArgs& a, const SeqPlan& p, const SeqWorkspace& ws, bool local, hipStream_t stream);
+
 struct Segment {
     int ok;           // 0: no such slot, or seq_start is invalid
     int seq, k, n;    // sequence, index among its n segments
