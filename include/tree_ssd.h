@@ -514,8 +514,8 @@ typedef struct {
  * Arithmetic: bf16 inputs with P == 64 and N in {64, 128} take an MFMA kernel
  * over chunks of 64 tokens: scores and decays in fp32, their masked product
  * rounded once to bf16 as the operand of the product with x; the state held in
- * fp32, read out as a bf16 high and low part (16 bits), and updated with
- * weighted inputs split into three bf16 parts (24 bits). Per-token log decays
+ * fp32, read out as a bf16 high and low part (off by at most 2^-18 of an
+ * element), and updated with weighted inputs in three such parts (24 bits). Per-token log decays
  * below -128 count as -128 (exp of both is 0 in fp32). Other inputs run the
  * recurrence token by token in fp32.
  * TSV_E_SHAPE for negative sizes, TSV_E_NULL also for a missing workspace.

@@ -19,11 +19,14 @@ template <typename TIO, int NS, bool LOCAL>
 __global__ __launch_bounds__(256) void prefill_plain_kernel(PrefillArgs a, SeqPlan plan, SeqWorkspace ws, int pblocks) {
     __shared__ int s_red[4];
     __shared__ Segment s_seg;
+    __shared__ int s_len[kSortMax];
     __shared__ __attribute__((aligned(16))) float s_B[kTok][4 * NS], s_C[kTok][4 * NS];
     __shared__ float s_x[kTok][kWave], s_y[4][kTok][kWave], s_dec[kTok], s_dt[kTok];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int pb = blockIdx.x % pblocks, h = blockIdx.x / pblocks % a.H, slot = blockIdx.x / pblocks / a.H;
-    const Segment sg = find_segment<256>(a.seq_start, a.n_seqs, a.n_tokens, plan.seg, slot, false, s_red, &s_seg);
+    int slot, hb;
+    place_block(plan, a.H * pblocks, &slot, &hb);
+    const int pb = hb % pblocks, h = hb / pblocks;
+    const Segment sg = find_segment<256, LOCAL>(a.seq_start, a.n_seqs, a.n_tokens, plan, slot, false, s_red, &s_seg, s_len);
     if (!sg.ok) return;
     if (LOCAL && sg.k == sg.n - 1) return;
     const int p = pb * kWave + lane, P = a.P, N = a.N;
@@ -120,8 +123,10 @@ template <int V>
 __global__ __launch_bounds__(256) void prefill_combine_kernel(PrefillArgs a, SeqPlan plan, SeqWorkspace ws, int chunks) {
     __shared__ int s_red[4];
     __shared__ Segment s_seg;
+    __shared__ int s_len[kSortMax];
     const int c = blockIdx.x % chunks, h = blockIdx.x / chunks % a.H, q = blockIdx.x / chunks / a.H;
-    const Segment sg = find_segment<256>(a.seq_start, a.n_seqs, a.n_tokens, plan.seg, q, true, s_red, &s_seg);
+    if (a.seq_start[q + 1] - a.seq_start[q] <= plan.seg) return;
+    const Segment sg = find_segment<256, true>(a.seq_start, a.n_seqs, a.n_tokens, plan, q, true, s_red, &s_seg, s_len);
     if (!sg.ok || sg.n < 2) return;
     const size_t PN = (size_t)a.P * a.N;
     const size_t e = ((size_t)c * 256 + threadIdx.x) * V;
