@@ -573,7 +573,7 @@ typedef struct {
     int32_t head_dim;    /* D in [1, 256] */
     int32_t n_pages;     /* pages of the pool >= 0 */
     int32_t page_size;   /* positions per page, in [1, 65536] */
-    int32_t max_pages;   /* row length of page_table >= 0; max_pages * page_size < 2^31 */
+    int32_t max_pages;   /* row length of page_table >= 0; max_pages * page_size <= 2^31 - 2^16 */
     int32_t in_dtype;    /* tsv_dtype of q, k, v, o */
     int32_t cache_dtype; /* in_dtype or TSV_E4M3 (TSV_E_UNSUPPORTED for other pairs) */
     int32_t flags;       /* TSV_FLAG_FORCE_GENERIC or 0 */

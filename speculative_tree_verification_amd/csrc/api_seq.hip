@@ -36,7 +36,7 @@ tsv_status check_attn(const tsv_attn_shape* s, bool tree) {
     if (s->n_heads < 1 || s->n_kv_heads < 1 || s->n_heads % s->n_kv_heads != 0) return TSV_E_SHAPE;
     if (s->head_dim < 1 || s->n_pages < 0 || s->max_pages < 0) return TSV_E_SHAPE;
     if (s->page_size < 1 || s->page_size > 65536) return TSV_E_SHAPE;
-    if ((long long)s->max_pages * s->page_size > 0x7fffffffLL) return TSV_E_SHAPE;
+    if ((long long)s->max_pages * s->page_size > 0x7fff0000LL) return TSV_E_SHAPE;
     if (!isfinite(s->scale)) return TSV_E_SHAPE;
     if (s->cache_dtype != s->in_dtype && s->cache_dtype != TSV_E4M3) return TSV_E_UNSUPPORTED;
     if (s->head_dim > kMaxDim || s->n_heads > 0xffff) return TSV_E_UNSUPPORTED;

@@ -1,6 +1,8 @@
 // attn_common.hpp -- the paged cache and the split of an attention pass over it.
 #pragma once
 
+#include <type_traits>
+
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -130,19 +132,30 @@ __device__ __forceinline__ Part find_part(const int32_t* __restrict__ cache_len,
     return *s_out;
 }
 
-// 8 e4m3 bytes -> 8 floats
-__device__ __forceinline__ void e4m3x8(uint2 u, float* f) {
-    typedef float f2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int wd = (int)(i ? u.y : u.x);
-        const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(wd, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(wd, true);
-        f[4 * i] = lo.x;
-        f[4 * i + 1] = lo.y;
-        f[4 * i + 2] = hi.x;
-        f[4 * i + 3] = hi.y;
+// bf16 MFMA kernels (attn_mfma.hip): block_rows 16, 64 or 128 rows of a key head
+// per work-group
+void launch_attn_mfma(const AttnArgs& a, bool e4m3, const AttnPlan& p, const AttnWorkspace& ws, int block_rows, int row_blocks,
+                      hipStream_t stream);
+
+// Status bits of the tree, and each of `rows` rows' ancestors as bit words
+// (row i is node first + i); s_par: T ints. Acts as a barrier.
+template <int NT>
+__device__ __forceinline__ int tree_words(const int32_t* __restrict__ parent, int T, int first, int rows, int words, int* s_par, uint32_t* s_anc) {
+    int bits = 0;
+    for (int i = threadIdx.x; i < T; i += NT) {
+        const int p = parent[i];
+        s_par[i] = p;
+        bits |= i == 0 ? (p != -1 ? kStBadRoot : 0) : (p < 0 || p >= i ? kStBadParent : 0);
     }
+    for (int i = threadIdx.x; i < rows * words; i += NT) s_anc[i] = 0;
+    const int any = __syncthreads_or(bits);
+    if (any) return (__syncthreads_or(bits & kStBadRoot) ? kStBadRoot : 0) | (__syncthreads_or(bits & kStBadParent) ? kStBadParent : 0);
+    for (int i = threadIdx.x; i < rows; i += NT)
+        for (int j = first + i; j >= 0; j = s_par[j]) s_anc[i * words + j / 32] |= 1u << (j % 32);
+    __syncthreads();
+    return 0;
 }
+
 __device__ __forceinline__ float e4m3_ld(const uint8_t* p) { return __builtin_amdgcn_cvt_f32_fp8((int)*p, 0); }
 // the byte nearest to f (|f| <= 448), ties to even
 __device__ __forceinline__ uint32_t e4m3_byte(float f) { return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f, f, 0, false) & 0xffu; }

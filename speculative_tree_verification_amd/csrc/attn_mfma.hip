@@ -1,0 +1,662 @@
+// attn_mfma.hip -- tree attention over the paged cache on bf16 matrix
+// instructions (head_dim 64 or 128, cache in bf16 or e4m3).
+//
+// Both kernels form the scores transposed, S^T = K Q^T (16 keys x 16 rows a
+// tile): a lane then holds the keys 4 (l / 16) + r of one row l % 16, so that the
+// softmax statistics of a row are a reduction in registers and over four lanes,
+// the factor of a rescaling is one value per lane, and two tiles of weights are
+// the operand of the next product, O^T = V^T P^T, as they are. V^T comes from LDS
+// through the transposing read, in the same order of keys.
+//   rows   up to 16 rows (node, query head) share a key head: one new token, or a
+//          small tree. Four waves take 32 keys each in turn and meet at the end;
+//          K goes from memory into the operand registers directly. Bound by the
+//          cache's bytes.
+//   tiles  more rows: a wave has 16 or 32 rows of its own, and 64 keys at a time
+//          are shared in LDS. Bound by matrix and vector work.
+// In both, the loads of the next keys are under way while these are worked on,
+// and the page of a key is looked up one step before its row is loaded.
+#include "attn_common.hpp"
+#include "mfma_util.hpp"
+
+namespace tsv {
+namespace {
+
+constexpr int kStepKeys = 32;  // keys of a wave's step in the row kernel
+constexpr int kTileKeys = 64;  // keys of a shared tile in the tile kernel
+
+// Largest of / sum over the four lanes that hold a row's keys
+__device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16, kWave));
+    return fmaxf(v, __shfl_xor(v, 32, kWave));
+}
+__device__ __forceinline__ float row_sum(float v) {
+    v += __shfl_xor(v, 16, kWave);
+    return v + __shfl_xor(v, 32, kWave);
+}
+
+// Row index of position `pos` of an item in the cache's arrays, or -1 for a page
+// out of range. `page` is what the table holds for it.
+__device__ __forceinline__ bool page_ok(const AttnArgs& a, int page) { return (uint32_t)page < (uint32_t)a.n_pages; }
+__device__ __forceinline__ uint32_t cache_row(const AttnArgs& a, int page, int hk, int pos) {
+    const int off = pos - page_of(pos, a.div) * a.page_size;
+    return ((uint32_t)page * a.Hk + hk) * a.page_size + off;
+}
+
+__device__ __forceinline__ bf16x8 as_operand(uint4 u) { return __builtin_bit_cast(bf16x8, u); }
+
+// What the values that are not finite among 32 keys' V add to a row that sees
+// them: v is V^T of these keys, seen the row's 0/1 weights of them. Such a V is
+// taken out of the ordinary product, where a weight of 0 would spread it.
+__device__ __forceinline__ bf16x8 only_finite(bf16x8 v) {
+    s16x8 s = __builtin_bit_cast(s16x8, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = (s[e] & 0x7f80) == 0x7f80 ? (short)0 : s[e];
+    return __builtin_bit_cast(bf16x8, s);
+}
+__device__ __forceinline__ f32x4 nonfinite_part(bf16x8 v, bf16x8 seen) {
+    s16x8 up = __builtin_bit_cast(s16x8, v), down = up;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {  // 1 for +inf and NaN, and for -inf and NaN
+        const int b = (uint16_t)up[e];
+        const bool odd = (b & 0x7f80) == 0x7f80, nan = odd && (b & 0x7f);
+        up[e] = odd && (nan || !(b & 0x8000)) ? 0x3f80 : 0;
+        down[e] = odd && (nan || (b & 0x8000)) ? 0x3f80 : 0;
+    }
+    const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+    const f32x4 p = mma(__builtin_bit_cast(bf16x8, up), seen, z), n = mma(__builtin_bit_cast(bf16x8, down), seen, z);
+    f32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = (p[i] > 0.f ? INFINITY : 0.f) + (n[i] > 0.f ? -INFINITY : 0.f);
+    return r;
+}
+
+// ---------------------------------------------------------------- rows
+// ND = D / 32; E4M3: the cache's type
+template <int ND, bool E4M3>
+__global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan plan, AttnWorkspace ws) {
+    constexpr int D = ND * 32, kVs = D + 16, kOs = D + 4;
+    __shared__ __attribute__((aligned(8))) int s_red[6];
+    __shared__ Part s_part;
+    __shared__ __attribute__((aligned(16))) uint16_t s_V[4][kStepKeys * kVs];  // then the waves' outputs
+    __shared__ __attribute__((aligned(16))) float s_ks[4][kStepKeys], s_vs[4][kStepKeys], s_ml[4][16][2];
+    __shared__ uint32_t s_row[4][2][kStepKeys];
+    __shared__ uint32_t s_anc[16];
+    __shared__ int s_par[16];
+    static_assert(sizeof(s_V) >= 4 * 16 * kOs * sizeof(float), "outputs take the place of V");
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int l16 = lane & 15, lg = lane >> 4;
+    const int lid = xcd_block(blockIdx.x, gridDim.x), hk = lid % a.Hk, part = lid / a.Hk;
+    const Part pt = find_part<256>(a.cache_len, a.batch, a.room, plan, part, false, s_red, &s_part);
+    if (!pt.ok) return;
+    const int b = pt.item, T = a.T, H = a.H, g = H / a.Hk, R = T * g;
+    const bool last = pt.k == pt.n - 1;
+    int st = pt.bad_len ? kStBadCache : 0;
+
+    // this lane's row: query operand, k-slot e of step 2 j + h is d = 64 j + 16 lg + 8 h + e
+    const int row = min(l16, R - 1), node = row / g, head = hk * g + row % g;
+    bf16x8 q[ND];
+    {
+        const uint16_t* qp = (const uint16_t*)a.q + (((size_t)b * T + node) * H + head) * D + 16 * lg;
+#pragma unroll
+        for (int i = 0; i < ND; ++i) q[i] = as_operand(gload((const uint4*)(qp + 64 * (i / 2) + 8 * (i % 2))));
+    }
+    if (last) {  // at most 16 nodes: one word of ancestors each
+        int bits = 0;
+        if (tid < T) {
+            const int p = a.parent[(size_t)b * T + tid];
+            s_par[tid] = p;
+            bits = tid == 0 ? (p != -1 ? kStBadRoot : 0) : (p < 0 || p >= tid ? kStBadParent : 0);
+        }
+        if (__syncthreads_or(bits)) {
+            st |= __syncthreads_or(bits & kStBadRoot) ? kStBadRoot : 0;
+            st |= __syncthreads_or(bits & kStBadParent) ? kStBadParent : 0;
+        } else {
+            if (tid < T) {
+                uint32_t m = 0;
+                for (int j = tid; j >= 0; j = s_par[j]) m |= 1u << j;
+                s_anc[tid] = m;
+            }
+            __syncthreads();
+        }
+    }
+
+    float m = -INFINITY, l = 0.f;
+    f32x4 o[D / 16];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // softmax and product of 32 keys: s the scores times scale log2(e) (masked:
+    // -inf), vs the factor of each value row; V in this wave's LDS
+    auto take = [&](const f32x4* s, const f32x4* vs, bool odd) {
+        float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                          fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+        top = row_max(top);
+        const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
+        if (__ballot(mn > m)) {  // some row's maximum moved
+            const float al = __builtin_amdgcn_exp2f(m - base);
+            l *= al;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) o[i] *= al;
+        }
+        m = mn;
+        float p[8], sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            p[e] = __builtin_amdgcn_exp2f(s[e / 4][e % 4] - base);
+            sum += p[e];
+        }
+        l += sum;  // of this lane's keys; the four lanes of a row meet at the end
+        if (E4M3 && vs) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = p[e] == 0.f ? 0.f : p[e] * vs[e / 4][e % 4];
+        }
+        const bf16x8 pf = as_operand(make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]),
+                                                pack_bf16x2(p[6], p[7])));
+        if (!odd) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) o[i] = mma(read_columns(&s_V[w][16 * i], kVs, lane), pf, o[i]);
+        } else {
+            s16x8 seen;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) seen[e] = s[e / 4][e % 4] != -INFINITY ? 0x3f80 : 0;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const bf16x8 v = read_columns(&s_V[w][16 * i], kVs, lane);
+                o[i] = mma(only_finite(v), pf, o[i]) + nonfinite_part(v, __builtin_bit_cast(bf16x8, seen));
+            }
+        }
+    };
+
+    // the tree's own keys, in the wave that has the fewest cache steps
+    if (last && !st && w == 3) {
+        const uint16_t* kp = (const uint16_t*)a.k + ((size_t)b * T * a.Hk + hk) * D;
+        const uint16_t* vp = (const uint16_t*)a.v + ((size_t)b * T * a.Hk + hk) * D;
+        const size_t stride = (size_t)a.Hk * D;
+        f32x4 s[2];
+        s[0] = s[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const uint16_t* krow = kp + (size_t)min(l16, T - 1) * stride + 16 * lg;
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+            s[0] = mma(as_operand(gload((const uint4*)(krow + 64 * (i / 2) + 8 * (i % 2)))), q[i], s[0]);
+        const uint32_t anc = s_anc[node];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int j = 4 * lg + r;
+            s[0][r] = j < T && (anc >> j & 1) ? s[0][r] * a.scale_log2 : -INFINITY;
+            s[1][r] = -INFINITY;
+        }
+        uint32_t strange = 0;
+        for (int i = lane; i < kStepKeys * (D / 8); i += kWave) {
+            const int key = i / (D / 8), c = i % (D / 8) * 8;
+            const uint4 u = key < T ? gload((const uint4*)(vp + (size_t)key * stride + c)) : make_uint4(0, 0, 0, 0);
+            strange |= nonfinite_bits(u);
+            *(uint4*)&s_V[w][key * kVs + c] = u;
+        }
+        wave_sync();
+        take(s, nullptr, __ballot((strange & 0x80008000u) != 0) != 0);
+        wave_sync();
+    }
+
+    // the cache: wave w has steps w, w + 4, ...
+    const int k0 = pt.k * pt.keys, k1 = last ? pt.len : min(pt.len, k0 + pt.keys);
+    int bad = 0;
+    if (k1 > k0 && a.n_pages > 0) {
+        constexpr int EB = E4M3 ? 1 : 2;          // bytes of an element
+        constexpr int KL = E4M3 ? ND / 2 : ND;    // 16-byte loads of a key's lane
+        constexpr int VL = kStepKeys * D * EB / 16 / kWave;  // of V per lane
+        constexpr int VR = kWave / (D * EB / 16);            // rows of V a load covers
+        const char* kc = (const char*)a.k_cache;
+        const char* vc = (const char*)a.v_cache;
+        const int32_t* table = a.page_table + (size_t)b * a.max_pages;
+        uint4 rk[2][KL], rv[VL];
+        float rks = 1.f, rvs = 1.f;
+        int page = 0;  // of this lane's key (lane % 32) of the step after the one being requested
+        auto key_of = [&](int t) { return min(t + (lane & 31), k1 - 1); };
+        auto look_up = [&](int t) { page = table[page_of(key_of(t), a.div)]; };
+        auto request_rows = [&](int t, int set) {  // row of each key, to all lanes
+            const bool fine = page_ok(a, page);
+            bad |= !fine;
+            const uint32_t r = cache_row(a, fine ? page : 0, hk, key_of(t));
+            if (lane < kStepKeys) s_row[w][set][lane] = r;
+            if (E4M3) {
+                rks = gload(a.k_scale + r);
+                rvs = gload(a.v_scale + r);
+            }
+            wave_sync();
+        };
+        auto request_K = [&](int set) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const char* p = kc + (size_t)s_row[w][set][16 * t + l16] * (D * EB) + lg * (E4M3 ? 16 : 32);
+#pragma unroll
+                for (int i = 0; i < KL; ++i)
+                    rk[t][i] = gload((const uint4*)(p + (E4M3 ? 64 * i : 128 * (i / 2) + 16 * (i % 2))));
+            }
+        };
+        auto request_V = [&](int set) {
+#pragma unroll
+            for (int i = 0; i < VL; ++i) {
+                const int key = i * VR + lane / (D * EB / 16), c = lane % (D * EB / 16) * 16;
+                rv[i] = gload((const uint4*)(vc + (size_t)s_row[w][set][key] * (D * EB) + c));
+            }
+        };
+        int t = k0 + w * kStepKeys, set = 0;
+        if (t < k1) {
+            look_up(t);
+            request_rows(t, 0);
+            request_K(0);
+            request_V(0);
+            look_up(t + 4 * kStepKeys);
+        }
+        for (; t < k1; t += 4 * kStepKeys, set ^= 1) {
+            const bool more = t + 4 * kStepKeys < k1;
+            if (E4M3) {
+                if (lane < kStepKeys) {
+                    s_ks[w][lane] = rks * a.scale_log2;
+                    s_vs[w][lane] = rvs;
+                }
+                wave_sync();
+            }
+            f32x4 s[2], vs[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                s[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (E4M3) {
+#pragma unroll
+                    for (int i = 0; i < KL; ++i) {
+                        s[x] = mma(as_operand(e4m3_to_bf16(make_uint2(rk[x][i].x, rk[x][i].y))), q[2 * i], s[x]);
+                        s[x] = mma(as_operand(e4m3_to_bf16(make_uint2(rk[x][i].z, rk[x][i].w))), q[2 * i + 1], s[x]);
+                    }
+                    s[x] *= *(const f32x4*)&s_ks[w][16 * x + 4 * lg];
+                    vs[x] = *(const f32x4*)&s_vs[w][16 * x + 4 * lg];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < KL; ++i) s[x] = mma(as_operand(rk[x][i]), q[i], s[x]);
+                    s[x] *= a.scale_log2;
+                }
+            }
+            if (more) {
+                request_rows(t + 4 * kStepKeys, set ^ 1);
+                request_K(set ^ 1);
+            }
+            // V into LDS, its registers free for the next step
+#pragma unroll
+            for (int i = 0; i < VL; ++i) {
+                const int key = i * VR + lane / (D * EB / 16), c = lane % (D * EB / 16) * (16 / EB);
+                if (E4M3) {
+                    *(uint4*)&s_V[w][key * kVs + c] = e4m3_to_bf16(make_uint2(rv[i].x, rv[i].y));
+                    *(uint4*)&s_V[w][key * kVs + c + 8] = e4m3_to_bf16(make_uint2(rv[i].z, rv[i].w));
+                } else {
+                    *(uint4*)&s_V[w][key * kVs + c] = rv[i];
+                }
+            }
+            if (more) {
+                request_V(set ^ 1);
+                look_up(t + 8 * kStepKeys);
+            }
+            if (t + kStepKeys > k1) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (t + 16 * (e / 4) + 4 * lg + e % 4 >= k1) s[e / 4][e % 4] = -INFINITY;
+            }
+            wave_sync();
+            take(s, vs, false);
+            wave_sync();
+        }
+    } else if (k1 > k0) {
+        bad = 1;  // positions without a page
+    }
+    l = row_sum(l);
+
+    // the four waves
+    if (lg == 0) {
+        s_ml[w][l16][0] = m;
+        s_ml[w][l16][1] = l;
+    }
+    st |= __syncthreads_or(bad) ? kStBadCache : 0;
+    float mt = -INFINITY, lt = 0.f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) mt = fmaxf(mt, s_ml[x][l16][0]);
+    const float base = mt == -INFINITY ? 0.f : mt;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) lt += s_ml[x][l16][1] * __builtin_amdgcn_exp2f(s_ml[x][l16][0] - base);
+    {
+        const float al = __builtin_amdgcn_exp2f(m - base);
+        float* so = (float*)s_V + (w * 16 + l16) * kOs + 4 * lg;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) *(f32x4*)(so + 16 * i) = o[i] * al;
+    }
+    // a row's m and l for all threads
+    __shared__ float s_m[16], s_l[16];
+    if (tid < 16) {
+        s_m[tid] = mt;
+        s_l[tid] = lt;
+    }
+    __syncthreads();
+    if (hk == 0 && tid == 0) {
+        if (pt.n > 1)
+            ws.bits[part] = st;
+        else if (a.status)
+            a.status[b] = st;
+    }
+    if (pt.n == 1 && st) return;
+    for (int i = tid; i < R * (D / 4); i += 256) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v += *(const f32x4*)((const float*)s_V + (x * 16 + r) * kOs + d);
+        const size_t at = (size_t)(r / g) * H + hk * g + r % g;
+        if (pt.n > 1) {
+            *(f32x4*)(ws.o + ((size_t)part * T * H + at) * D + d) = v;
+            if (d == 0) {
+                ws.ml[((size_t)part * T * H + at) * 2] = s_m[r];
+                ws.ml[((size_t)part * T * H + at) * 2 + 1] = s_l[r];
+            }
+        } else {
+            const float lr = s_l[r];
+            gstore((uint2*)((uint16_t*)a.o + ((size_t)b * T * H + at) * D + d),
+                   make_uint2(pack_bf16x2(v[0] / lr, v[1] / lr), pack_bf16x2(v[2] / lr, v[3] / lr)));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- tiles
+// RT row tiles of 16 per wave
+template <int ND, bool E4M3, int RT>
+__global__ __launch_bounds__(256, 2) void attn_tiles_kernel(AttnArgs a, AttnPlan plan, AttnWorkspace ws, int row_blocks) {
+    constexpr int D = ND * 32, M = 64 * RT, kKs = D + 8, kVs = D + 16;
+    __shared__ __attribute__((aligned(8))) int s_red[6];
+    __shared__ Part s_part;
+    __shared__ __attribute__((aligned(16))) uint16_t s_K[kTileKeys * kKs], s_V[kTileKeys * kVs];
+    __shared__ __attribute__((aligned(16))) float s_ks[kTileKeys], s_vs[kTileKeys];
+    __shared__ uint32_t s_row[2][kTileKeys];
+    __shared__ int s_par[1024], s_odd;
+    extern __shared__ uint32_t s_anc[];  // [nodes of the block][words of T bits]
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int l16 = lane & 15, lg = lane >> 4;
+    const int lid = xcd_block(blockIdx.x, gridDim.x), reader = lid % plan.readers, part = lid / plan.readers;
+    const int hk = reader / row_blocks, rb = reader % row_blocks;
+    const Part pt = find_part<256>(a.cache_len, a.batch, a.room, plan, part, false, s_red, &s_part);
+    if (!pt.ok) return;
+    const int b = pt.item, T = a.T, H = a.H, g = H / a.Hk, R = T * g, row0 = rb * M;
+    const bool last = pt.k == pt.n - 1;
+    int st = pt.bad_len ? kStBadCache : 0;
+    const int first = row0 / g, last_node = min(R - 1, row0 + M - 1) / g, words = (T + 31) / 32;
+    if (last) st |= tree_words<256>(a.parent + (size_t)b * T, T, first, last_node - first + 1, words, s_par, s_anc);
+    if (tid == 0) s_odd = 0;
+
+    // rows of this wave: row0 + 16 (w RT + t) + l16
+    int node[RT];
+    bf16x8 q[RT][ND];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int r = min(row0 + 16 * (w * RT + t) + l16, R - 1);
+        node[t] = r / g;
+        const uint16_t* qp = (const uint16_t*)a.q + (((size_t)b * T + node[t]) * H + hk * g + r % g) * D + 8 * lg;
+#pragma unroll
+        for (int i = 0; i < ND; ++i) q[t][i] = as_operand(gload((const uint4*)(qp + 32 * i)));
+    }
+    float m[RT], l[RT];
+    f32x4 o[RT][D / 16];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        m[t] = -INFINITY;
+        l[t] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) o[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // One tile of keys in LDS: scores, softmax, product. MASK: 0 all keys count,
+    // 1 those below `limit`, 2 the tree's (keys j0 + ..., by ancestors)
+    auto take = [&](auto mask, auto scaled, int limit, int j0, bool odd) {
+        constexpr int MASK = decltype(mask)::value;
+        constexpr bool SCALED = decltype(scaled)::value;
+        f32x4 s[RT][4];
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int i = 0; i < ND; ++i) {
+                const bf16x8 kf = *(const bf16x8*)&s_K[(16 * x + l16) * kKs + 32 * i + 8 * lg];
+#pragma unroll
+                for (int t = 0; t < RT; ++t) s[t][x] = mma(kf, q[t][i], s[t][x]);
+            }
+        bf16x8 pf[RT][2];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                if (SCALED)
+                    s[t][x] *= *(const f32x4*)&s_ks[16 * x + 4 * lg];
+                else
+                    s[t][x] *= a.scale_log2;
+                if (MASK) {
+                    const int j = 16 * x + 4 * lg;
+                    uint32_t bits = 0;
+                    if (MASK == 2) bits = s_anc[(node[t] - first) * words + min((j0 + j) / 32, words - 1)] >> ((j0 + j) % 32);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const bool seen = j + r < limit && (MASK == 1 || (bits >> r & 1));
+                        s[t][x][r] = seen ? s[t][x][r] : -INFINITY;
+                    }
+                }
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) top = fmaxf(top, fmaxf(fmaxf(s[t][x][0], s[t][x][1]), fmaxf(s[t][x][2], s[t][x][3])));
+            top = row_max(top);
+            const float mn = fmaxf(m[t], top), base = mn == -INFINITY ? 0.f : mn;
+            if (__ballot(mn > m[t])) {  // some row's maximum moved
+                const float al = __builtin_amdgcn_exp2f(m[t] - base);
+                l[t] *= al;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) o[t][i] *= al;
+            }
+            m[t] = mn;
+            float sum = 0.f;
+            uint32_t u[8];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                f32x4 p;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    p[r] = __builtin_amdgcn_exp2f(s[t][x][r] - base);
+                    sum += p[r];
+                }
+                if (SCALED) {
+                    const f32x4 vs = *(const f32x4*)&s_vs[16 * x + 4 * lg];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) p[r] = MASK && p[r] == 0.f ? 0.f : p[r] * vs[r];
+                }
+                u[2 * x] = pack_bf16x2(p[0], p[1]);
+                u[2 * x + 1] = pack_bf16x2(p[2], p[3]);
+            }
+            l[t] += sum;  // of this lane's keys; the four lanes of a row meet at the end
+            pf[t][0] = as_operand(make_uint4(u[0], u[1], u[2], u[3]));
+            pf[t][1] = as_operand(make_uint4(u[4], u[5], u[6], u[7]));
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const bf16x8 v = read_columns(&s_V[32 * x * kVs + 16 * i], kVs, lane);
+                if (MASK == 2 && odd) {
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        s16x8 seen;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) seen[e] = s[t][2 * x + e / 4][e % 4] != -INFINITY ? 0x3f80 : 0;
+                        o[t][i] = mma(only_finite(v), pf[t][x], o[t][i]) + nonfinite_part(v, __builtin_bit_cast(bf16x8, seen));
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) o[t][i] = mma(v, pf[t][x], o[t][i]);
+                }
+            }
+    };
+    using yes = std::true_type;
+    using no = std::false_type;
+
+    const int k0 = pt.k * pt.keys, k1 = last ? pt.len : min(pt.len, k0 + pt.keys);
+    int bad = 0;
+    if (k1 > k0 && a.n_pages > 0) {
+        constexpr int EB = E4M3 ? 1 : 2;
+        constexpr int L = kTileKeys * D * EB / 16 / 256;  // 16-byte loads of K, and of V, per thread
+        constexpr int RR = 256 / (D * EB / 16);           // rows that one of them covers
+        const int32_t* table = a.page_table + (size_t)b * a.max_pages;
+        uint4 rk[L], rv[L];
+        float rks = 1.f, rvs = 1.f;
+        int page = 0;
+        const int prow = tid / (D * EB / 16), pcol = tid % (D * EB / 16) * 16;
+        // the first wave looks up pages and rows, for all
+        auto key_of = [&](int t) { return min(t + lane, k1 - 1); };
+        auto look_up = [&](int t) {
+            if (w == 0) page = table[page_of(key_of(t), a.div)];
+        };
+        auto find_rows = [&](int t, int set) {
+            if (w != 0) return;
+            const bool fine = page_ok(a, page);
+            bad |= !fine;
+            s_row[set][lane] = cache_row(a, fine ? page : 0, hk, key_of(t));
+        };
+        auto request = [&](int set) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const size_t at = (size_t)s_row[set][prow + i * RR] * (D * EB) + pcol;
+                rk[i] = gload((const uint4*)((const char*)a.k_cache + at));
+                rv[i] = gload((const uint4*)((const char*)a.v_cache + at));
+            }
+            if (E4M3 && w == 0) {
+                rks = gload(a.k_scale + s_row[set][lane]);
+                rvs = gload(a.v_scale + s_row[set][lane]);
+            }
+        };
+        look_up(k0);
+        find_rows(k0, 0);
+        look_up(k0 + kTileKeys);
+        __syncthreads();
+        request(0);
+        int set = 0;
+        for (int t = k0; t < k1; t += kTileKeys, set ^= 1) {
+            lds_barrier();  // the last tile's reads are done
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const int key = prow + i * RR, c = pcol / EB;
+                if (E4M3) {
+                    *(uint4*)&s_K[key * kKs + c] = e4m3_to_bf16(make_uint2(rk[i].x, rk[i].y));
+                    *(uint4*)&s_K[key * kKs + c + 8] = e4m3_to_bf16(make_uint2(rk[i].z, rk[i].w));
+                    *(uint4*)&s_V[key * kVs + c] = e4m3_to_bf16(make_uint2(rv[i].x, rv[i].y));
+                    *(uint4*)&s_V[key * kVs + c + 8] = e4m3_to_bf16(make_uint2(rv[i].z, rv[i].w));
+                } else {
+                    *(uint4*)&s_K[key * kKs + c] = rk[i];
+                    *(uint4*)&s_V[key * kVs + c] = rv[i];
+                }
+            }
+            if (E4M3 && w == 0) {
+                s_ks[lane] = rks * a.scale_log2;
+                s_vs[lane] = rvs;
+            }
+            find_rows(t + kTileKeys, set ^ 1);
+            lds_barrier();
+            if (t + kTileKeys < k1) {
+                request(set ^ 1);
+                look_up(t + 2 * kTileKeys);
+            }
+            if (t + kTileKeys <= k1)
+                take(std::integral_constant<int, 0>(), std::integral_constant<bool, E4M3>(), 0, 0, false);
+            else
+                take(std::integral_constant<int, 1>(), std::integral_constant<bool, E4M3>(), k1 - t, 0, false);
+        }
+    } else if (k1 > k0) {
+        bad = 1;  // positions without a page
+    }
+    // the tree's own keys, up to the block's last node
+    if (last && !st) {
+        const size_t stride = (size_t)a.Hk * D;
+        const uint16_t* kp = (const uint16_t*)a.k + ((size_t)b * T * a.Hk + hk) * D;
+        const uint16_t* vp = (const uint16_t*)a.v + ((size_t)b * T * a.Hk + hk) * D;
+        for (int j0 = 0; j0 <= last_node; j0 += kTileKeys) {
+            __syncthreads();
+            if (tid == 0) s_odd = 0;
+            __syncthreads();
+            uint32_t strange = 0;
+            for (int i = tid; i < kTileKeys * (D / 8); i += 256) {
+                const int key = i / (D / 8), c = i % (D / 8) * 8;
+                uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
+                if (j0 + key < T) {
+                    ku = gload((const uint4*)(kp + (size_t)(j0 + key) * stride + c));
+                    vu = gload((const uint4*)(vp + (size_t)(j0 + key) * stride + c));
+                }
+                strange |= nonfinite_bits(vu);
+                *(uint4*)&s_K[key * kKs + c] = ku;
+                *(uint4*)&s_V[key * kVs + c] = vu;
+            }
+            if (strange & 0x80008000u) s_odd = 1;
+            __syncthreads();
+            take(std::integral_constant<int, 2>(), no(), T - j0, j0, s_odd != 0);
+        }
+    }
+    st |= __syncthreads_or(bad) ? kStBadCache : 0;
+    if (reader == 0 && tid == 0) {
+        if (pt.n > 1)
+            ws.bits[part] = st;
+        else if (a.status)
+            a.status[b] = st;
+    }
+    if (pt.n == 1 && st) return;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const float lr = row_sum(l[t]);
+        const int r = row0 + 16 * (w * RT + t) + l16;
+        if (r >= R) continue;
+        const size_t at = (size_t)node[t] * H + hk * g + r % g;
+        if (pt.n > 1) {
+            float* to = ws.o + ((size_t)part * T * H + at) * D + 4 * lg;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) *(f32x4*)(to + 16 * i) = o[t][i];
+            if (lg == 0) {
+                ws.ml[((size_t)part * T * H + at) * 2] = m[t];
+                ws.ml[((size_t)part * T * H + at) * 2 + 1] = lr;
+            }
+        } else {
+            const float inv = 1.f / lr;
+            uint16_t* to = (uint16_t*)a.o + ((size_t)b * T * H + at) * D + 4 * lg;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                gstore((uint2*)(to + 16 * i), make_uint2(pack_bf16x2(o[t][i][0] * inv, o[t][i][1] * inv),
+                                                         pack_bf16x2(o[t][i][2] * inv, o[t][i][3] * inv)));
+        }
+    }
+}
+
+template <int ND, bool E4M3>
+void launch_nd(const AttnArgs& a, const AttnPlan& p, const AttnWorkspace& ws, int block_rows, int row_blocks, hipStream_t stream) {
+    const dim3 grid((unsigned)((long long)p.parts * p.readers));
+    const int g = a.H / a.Hk;
+    const unsigned words = (a.T + 31) / 32;
+    const unsigned nodes = min(a.T, (block_rows + g - 2) / g + 1);
+    const unsigned lds = nodes * words * 4;
+    if (block_rows == 16)
+        hipLaunchKernelGGL((attn_rows_kernel<ND, E4M3>), grid, dim3(256), 0, stream, a, p, ws);
+    else if (block_rows == 64)
+        hipLaunchKernelGGL((attn_tiles_kernel<ND, E4M3, 1>), grid, dim3(256), lds, stream, a, p, ws, row_blocks);
+    else
+        hipLaunchKernelGGL((attn_tiles_kernel<ND, E4M3, 2>), grid, dim3(256), lds, stream, a, p, ws, row_blocks);
+}
+
+}  // namespace
+
+void launch_attn_mfma(const AttnArgs& a, bool e4m3, const AttnPlan& p, const AttnWorkspace& ws, int block_rows, int row_blocks,
+                      hipStream_t stream) {
+    if (a.D == 64)
+        e4m3 ? launch_nd<2, true>(a, p, ws, block_rows, row_blocks, stream)
+             : launch_nd<2, false>(a, p, ws, block_rows, row_blocks, stream);
+    else
+        e4m3 ? launch_nd<4, true>(a, p, ws, block_rows, row_blocks, stream)
+             : launch_nd<4, false>(a, p, ws, block_rows, row_blocks, stream);
+}
+
+}  // namespace tsv

@@ -17,25 +17,6 @@
 
 namespace tsv {
 
-// Status bits of the tree, and each of `rows` rows' ancestors as bit words
-// (row i is node first + i); s_par: T ints. Acts as a barrier.
-template <int NT>
-__device__ int tree_words(const int32_t* __restrict__ parent, int T, int first, int rows, int words, int* s_par, uint32_t* s_anc) {
-    int bits = 0;
-    for (int i = threadIdx.x; i < T; i += NT) {
-        const int p = parent[i];
-        s_par[i] = p;
-        bits |= i == 0 ? (p != -1 ? kStBadRoot : 0) : (p < 0 || p >= i ? kStBadParent : 0);
-    }
-    for (int i = threadIdx.x; i < rows * words; i += NT) s_anc[i] = 0;
-    const int any = __syncthreads_or(bits);
-    if (any) return (__syncthreads_or(bits & kStBadRoot) ? kStBadRoot : 0) | (__syncthreads_or(bits & kStBadParent) ? kStBadParent : 0);
-    for (int i = threadIdx.x; i < rows; i += NT)
-        for (int j = first + i; j >= 0; j = s_par[j]) s_anc[i * words + j / 32] |= 1u << (j % 32);
-    __syncthreads();
-    return 0;
-}
-
 namespace {
 
 constexpr int kRows = 8;
@@ -286,33 +267,63 @@ void launch_join(const AttnArgs& a, const AttnPlan& p, const AttnWorkspace& ws, 
         hipLaunchKernelGGL((attn_join_kernel<TIO, 4>), grid, dim3(256), 0, stream, a, p, ws, blocks);
 }
 
-AttnPlan plan_of(int batch, int T, int H, int Hk, long long room, int* row_blocks) {
-    *row_blocks = (T * (H / Hk) + kRows - 1) / kRows;
-    return attn_plan(batch, room, Hk * *row_blocks, kAttnMinKeys);
+// Whether the bf16 kernels take the shape: 32-bit row numbers into the pool, and
+// 16-byte rows of 64 or 128 elements (their alignment is looked at per call)
+bool matrix_shape(const tsv_attn_shape* s) {
+    return s->in_dtype == TSV_BF16 && (s->head_dim == 64 || s->head_dim == 128) && !(s->flags & TSV_FLAG_FORCE_GENERIC) &&
+           (long long)s->n_pages * s->n_kv_heads * s->page_size < (1LL << 32);
+}
+
+// Rows of a work-group: 16 (attn_rows_kernel), 64 or 128 (attn_tiles_kernel, 128
+// unless that leaves a fifth more rows empty than 64 would), 8 (plain)
+int block_rows_of(const tsv_attn_shape* s, bool matrix) {
+    if (!matrix) return kRows;
+    const int R = s->n_nodes * (s->n_heads / s->n_kv_heads);
+    if (R <= 16) return 16;
+    const int r64 = (R + 63) / 64 * 64, r128 = (R + 127) / 128 * 128;
+    return r128 * 5 > r64 * 6 ? 64 : 128;
+}
+
+AttnPlan plan_of(const tsv_attn_shape* s, bool matrix, int* block_rows, int* row_blocks) {
+    *block_rows = block_rows_of(s, matrix);
+    *row_blocks = (int)(((long long)s->n_nodes * (s->n_heads / s->n_kv_heads) + *block_rows - 1) / *block_rows);
+    return attn_plan(s->batch, (long long)s->max_pages * s->page_size, s->n_kv_heads * *row_blocks, kAttnMinKeys);
 }
 
 }  // namespace
 
+// both kernels' needs: which of them runs depends on the pointers too
 uint64_t attn_verify_workspace_bytes(const tsv_attn_shape* s) {
-    int rb;
-    const AttnPlan p = plan_of(s->batch, s->n_nodes, s->n_heads, s->n_kv_heads, (long long)s->max_pages * s->page_size, &rb);
-    return attn_workspace_bytes(p, s->n_nodes, s->n_heads, s->head_dim);
+    uint64_t most = 0;
+    for (int matrix = 0; matrix <= (int)matrix_shape(s); ++matrix) {
+        int br, rb;
+        const uint64_t n = attn_workspace_bytes(plan_of(s, matrix, &br, &rb), s->n_nodes, s->n_heads, s->head_dim);
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 long long attn_verify_blocks(const tsv_attn_shape* s) {
-    int rb;
-    const AttnPlan p = plan_of(s->batch, s->n_nodes, s->n_heads, s->n_kv_heads, (long long)s->max_pages * s->page_size, &rb);
-    const long long join = (long long)s->batch * (((long long)s->n_nodes * s->n_heads + 3) / 4);
-    const long long parts = (long long)p.parts * p.readers;
-    return parts > join ? parts : join;
+    long long most = (long long)s->batch * (((long long)s->n_nodes * s->n_heads + 3) / 4);  // the join
+    for (int matrix = 0; matrix <= (int)matrix_shape(s); ++matrix) {
+        int br, rb;
+        const AttnPlan p = plan_of(s, matrix, &br, &rb);
+        const long long n = (long long)p.parts * p.readers;
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 hipError_t launch_attn_verify(const AttnArgs& a, const tsv_attn_shape* s, void* workspace, hipStream_t stream) {
-    int row_blocks;
-    const AttnPlan p = plan_of(a.batch, a.T, a.H, a.Hk, a.room, &row_blocks);
+    const uintptr_t all = (uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.o | (uintptr_t)a.k_cache | (uintptr_t)a.v_cache;
+    const bool matrix = matrix_shape(s) && all % 16 == 0;
+    int block_rows, row_blocks;
+    const AttnPlan p = plan_of(s, matrix, &block_rows, &row_blocks);
     const AttnWorkspace ws = attn_workspace(workspace, p, a.T, a.H, a.D);
     const bool bf16 = s->in_dtype == TSV_BF16, e4m3 = s->cache_dtype == TSV_E4M3;
-    if (bf16 && e4m3)
+    if (matrix)
+        launch_attn_mfma(a, e4m3, p, ws, block_rows, row_blocks, stream);
+    else if (bf16 && e4m3)
         launch_plain<uint16_t, uint8_t>(a, p, ws, row_blocks, stream);
     else if (bf16)
         launch_plain<uint16_t, uint16_t>(a, p, ws, row_blocks, stream);

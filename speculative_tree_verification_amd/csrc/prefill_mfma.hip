@@ -39,6 +39,7 @@
 //  - The next chunk's rows are requested between the products of this one, a
 //    third at a time: a compute unit takes about 32 bytes a cycle from its L2,
 //    and a wave waits where it asks for more at once.
+#include "mfma_util.hpp"
 #include "seq_common.hpp"
 
 namespace tsv {
@@ -48,32 +49,6 @@ constexpr int kQ = 64;        // tokens per chunk
 constexpr int kP = 64;        // head_dim
 constexpr int kXs = kP + 16;  // LDS row strides (elements)
 constexpr int kPs = kQ + 8;
-
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
-
-// Columns of a row-major LDS tile as an operand: the lane with column l % 16 of
-// `tile` gets rows 4 (l / 16) + e, e < 4, and the same 16 rows on. (Each 16-lane
-// group names 4 rows of 16 columns, 4 columns a lane, and receives them
-// transposed.) The 16 columns are 4 pieces of 4, PIECE elements apart.
-template <int PIECE = 4>
-__device__ __forceinline__ bf16x8 read_columns(const uint16_t* tile, int stride, int lane) {
-    const uint16_t* p = tile + lane / 4 * stride + lane % 4 * PIECE;
-    typedef s16x4 __attribute__((address_space(3))) lds_s16x4;
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * stride));
-    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
-}
-
-// Two 4-element pieces of a row, 16 elements apart, in the same order
-__device__ __forceinline__ bf16x8 read_row(const uint16_t* p) {
-    const s16x4 a = *(const s16x4*)p, b = *(const s16x4*)(p + 16);
-    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
-}
-
-__device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
 
 // 8 floats as NP bf16 parts, each the rounding of what the ones before leave (exact)
 template <int NP>
@@ -97,13 +72,6 @@ __device__ __forceinline__ Parts<NP> split(const float* v) {
 #pragma unroll
     for (int n = 0; n < NP; ++n) p.part[n] = __builtin_bit_cast(bf16x8, make_uint4(u[n][0], u[n][1], u[n][2], u[n][3]));
     return p;
-}
-
-// Sign bits of the halves of the result: whether a bf16 of `u` is not finite
-// (an exponent of ones carries into the sign)
-__device__ __forceinline__ uint32_t nonfinite_bits(uint4 u) {
-    return ((u.x & 0x7fff7fffu) + 0x00800080u) | ((u.y & 0x7fff7fffu) + 0x00800080u) |
-           ((u.z & 0x7fff7fffu) + 0x00800080u) | ((u.w & 0x7fff7fffu) + 0x00800080u);
 }
 
 // inclusive sum over the wave's lanes 0 .. lane (row shifts, then the last lane
