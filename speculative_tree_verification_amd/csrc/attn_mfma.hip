@@ -11,8 +11,8 @@
 //          small tree. Four waves take 32 keys each in turn and meet at the end;
 //          K goes from memory into the operand registers directly. Bound by the
 //          cache's bytes.
-//   tiles  more rows: a wave has 16 or 32 rows of its own, and 64 keys at a time
-//          are shared in LDS. Bound by matrix and vector work.
+//   tiles  more rows: a wave has 16 rows of its own, and 64 keys at a time are
+//          shared in LDS by 4 or 8 waves. Bound by matrix and vector work.
 // In both, the loads of the next keys are under way while these are worked on,
 // and the page of a key is looked up one step before its row is loaded.
 #include "attn_common.hpp"
@@ -44,30 +44,37 @@ __device__ __forceinline__ uint32_t cache_row(const AttnArgs& a, int page, int h
 
 __device__ __forceinline__ bf16x8 as_operand(uint4 u) { return __builtin_bit_cast(bf16x8, u); }
 
-// What the values that are not finite among 32 keys' V add to a row that sees
-// them: v is V^T of these keys, seen the row's 0/1 weights of them. Such a V is
-// taken out of the ordinary product, where a weight of 0 would spread it.
-__device__ __forceinline__ bf16x8 only_finite(bf16x8 v) {
-    s16x8 s = __builtin_bit_cast(s16x8, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = (s[e] & 0x7f80) == 0x7f80 ? (short)0 : s[e];
-    return __builtin_bit_cast(bf16x8, s);
+// Scores stay as the product gives them, and their factor enters the exponent's
+// multiply-add: it has to be positive, so a negative one turns q's signs (exact),
+// and 0 becomes the smallest normal number (a masked score of -inf stays one).
+__device__ __forceinline__ float score_factor(const AttnArgs& a) { return fmaxf(fabsf(a.scale_log2), 1.17549435e-38f); }
+__device__ __forceinline__ bf16x8 query_operand(const AttnArgs& a, uint4 u) {
+    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    return as_operand(make_uint4(u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip));
 }
-__device__ __forceinline__ f32x4 nonfinite_part(bf16x8 v, bf16x8 seen) {
-    s16x8 up = __builtin_bit_cast(s16x8, v), down = up;
+
+// A node's value that is not finite may reach the rows that see the node only,
+// but a product would carry it to all rows, at weight 0. So such elements enter
+// the product as 0, and afterwards each row adds those of the nodes it sees.
+__device__ __forceinline__ uint4 only_finite(uint4 u) {
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {  // 1 for +inf and NaN, and for -inf and NaN
-        const int b = (uint16_t)up[e];
-        const bool odd = (b & 0x7f80) == 0x7f80, nan = odd && (b & 0x7f);
-        up[e] = odd && (nan || !(b & 0x8000)) ? 0x3f80 : 0;
-        down[e] = odd && (nan || (b & 0x8000)) ? 0x3f80 : 0;
+    for (int i = 0; i < 4; ++i) {
+        if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+        if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0x0000ffffu;
     }
-    const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-    const f32x4 p = mma(__builtin_bit_cast(bf16x8, up), seen, z), n = mma(__builtin_bit_cast(bf16x8, down), seen, z);
-    f32x4 r;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// v: the node's values from this lane's first d on; o[i] holds d = 16 i + r
+template <int NO>
+__device__ __forceinline__ void add_nonfinite(const uint16_t* v, f32x4* o) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = (p[i] > 0.f ? INFINITY : 0.f) + (n[i] > 0.f ? -INFINITY : 0.f);
-    return r;
+    for (int i = 0; i < NO; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint16_t b = gload(v + 16 * i + r);
+            if ((b & 0x7f80) == 0x7f80) o[i][r] += bf16_bits_to_f32(b);
+        }
 }
 
 // ---------------------------------------------------------------- rows
@@ -98,8 +105,9 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
     {
         const uint16_t* qp = (const uint16_t*)a.q + (((size_t)b * T + node) * H + head) * D + 16 * lg;
 #pragma unroll
-        for (int i = 0; i < ND; ++i) q[i] = as_operand(gload((const uint4*)(qp + 64 * (i / 2) + 8 * (i % 2))));
+        for (int i = 0; i < ND; ++i) q[i] = query_operand(a, gload((const uint4*)(qp + 64 * (i / 2) + 8 * (i % 2))));
     }
+    const float c = score_factor(a);
     if (last) {  // at most 16 nodes: one word of ancestors each
         int bits = 0;
         if (tid < T) {
@@ -120,20 +128,20 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
         }
     }
 
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f;  // in units of the raw scores
     f32x4 o[D / 16];
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // softmax and product of 32 keys: s the scores times scale log2(e) (masked:
-    // -inf), vs the factor of each value row; V in this wave's LDS
-    auto take = [&](const f32x4* s, const f32x4* vs, bool odd) {
+    // softmax and product of 32 keys: s the raw scores (masked: -inf), vs the factor
+    // of each value row; V in this wave's LDS
+    auto take = [&](const f32x4* s, const f32x4* vs) {
         float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                           fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
         top = row_max(top);
-        const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
+        const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn * c;
         if (__ballot(mn > m)) {  // some row's maximum moved
-            const float al = __builtin_amdgcn_exp2f(m - base);
+            const float al = __builtin_amdgcn_exp2f(fmaf(m, c, -base));
             l *= al;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) o[i] *= al;
@@ -142,7 +150,7 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
         float p[8], sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            p[e] = __builtin_amdgcn_exp2f(s[e / 4][e % 4] - base);
+            p[e] = __builtin_amdgcn_exp2f(fmaf(s[e / 4][e % 4], c, -base));
             sum += p[e];
         }
         l += sum;  // of this lane's keys; the four lanes of a row meet at the end
@@ -152,19 +160,8 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
         }
         const bf16x8 pf = as_operand(make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]),
                                                 pack_bf16x2(p[6], p[7])));
-        if (!odd) {
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) o[i] = mma(read_columns(&s_V[w][16 * i], kVs, lane), pf, o[i]);
-        } else {
-            s16x8 seen;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) seen[e] = s[e / 4][e % 4] != -INFINITY ? 0x3f80 : 0;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const bf16x8 v = read_columns(&s_V[w][16 * i], kVs, lane);
-                o[i] = mma(only_finite(v), pf, o[i]) + nonfinite_part(v, __builtin_bit_cast(bf16x8, seen));
-            }
-        }
+        for (int i = 0; i < D / 16; ++i) o[i] = mma(read_columns(&s_V[w][16 * i], kVs, lane), pf, o[i]);
     };
 
     // the tree's own keys, in the wave that has the fewest cache steps
@@ -182,18 +179,27 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int j = 4 * lg + r;
-            s[0][r] = j < T && (anc >> j & 1) ? s[0][r] * a.scale_log2 : -INFINITY;
+            s[0][r] = j < T && (anc >> j & 1) ? s[0][r] : -INFINITY;
             s[1][r] = -INFINITY;
         }
-        uint32_t strange = 0;
+        uint32_t strange = 0;  // nodes whose values are not all finite, of this lane's pieces
         for (int i = lane; i < kStepKeys * (D / 8); i += kWave) {
             const int key = i / (D / 8), c = i % (D / 8) * 8;
-            const uint4 u = key < T ? gload((const uint4*)(vp + (size_t)key * stride + c)) : make_uint4(0, 0, 0, 0);
-            strange |= nonfinite_bits(u);
+            uint4 u = key < T ? gload((const uint4*)(vp + (size_t)key * stride + c)) : make_uint4(0, 0, 0, 0);
+            if (nonfinite_bits(u) & 0x80008000u) {
+                strange |= 1u << key;
+                u = only_finite(u);
+            }
             *(uint4*)&s_V[w][key * kVs + c] = u;
         }
         wave_sync();
-        take(s, nullptr, __ballot((strange & 0x80008000u) != 0) != 0);
+        take(s, nullptr);
+        if (__ballot(strange != 0)) {
+#pragma unroll
+            for (int x = 1; x < kWave; x <<= 1) strange |= __shfl_xor(strange, x, kWave);
+            for (int j = 0; j < T; ++j)
+                if (strange & anc & (1u << j)) add_nonfinite<D / 16>(vp + (size_t)j * stride + 4 * lg, o);
+        }
         wave_sync();
     }
 
@@ -252,7 +258,7 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
             const bool more = t + 4 * kStepKeys < k1;
             if (E4M3) {
                 if (lane < kStepKeys) {
-                    s_ks[w][lane] = rks * a.scale_log2;
+                    s_ks[w][lane] = rks;
                     s_vs[w][lane] = rvs;
                 }
                 wave_sync();
@@ -272,7 +278,6 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
                 } else {
 #pragma unroll
                     for (int i = 0; i < KL; ++i) s[x] = mma(as_operand(rk[x][i]), q[i], s[x]);
-                    s[x] *= a.scale_log2;
                 }
             }
             if (more) {
@@ -300,13 +305,14 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
                     if (t + 16 * (e / 4) + 4 * lg + e % 4 >= k1) s[e / 4][e % 4] = -INFINITY;
             }
             wave_sync();
-            take(s, vs, false);
+            take(s, vs);
             wave_sync();
         }
     } else if (k1 > k0) {
         bad = 1;  // positions without a page
     }
     l = row_sum(l);
+    m = m == -INFINITY ? m : m * c;
 
     // the four waves
     if (lg == 0) {
@@ -361,155 +367,126 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
 }
 
 // ---------------------------------------------------------------- tiles
-// RT row tiles of 16 per wave
-template <int ND, bool E4M3, int RT>
-__global__ __launch_bounds__(256, 2) void attn_tiles_kernel(AttnArgs a, AttnPlan plan, AttnWorkspace ws, int row_blocks) {
-    constexpr int D = ND * 32, M = 64 * RT, kKs = D + 8, kVs = D + 16;
-    __shared__ __attribute__((aligned(8))) int s_red[6];
+// NW waves of 16 rows
+template <int ND, bool E4M3, int NW>
+__global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(AttnArgs a, AttnPlan plan, AttnWorkspace ws, int row_blocks) {
+    constexpr int D = ND * 32, TH = 64 * NW, M = 16 * NW, kKs = D + 8, kVs = D + 16;
+    __shared__ __attribute__((aligned(8))) int s_red[NW + 2];
     __shared__ Part s_part;
     __shared__ __attribute__((aligned(16))) uint16_t s_K[kTileKeys * kKs], s_V[kTileKeys * kVs];
     __shared__ __attribute__((aligned(16))) float s_ks[kTileKeys], s_vs[kTileKeys];
     __shared__ uint32_t s_row[2][kTileKeys];
-    __shared__ int s_par[1024], s_odd;
+    __shared__ int s_par[1024];
+    __shared__ uint32_t s_odd[32];  // nodes whose values are not all finite
     extern __shared__ uint32_t s_anc[];  // [nodes of the block][words of T bits]
     const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int l16 = lane & 15, lg = lane >> 4;
     const int lid = xcd_block(blockIdx.x, gridDim.x), reader = lid % plan.readers, part = lid / plan.readers;
     const int hk = reader / row_blocks, rb = reader % row_blocks;
-    const Part pt = find_part<256>(a.cache_len, a.batch, a.room, plan, part, false, s_red, &s_part);
+    const Part pt = find_part<TH>(a.cache_len, a.batch, a.room, plan, part, false, s_red, &s_part);
     if (!pt.ok) return;
     const int b = pt.item, T = a.T, H = a.H, g = H / a.Hk, R = T * g, row0 = rb * M;
     const bool last = pt.k == pt.n - 1;
     int st = pt.bad_len ? kStBadCache : 0;
     const int first = row0 / g, last_node = min(R - 1, row0 + M - 1) / g, words = (T + 31) / 32;
-    if (last) st |= tree_words<256>(a.parent + (size_t)b * T, T, first, last_node - first + 1, words, s_par, s_anc);
-    if (tid == 0) s_odd = 0;
+    if (last) st |= tree_words<TH>(a.parent + (size_t)b * T, T, first, last_node - first + 1, words, s_par, s_anc);
+    if (tid < 32) s_odd[tid] = 0;
 
-    // rows of this wave: row0 + 16 (w RT + t) + l16
-    int node[RT];
-    bf16x8 q[RT][ND];
+    // this lane's row
+    const int row = row0 + 16 * w + l16, node = min(row, R - 1) / g;
+    bf16x8 q[ND];
+    {
+        const uint16_t* qp = (const uint16_t*)a.q + (((size_t)b * T + node) * H + hk * g + min(row, R - 1) % g) * D + 8 * lg;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        const int r = min(row0 + 16 * (w * RT + t) + l16, R - 1);
-        node[t] = r / g;
-        const uint16_t* qp = (const uint16_t*)a.q + (((size_t)b * T + node[t]) * H + hk * g + r % g) * D + 8 * lg;
-#pragma unroll
-        for (int i = 0; i < ND; ++i) q[t][i] = as_operand(gload((const uint4*)(qp + 32 * i)));
+        for (int i = 0; i < ND; ++i) q[i] = query_operand(a, gload((const uint4*)(qp + 32 * i)));
     }
-    float m[RT], l[RT];
-    f32x4 o[RT][D / 16];
+    const float c = score_factor(a);
+    float m = -INFINITY, l = 0.f;  // in units of the raw scores
+    f32x4 o[D / 16];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        m[t] = -INFINITY;
-        l[t] = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) o[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int i = 0; i < D / 16; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     // One tile of keys in LDS: scores, softmax, product. MASK: 0 all keys count,
     // 1 those below `limit`, 2 the tree's (keys j0 + ..., by ancestors)
-    auto take = [&](auto mask, auto scaled, int limit, int j0, bool odd) {
+    auto take = [&](auto mask, auto scaled, int limit, int j0) {
         constexpr int MASK = decltype(mask)::value;
         constexpr bool SCALED = decltype(scaled)::value;
-        f32x4 s[RT][4];
+        f32x4 s[4];
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
+        for (int x = 0; x < 4; ++x) s[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // (fences: the compiler would read all of K, or of V, into registers first)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) s[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < ND; ++i) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int i = 0; i < ND; ++i) {
-                const bf16x8 kf = *(const bf16x8*)&s_K[(16 * x + l16) * kKs + 32 * i + 8 * lg];
-#pragma unroll
-                for (int t = 0; t < RT; ++t) s[t][x] = mma(kf, q[t][i], s[t][x]);
-            }
-        bf16x8 pf[RT][2];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                if (SCALED)
-                    s[t][x] *= *(const f32x4*)&s_ks[16 * x + 4 * lg];
-                else
-                    s[t][x] *= a.scale_log2;
-                if (MASK) {
-                    const int j = 16 * x + 4 * lg;
-                    uint32_t bits = 0;
-                    if (MASK == 2) bits = s_anc[(node[t] - first) * words + min((j0 + j) / 32, words - 1)] >> ((j0 + j) % 32);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const bool seen = j + r < limit && (MASK == 1 || (bits >> r & 1));
-                        s[t][x][r] = seen ? s[t][x][r] : -INFINITY;
-                    }
-                }
-            }
-            float top = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) top = fmaxf(top, fmaxf(fmaxf(s[t][x][0], s[t][x][1]), fmaxf(s[t][x][2], s[t][x][3])));
-            top = row_max(top);
-            const float mn = fmaxf(m[t], top), base = mn == -INFINITY ? 0.f : mn;
-            if (__ballot(mn > m[t])) {  // some row's maximum moved
-                const float al = __builtin_amdgcn_exp2f(m[t] - base);
-                l[t] *= al;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) o[t][i] *= al;
-            }
-            m[t] = mn;
-            float sum = 0.f;
-            uint32_t u[8];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                f32x4 p;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    p[r] = __builtin_amdgcn_exp2f(s[t][x][r] - base);
-                    sum += p[r];
-                }
-                if (SCALED) {
-                    const f32x4 vs = *(const f32x4*)&s_vs[16 * x + 4 * lg];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) p[r] = MASK && p[r] == 0.f ? 0.f : p[r] * vs[r];
-                }
-                u[2 * x] = pack_bf16x2(p[0], p[1]);
-                u[2 * x + 1] = pack_bf16x2(p[2], p[3]);
-            }
-            l[t] += sum;  // of this lane's keys; the four lanes of a row meet at the end
-            pf[t][0] = as_operand(make_uint4(u[0], u[1], u[2], u[3]));
-            pf[t][1] = as_operand(make_uint4(u[4], u[5], u[6], u[7]));
+            for (int x = 0; x < 4; ++x) s[x] = mma(*(const bf16x8*)&s_K[(16 * x + l16) * kKs + 32 * i + 8 * lg], q[i], s[x]);
+            __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < 4; ++x) {
+            if (SCALED) s[x] *= *(const f32x4*)&s_ks[16 * x + 4 * lg];
+            if (MASK) {
+                const int j = 16 * x + 4 * lg;
+                uint32_t bits = 0;
+                if (MASK == 2) bits = s_anc[(node - first) * words + min((j0 + j) / 32, words - 1)] >> ((j0 + j) % 32);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const bool seen = j + r < limit && (MASK == 1 || (bits >> r & 1));
+                    s[x][r] = seen ? s[x][r] : -INFINITY;
+                }
+            }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) top = fmaxf(top, fmaxf(fmaxf(s[x][0], s[x][1]), fmaxf(s[x][2], s[x][3])));
+        top = row_max(top);
+        const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn * c;
+        if (__ballot(mn > m)) {  // some row's maximum moved
+            const float al = __builtin_amdgcn_exp2f(fmaf(m, c, -base));
+            l *= al;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) o[i] *= al;
+        }
+        m = mn;
+        uint32_t u[8];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            f32x4 p;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                p[r] = __builtin_amdgcn_exp2f(fmaf(s[x][r], c, -base));
+                l += p[r];  // of this lane's keys; the four lanes of a row meet at the end
+            }
+            if (SCALED) {
+                const f32x4 vs = *(const f32x4*)&s_vs[16 * x + 4 * lg];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) p[r] = MASK && p[r] == 0.f ? 0.f : p[r] * vs[r];
+            }
+            u[2 * x] = pack_bf16x2(p[0], p[1]);
+            u[2 * x + 1] = pack_bf16x2(p[2], p[3]);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const bf16x8 pf = as_operand(make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]));
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 const bf16x8 v = read_columns(&s_V[32 * x * kVs + 16 * i], kVs, lane);
-                if (MASK == 2 && odd) {
-#pragma unroll
-                    for (int t = 0; t < RT; ++t) {
-                        s16x8 seen;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) seen[e] = s[t][2 * x + e / 4][e % 4] != -INFINITY ? 0x3f80 : 0;
-                        o[t][i] = mma(only_finite(v), pf[t][x], o[t][i]) + nonfinite_part(v, __builtin_bit_cast(bf16x8, seen));
-                    }
-                } else {
-#pragma unroll
-                    for (int t = 0; t < RT; ++t) o[t][i] = mma(v, pf[t][x], o[t][i]);
-                }
+                o[i] = mma(v, pf, o[i]);
+                if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
+        }
     };
-    using yes = std::true_type;
-    using no = std::false_type;
 
     const int k0 = pt.k * pt.keys, k1 = last ? pt.len : min(pt.len, k0 + pt.keys);
     int bad = 0;
     if (k1 > k0 && a.n_pages > 0) {
         constexpr int EB = E4M3 ? 1 : 2;
-        constexpr int L = kTileKeys * D * EB / 16 / 256;  // 16-byte loads of K, and of V, per thread
-        constexpr int RR = 256 / (D * EB / 16);           // rows that one of them covers
+        constexpr int L = (kTileKeys * D * EB / 16 + TH - 1) / TH;  // 16-byte loads of K, and of V, per thread
+        constexpr int RR = TH / (D * EB / 16);           // rows that one of them covers
         const int32_t* table = a.page_table + (size_t)b * a.max_pages;
         uint4 rk[L], rv[L];
         float rks = 1.f, rvs = 1.f;
         int page = 0;
+        const bool loads = tid < kTileKeys * D * EB / 16;  // false only where half of the threads hold a whole tile
         const int prow = tid / (D * EB / 16), pcol = tid % (D * EB / 16) * 16;
         // the first wave looks up pages and rows, for all
         auto key_of = [&](int t) { return min(t + lane, k1 - 1); };
@@ -525,6 +502,7 @@ __global__ __launch_bounds__(256, 2) void attn_tiles_kernel(AttnArgs a, AttnPlan
         auto request = [&](int set) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
+                if (!loads) break;
                 const size_t at = (size_t)s_row[set][prow + i * RR] * (D * EB) + pcol;
                 rk[i] = gload((const uint4*)((const char*)a.k_cache + at));
                 rv[i] = gload((const uint4*)((const char*)a.v_cache + at));
@@ -544,6 +522,7 @@ __global__ __launch_bounds__(256, 2) void attn_tiles_kernel(AttnArgs a, AttnPlan
             lds_barrier();  // the last tile's reads are done
 #pragma unroll
             for (int i = 0; i < L; ++i) {
+                if (!loads) break;
                 const int key = prow + i * RR, c = pcol / EB;
                 if (E4M3) {
                     *(uint4*)&s_K[key * kKs + c] = e4m3_to_bf16(make_uint2(rk[i].x, rk[i].y));
@@ -556,7 +535,7 @@ __global__ __launch_bounds__(256, 2) void attn_tiles_kernel(AttnArgs a, AttnPlan
                 }
             }
             if (E4M3 && w == 0) {
-                s_ks[lane] = rks * a.scale_log2;
+                s_ks[lane] = rks;
                 s_vs[lane] = rvs;
             }
             find_rows(t + kTileKeys, set ^ 1);
@@ -566,9 +545,9 @@ __global__ __launch_bounds__(256, 2) void attn_tiles_kernel(AttnArgs a, AttnPlan
                 look_up(t + 2 * kTileKeys);
             }
             if (t + kTileKeys <= k1)
-                take(std::integral_constant<int, 0>(), std::integral_constant<bool, E4M3>(), 0, 0, false);
+                take(std::integral_constant<int, 0>(), std::integral_constant<bool, E4M3>(), 0, 0);
             else
-                take(std::integral_constant<int, 1>(), std::integral_constant<bool, E4M3>(), k1 - t, 0, false);
+                take(std::integral_constant<int, 1>(), std::integral_constant<bool, E4M3>(), k1 - t, 0);
         }
     } else if (k1 > k0) {
         bad = 1;  // positions without a page
@@ -580,23 +559,28 @@ __global__ __launch_bounds__(256, 2) void attn_tiles_kernel(AttnArgs a, AttnPlan
         const uint16_t* vp = (const uint16_t*)a.v + ((size_t)b * T * a.Hk + hk) * D;
         for (int j0 = 0; j0 <= last_node; j0 += kTileKeys) {
             __syncthreads();
-            if (tid == 0) s_odd = 0;
-            __syncthreads();
-            uint32_t strange = 0;
-            for (int i = tid; i < kTileKeys * (D / 8); i += 256) {
+            for (int i = tid; i < kTileKeys * (D / 8); i += TH) {
                 const int key = i / (D / 8), c = i % (D / 8) * 8;
                 uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
                 if (j0 + key < T) {
                     ku = gload((const uint4*)(kp + (size_t)(j0 + key) * stride + c));
                     vu = gload((const uint4*)(vp + (size_t)(j0 + key) * stride + c));
                 }
-                strange |= nonfinite_bits(vu);
+                if (nonfinite_bits(vu) & 0x80008000u) {
+                    atomicOr(&s_odd[(j0 + key) / 32], 1u << ((j0 + key) % 32));
+                    vu = only_finite(vu);
+                }
                 *(uint4*)&s_K[key * kKs + c] = ku;
                 *(uint4*)&s_V[key * kVs + c] = vu;
             }
-            if (strange & 0x80008000u) s_odd = 1;
             __syncthreads();
-            take(std::integral_constant<int, 2>(), no(), T - j0, j0, s_odd != 0);
+            take(std::integral_constant<int, 2>(), std::false_type(), T - j0, j0);
+        }
+        for (int x = 0; x < words; ++x) {
+            if (!s_odd[x]) continue;
+            for (int j = 0; j < 32; ++j)
+                if (s_odd[x] & s_anc[(node - first) * words + x] & (1u << j))
+                    add_nonfinite<D / 16>(vp + (size_t)(32 * x + j) * stride + 4 * lg, o);
         }
     }
     st |= __syncthreads_or(bad) ? kStBadCache : 0;
@@ -607,28 +591,24 @@ __global__ __launch_bounds__(256, 2) void attn_tiles_kernel(AttnArgs a, AttnPlan
             a.status[b] = st;
     }
     if (pt.n == 1 && st) return;
+    l = row_sum(l);
+    if (row >= R) return;
+    const size_t at = (size_t)node * H + hk * g + row % g;
+    if (pt.n > 1) {
+        float* to = ws.o + ((size_t)part * T * H + at) * D + 4 * lg;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        const float lr = row_sum(l[t]);
-        const int r = row0 + 16 * (w * RT + t) + l16;
-        if (r >= R) continue;
-        const size_t at = (size_t)node[t] * H + hk * g + r % g;
-        if (pt.n > 1) {
-            float* to = ws.o + ((size_t)part * T * H + at) * D + 4 * lg;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) *(f32x4*)(to + 16 * i) = o[t][i];
-            if (lg == 0) {
-                ws.ml[((size_t)part * T * H + at) * 2] = m[t];
-                ws.ml[((size_t)part * T * H + at) * 2 + 1] = lr;
-            }
-        } else {
-            const float inv = 1.f / lr;
-            uint16_t* to = (uint16_t*)a.o + ((size_t)b * T * H + at) * D + 4 * lg;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-                gstore((uint2*)(to + 16 * i), make_uint2(pack_bf16x2(o[t][i][0] * inv, o[t][i][1] * inv),
-                                                         pack_bf16x2(o[t][i][2] * inv, o[t][i][3] * inv)));
+        for (int i = 0; i < D / 16; ++i) *(f32x4*)(to + 16 * i) = o[i];
+        if (lg == 0) {
+            ws.ml[((size_t)part * T * H + at) * 2] = m * c;
+            ws.ml[((size_t)part * T * H + at) * 2 + 1] = l;
         }
+    } else {
+        const float inv = 1.f / l;
+        uint16_t* to = (uint16_t*)a.o + ((size_t)b * T * H + at) * D + 4 * lg;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            gstore((uint2*)(to + 16 * i),
+                   make_uint2(pack_bf16x2(o[i][0] * inv, o[i][1] * inv), pack_bf16x2(o[i][2] * inv, o[i][3] * inv)));
     }
 }
 
@@ -642,9 +622,9 @@ void launch_nd(const AttnArgs& a, const AttnPlan& p, const AttnWorkspace& ws, in
     if (block_rows == 16)
         hipLaunchKernelGGL((attn_rows_kernel<ND, E4M3>), grid, dim3(256), 0, stream, a, p, ws);
     else if (block_rows == 64)
-        hipLaunchKernelGGL((attn_tiles_kernel<ND, E4M3, 1>), grid, dim3(256), lds, stream, a, p, ws, row_blocks);
+        hipLaunchKernelGGL((attn_tiles_kernel<ND, E4M3, 4>), grid, dim3(256), lds, stream, a, p, ws, row_blocks);
     else
-        hipLaunchKernelGGL((attn_tiles_kernel<ND, E4M3, 2>), grid, dim3(256), lds, stream, a, p, ws, row_blocks);
+        hipLaunchKernelGGL((attn_tiles_kernel<ND, E4M3, 8>), grid, dim3(512), lds, stream, a, p, ws, row_blocks);
 }
 
 }  // namespace

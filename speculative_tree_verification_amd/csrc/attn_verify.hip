@@ -202,45 +202,118 @@ __global__ __launch_bounds__(256) void attn_plain_kernel(AttnArgs a, AttnPlan pl
     }
 }
 
-// A wave joins one row's parts.
-template <typename TIO, int DV>
+// Lanes take 4 elements of a row each, so a wave reads PW = 64 / LPR parts at
+// once, four times that before it adds; the parts' maxima and sums are a lane's
+// each, 64 at a time, with a running maximum over them. Many rows go to a wave
+// each, RW one after another where that leaves enough work-groups (the search for
+// the item's parts costs as much as a row: 66 -> 37 us for the 63-node trees of
+// 32 items); of few rows (one new token over a long cache, 128 parts) each has a
+// work-group, whose waves split its parts (RW 0: 38 -> 10 us).
+template <typename TIO, int LPR, int RW>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnPlan plan, AttnWorkspace ws, int blocks) {
+    constexpr int PW = kWave / LPR;
+    constexpr bool SHARED = RW == 0;
     __shared__ __attribute__((aligned(8))) int s_red[6];
     __shared__ Part s_part;
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave;
+    __shared__ __attribute__((aligned(16))) float s_o[4][LPR * 4];
+    __shared__ float s_ml[4][2];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
     const Part pt = find_part<256>(a.cache_len, a.batch, a.room, plan, blockIdx.x / blocks, true, s_red, &s_part);
     if (pt.n < 2) return;
-    const int rows = a.T * a.H;
-    int st = 0;
-    for (int k = 0; k < pt.n; ++k) st |= ws.bits[pt.base + k];
-    const int rb = blockIdx.x % blocks;
-    if (rb == 0 && tid == 0 && a.status) a.status[pt.item] = st;
-    const int row = rb * 4 + w;
-    if (st || row >= rows) return;
-    const float* ml = ws.ml + ((size_t)pt.base * rows + row) * 2;
-    const float* po = ws.o + ((size_t)pt.base * rows + row) * a.D;
-    float m = -INFINITY;
-    for (int k = lane; k < pt.n; k += kWave) m = fmaxf(m, ml[(size_t)k * rows * 2]);
-#pragma unroll
-    for (int x = 1; x < kWave; x <<= 1) m = fmaxf(m, __shfl_xor(m, x, kWave));
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[DV];
-#pragma unroll
-    for (int i = 0; i < DV; ++i) o[i] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < pt.n; ++k) {
-        const float al = exp2f(ml[(size_t)k * rows * 2] - base);
-        l += al * ml[(size_t)k * rows * 2 + 1];
-#pragma unroll
-        for (int i = 0; i < DV; ++i) {
-            const int d = lane + i * kWave;
-            if (d < a.D) o[i] = fmaf(al, po[(size_t)k * rows * a.D + d], o[i]);
-        }
+    const int rows = a.T * a.H, D = a.D, n = pt.n, rb = blockIdx.x % blocks;
+    int bits = 0;
+    for (int k = tid; k < n; k += 256) bits |= ws.bits[pt.base + k];
+    if (__syncthreads_or(bits)) {
+        int all = 0;
+        for (int bit = 1; bit <= kStBadCache; bit <<= 1) all |= __syncthreads_or(bits & bit) ? bit : 0;
+        if (rb == 0 && tid == 0 && a.status) a.status[pt.item] = all;
+        return;
     }
+    if (rb == 0 && tid == 0 && a.status) a.status[pt.item] = 0;
+    const int d = lane % LPR * 4, sub = lane / LPR;
+    const int per = SHARED ? (n + 3) / 4 : n, first = SHARED ? w * per : 0, end = min(n, first + per);
+    for (int i = 0; i < (SHARED ? 1 : RW); ++i) {
+        const int row = SHARED ? rb : (rb * 4 + w) * RW + i;
+        if (row >= rows) return;  // the same for all threads where they share
+        const float* ml = ws.ml + ((size_t)pt.base * rows + row) * 2;
+        const float* po = ws.o + ((size_t)pt.base * rows + row) * D + d;
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c0 = first; c0 < end; c0 += kWave) {
+            const int cnt = min(kWave, end - c0);
+            float mk = -INFINITY, lk = 0.f;
+            if (lane < cnt) {
+                mk = ml[(size_t)(c0 + lane) * rows * 2];
+                lk = ml[(size_t)(c0 + lane) * rows * 2 + 1];
+            }
+            float top = mk;
 #pragma unroll
-    for (int i = 0; i < DV; ++i) {
-        const int d = lane + i * kWave;
-        if (d < a.D) Elem<TIO>::st((TIO*)a.o, ((size_t)pt.item * rows + row) * a.D + d, o[i] / l);
+            for (int x = 1; x < kWave; x <<= 1) top = fmaxf(top, __shfl_xor(top, x, kWave));
+            const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn, old = exp2f(m - base);
+            const float al = exp2f(mk - base);
+            float sum = al * lk;
+#pragma unroll
+            for (int x = 1; x < kWave; x <<= 1) sum += __shfl_xor(sum, x, kWave);
+            l = l * old + sum;
+            o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+            m = mn;
+            for (int k0 = 0; k0 < cnt; k0 += 4 * PW) {
+                float4 v[4];
+                float f[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int k = k0 + u * PW + sub;
+                    v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k < cnt && d < D) v[u] = ld4<false>(po + (size_t)(c0 + k) * rows * D, D - d);
+                    f[u] = __shfl(al, min(k, kWave - 1), kWave);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (k0 + u * PW + sub >= cnt) continue;
+                    o.x = fmaf(f[u], v[u].x, o.x);
+                    o.y = fmaf(f[u], v[u].y, o.y);
+                    o.z = fmaf(f[u], v[u].z, o.z);
+                    o.w = fmaf(f[u], v[u].w, o.w);
+                }
+            }
+        }
+#pragma unroll
+        for (int x = LPR; x < kWave; x <<= 1) {
+            o.x += __shfl_xor(o.x, x, kWave);
+            o.y += __shfl_xor(o.y, x, kWave);
+            o.z += __shfl_xor(o.z, x, kWave);
+            o.w += __shfl_xor(o.w, x, kWave);
+        }
+        if (SHARED) {
+            if (sub == 0) *(float4*)&s_o[w][d] = o;
+            if (lane == 0) {
+                s_ml[w][0] = m;
+                s_ml[w][1] = l;
+            }
+            __syncthreads();
+            if (w != 0) return;
+            const float mt = fmaxf(fmaxf(s_ml[0][0], s_ml[1][0]), fmaxf(s_ml[2][0], s_ml[3][0]));
+            const float base = mt == -INFINITY ? 0.f : mt;
+            l = 0.f;
+            o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float4 t = *(const float4*)&s_o[x][d];
+                const float f = exp2f(s_ml[x][0] - base);
+                l = fmaf(f, s_ml[x][1], l);
+                o.x = fmaf(f, t.x, o.x);
+                o.y = fmaf(f, t.y, o.y);
+                o.z = fmaf(f, t.z, o.z);
+                o.w = fmaf(f, t.w, o.w);
+            }
+        }
+        if (sub == 0) {
+            const float f[4] = {o.x / l, o.y / l, o.z / l, o.w / l};
+            TIO* to = (TIO*)a.o + ((size_t)pt.item * rows + row) * D + d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (d + e < D) Elem<TIO>::st(to, e, f[e]);
+        }
     }
 }
 
@@ -255,16 +328,29 @@ void launch_plain(const AttnArgs& a, const AttnPlan& p, const AttnWorkspace& ws,
         hipLaunchKernelGGL((attn_plain_kernel<TIO, TC, 4>), grid, dim3(256), 0, stream, a, p, ws, row_blocks);
 }
 
+template <typename TIO, int LPR>
+void launch_join_lpr(const AttnArgs& a, const AttnPlan& p, const AttnWorkspace& ws, hipStream_t stream) {
+    const int rows = a.T * a.H;
+    const long long all = (long long)a.batch * rows;
+    const int rw = all <= kAttnWant ? 0 : all <= 16 * kAttnWant ? 1 : 4;
+    const int blocks = rw == 0 ? rows : (rows + 4 * rw - 1) / (4 * rw);
+    const dim3 grid((unsigned)((long long)a.batch * blocks));
+    if (rw == 0)
+        hipLaunchKernelGGL((attn_join_kernel<TIO, LPR, 0>), grid, dim3(256), 0, stream, a, p, ws, blocks);
+    else if (rw == 1)
+        hipLaunchKernelGGL((attn_join_kernel<TIO, LPR, 1>), grid, dim3(256), 0, stream, a, p, ws, blocks);
+    else
+        hipLaunchKernelGGL((attn_join_kernel<TIO, LPR, 4>), grid, dim3(256), 0, stream, a, p, ws, blocks);
+}
+
 template <typename TIO>
 void launch_join(const AttnArgs& a, const AttnPlan& p, const AttnWorkspace& ws, hipStream_t stream) {
-    const int blocks = (a.T * a.H + 3) / 4;
-    const dim3 grid((unsigned)((long long)a.batch * blocks));
     if (a.D <= 64)
-        hipLaunchKernelGGL((attn_join_kernel<TIO, 1>), grid, dim3(256), 0, stream, a, p, ws, blocks);
+        launch_join_lpr<TIO, 16>(a, p, ws, stream);
     else if (a.D <= 128)
-        hipLaunchKernelGGL((attn_join_kernel<TIO, 2>), grid, dim3(256), 0, stream, a, p, ws, blocks);
+        launch_join_lpr<TIO, 32>(a, p, ws, stream);
     else
-        hipLaunchKernelGGL((attn_join_kernel<TIO, 4>), grid, dim3(256), 0, stream, a, p, ws, blocks);
+        launch_join_lpr<TIO, 64>(a, p, ws, stream);
 }
 
 // Whether the bf16 kernels take the shape: 32-bit row numbers into the pool, and
@@ -304,7 +390,7 @@ uint64_t attn_verify_workspace_bytes(const tsv_attn_shape* s) {
 }
 
 long long attn_verify_blocks(const tsv_attn_shape* s) {
-    long long most = (long long)s->batch * (((long long)s->n_nodes * s->n_heads + 3) / 4);  // the join
+    long long most = (long long)s->batch * (((long long)s->n_nodes * s->n_heads + 15) / 16);  // the join
     for (int matrix = 0; matrix <= (int)matrix_shape(s); ++matrix) {
         int br, rb;
         const AttnPlan p = plan_of(s, matrix, &br, &rb);
