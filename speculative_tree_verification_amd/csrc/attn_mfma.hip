@@ -24,14 +24,34 @@ namespace {
 constexpr int kStepKeys = 32;  // keys of a wave's step in the row kernel
 constexpr int kTileKeys = 64;  // keys of a shared tile in the tile kernel
 
-// Largest of / sum over the four lanes that hold a row's keys
+// max of three, as the instruction: fmaxf first makes each product's result quiet
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+// Largest of / sum over the four lanes (16 apart) that hold a row's keys: halves
+// and rows of 16 lanes change places with a copy of themselves
+struct Two {
+    float a, b;
+};
+__device__ __forceinline__ Two swap32(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return {__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+__device__ __forceinline__ Two swap16(float v) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return {__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
 __device__ __forceinline__ float row_max(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16, kWave));
-    return fmaxf(v, __shfl_xor(v, 32, kWave));
+    const Two h = swap32(v);
+    const Two q = swap16(fmaxf(h.a, h.b));
+    return fmaxf(q.a, q.b);
 }
 __device__ __forceinline__ float row_sum(float v) {
-    v += __shfl_xor(v, 16, kWave);
-    return v + __shfl_xor(v, 32, kWave);
+    const Two h = swap32(v);
+    const Two q = swap16(h.a + h.b);
+    return q.a + q.b;
 }
 
 // Row index of position `pos` of an item in the cache's arrays, or -1 for a page
@@ -136,10 +156,9 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
     // softmax and product of 32 keys: s the raw scores (masked: -inf), vs the factor
     // of each value row; V in this wave's LDS
     auto take = [&](const f32x4* s, const f32x4* vs) {
-        float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                          fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-        top = row_max(top);
-        const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn * c;
+        const float mn = max3(row_max(max3(max3(s[0][0], s[0][1], s[0][2]), max3(s[0][3], s[1][0], s[1][1]),
+                                           max3(s[1][2], s[1][3], s[1][3]))), m, m);
+        const float base = mn == -INFINITY ? 0.f : mn * c;
         if (__ballot(mn > m)) {  // some row's maximum moved
             const float al = __builtin_amdgcn_exp2f(fmaf(m, c, -base));
             l *= al;
@@ -156,7 +175,7 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
         l += sum;  // of this lane's keys; the four lanes of a row meet at the end
         if (E4M3 && vs) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = p[e] == 0.f ? 0.f : p[e] * vs[e / 4][e % 4];
+            for (int e = 0; e < 8; ++e) p[e] *= vs[e / 4][e % 4];  // a key past the last one has the last one's
         }
         const bf16x8 pf = as_operand(make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]),
                                                 pack_bf16x2(p[6], p[7])));
@@ -406,11 +425,10 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // One tile of keys in LDS: scores, softmax, product. MASK: 0 all keys count,
-    // 1 those below `limit`, 2 the tree's (keys j0 + ..., by ancestors)
-    auto take = [&](auto mask, auto scaled, int limit, int j0) {
-        constexpr int MASK = decltype(mask)::value;
-        constexpr bool SCALED = decltype(scaled)::value;
+    // One tile of keys in LDS, `limit` of them: scores, softmax, product. TREE: keys
+    // j0 + ... of the tree, by ancestors
+    auto take = [&](auto tree, int limit, int j0) {
+        constexpr bool TREE = decltype(tree)::value, SCALED = E4M3 && !TREE;
         f32x4 s[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[x] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -419,27 +437,30 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
         for (int i = 0; i < ND; ++i) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) s[x] = mma(*(const bf16x8*)&s_K[(16 * x + l16) * kKs + 32 * i + 8 * lg], q[i], s[x]);
-            __builtin_amdgcn_sched_barrier(0);
+            if (i % 2) __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             if (SCALED) s[x] *= *(const f32x4*)&s_ks[16 * x + 4 * lg];
-            if (MASK) {
+            if (TREE) {
                 const int j = 16 * x + 4 * lg;
-                uint32_t bits = 0;
-                if (MASK == 2) bits = s_anc[(node - first) * words + min((j0 + j) / 32, words - 1)] >> ((j0 + j) % 32);
+                const uint32_t bits = s_anc[(node - first) * words + min((j0 + j) / 32, words - 1)] >> ((j0 + j) % 32);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const bool seen = j + r < limit && (MASK == 1 || (bits >> r & 1));
-                    s[x][r] = seen ? s[x][r] : -INFINITY;
-                }
+                for (int r = 0; r < 4; ++r) s[x][r] = j + r < limit && (bits >> r & 1) ? s[x][r] : -INFINITY;
             }
         }
-        float top = -INFINITY;
+        if (!TREE && limit < kTileKeys) {
+            const int left = limit - 4 * lg;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) top = fmaxf(top, fmaxf(fmaxf(s[x][0], s[x][1]), fmaxf(s[x][2], s[x][3])));
-        top = row_max(top);
-        const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn * c;
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s[x][r] = 16 * x + r < left ? s[x][r] : -INFINITY;
+        }
+        const float mn = max3(row_max(max3(max3(max3(s[0][0], s[0][1], s[0][2]), s[0][3], s[1][0]),
+                                           max3(max3(s[1][1], s[1][2], s[1][3]), s[2][0], s[2][1]),
+                                           max3(max3(s[2][2], s[2][3], s[3][0]), max3(s[3][1], s[3][2], s[3][3]), s[3][3]))),
+                              m, m);
+        const float base = mn == -INFINITY ? 0.f : mn * c;
         if (__ballot(mn > m)) {  // some row's maximum moved
             const float al = __builtin_amdgcn_exp2f(fmaf(m, c, -base));
             l *= al;
@@ -459,7 +480,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
             if (SCALED) {
                 const f32x4 vs = *(const f32x4*)&s_vs[16 * x + 4 * lg];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) p[r] = MASK && p[r] == 0.f ? 0.f : p[r] * vs[r];
+                for (int r = 0; r < 4; ++r) p[r] *= vs[r];  // a key past the last one has the last one's
             }
             u[2 * x] = pack_bf16x2(p[0], p[1]);
             u[2 * x + 1] = pack_bf16x2(p[2], p[3]);
@@ -544,10 +565,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
                 request(set ^ 1);
                 look_up(t + 2 * kTileKeys);
             }
-            if (t + kTileKeys <= k1)
-                take(std::integral_constant<int, 0>(), std::integral_constant<bool, E4M3>(), 0, 0);
-            else
-                take(std::integral_constant<int, 1>(), std::integral_constant<bool, E4M3>(), k1 - t, 0);
+            take(std::false_type(), min(kTileKeys, k1 - t), 0);
         }
     } else if (k1 > k0) {
         bad = 1;  // positions without a page
@@ -574,7 +592,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
                 *(uint4*)&s_V[key * kVs + c] = vu;
             }
             __syncthreads();
-            take(std::integral_constant<int, 2>(), std::false_type(), T - j0, j0);
+            take(std::true_type(), T - j0, j0);
         }
         for (int x = 0; x < words; ++x) {
             if (!s_odd[x]) continue;
