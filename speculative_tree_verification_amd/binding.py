@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import Dict, Optional
 
@@ -895,61 +896,75 @@ class PreparedSnapshot:
 
 
 # ---- sequences around the tree, and the paged cache of attention layers
-class _Launch:
-    """What one call needs of torch: the tensors' device made current (the
-    library launches on the current device), and the stream, also as the one
-    that buffers made here belong to."""
-
-    def __init__(self, dev, stream):
-        if dev.type != "cuda":
-            raise ValueError(f"tensors must be on a GPU, got {dev}")
-        self.device = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
-        if stream is None:
-            self.stream, self.alloc = torch.cuda.current_stream(dev), None
-        else:
-            self.stream, self.alloc = stream, _on_stream(stream)
-
-    def __enter__(self):
-        if self.device is not None:
-            self.device.__enter__()
-        if self.alloc is not None:
-            self.alloc.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.alloc is not None:
-            self.alloc.__exit__(*exc)
-        if self.device is not None:
-            self.device.__exit__(*exc)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
-def _workspace(query, shape, given, dev):
-    """(tensor or None, bytes) of at least what ``query`` says, made here if not given."""
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _need(t, name: str, shape, dtype, dev):
+    """_check with its common case first: these calls run once per layer and token."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or t.device != dev \
+            or not t.is_contiguous():
+        _check(t, name, shape, dtype, dev)
+
+
+def _launch(dev, stream, body):
+    """body(raw stream) with the tensors' device current (the library launches
+    on the current device) and, for a given stream, torch's current stream
+    being that one, so that the buffers that body makes belong to it."""
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {dev}")
+    if stream is None:
+        if dev.index == _current_device():
+            return body(_raw_stream(dev.index))
+        with torch.cuda.device(dev):
+            return body(_raw_stream(dev.index))
+    with torch.cuda.device(dev), _on_stream(stream):
+        return body(stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream))
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=4096)
+def _seq_workspace(*fields) -> int:
     need = ctypes.c_uint64()
-    rc = query(ctypes.byref(shape), ctypes.byref(need))
+    rc = lib.tree_ssd_prefill_workspace(ctypes.byref(SeqShape(*fields)), ctypes.byref(need))
     if rc != 0:
-        raise TreeSSDError(rc, query.__name__)
+        raise TreeSSDError(rc, "tree_ssd_prefill_workspace")
+    return need.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _attn_workspace(*fields) -> int:
+    need = ctypes.c_uint64()
+    rc = lib.tree_attn_verify_workspace(ctypes.byref(AttnShape(*fields)), ctypes.byref(need))
+    if rc != 0:
+        raise TreeSSDError(rc, "tree_attn_verify_workspace")
+    return need.value
+
+
+def _workspace(need: int, given, dev):
+    """(tensor or None, bytes): what the caller gave, or one made here."""
     if given is not None:
         if given.device != dev or not given.is_contiguous():
             raise ValueError("workspace must be contiguous and on the tensors' device")
         size = given.numel() * given.element_size()
-        if size < need.value:
-            raise ValueError(f"workspace has {size} bytes, {need.value} are needed")
+        if size < need:
+            raise ValueError(f"workspace has {size} bytes, {need} are needed")
         return given, size
-    if need.value == 0:
+    if need == 0:
         return None, 0
-    return torch.empty(need.value, dtype=torch.uint8, device=dev), need.value
+    return torch.empty(need, dtype=torch.uint8, device=dev), need
 
 
 def prefill_workspace_bytes(n_seqs, n_tokens, n_heads, head_dim, d_state, n_groups=1, dtype=torch.bfloat16) -> int:
     """Bytes of workspace a ``prefill`` of these sizes needs."""
-    shape = SeqShape(n_seqs, n_tokens, n_heads, head_dim, d_state, n_groups,
-                     TSV_BF16 if dtype == torch.bfloat16 else TSV_F32, 0)
-    need = ctypes.c_uint64()
-    rc = lib.tree_ssd_prefill_workspace(ctypes.byref(shape), ctypes.byref(need))
-    if rc != 0:
-        raise TreeSSDError(rc, "tree_ssd_prefill_workspace")
-    return need.value
+    return _seq_workspace(n_seqs, n_tokens, n_heads, head_dim, d_state, n_groups,
+                          TSV_BF16 if dtype == torch.bfloat16 else TSV_F32, 0)
 
 
 def prefill(x, dt, A, B, C, D, h, seq_start, y=None, seq_status=None, workspace=None, stream=None,
@@ -960,83 +975,88 @@ def prefill(x, dt, A, B, C, D, h, seq_start, y=None, seq_status=None, workspace=
     ``prefill_workspace_bytes``) is made here if not given; calls that may
     overlap need one each."""
     L, H, P = x.shape
-    G, N = B.shape[1], B.shape[2]
+    _, G, N = B.shape
     n, dev, io = h.shape[0], x.device, x.dtype
-    _check(x, "x", (L, H, P), io, dev)
-    _check(dt, "dt", (L, H), io, dev)
-    _check(A, "A", (H,), torch.float32, dev)
-    _check(B, "B", (L, G, N), io, dev)
-    _check(C, "C", (L, G, N), io, dev)
-    _check(D, "D", (H,), torch.float32, dev)
-    _check(h, "h", (n, H, P, N), torch.float32, dev)
-    _check(seq_start, "seq_start", (n + 1,), torch.int32, dev)
+    _need(x, "x", (L, H, P), io, dev)
+    _need(dt, "dt", (L, H), io, dev)
+    _need(A, "A", (H,), torch.float32, dev)
+    _need(B, "B", (L, G, N), io, dev)
+    _need(C, "C", (L, G, N), io, dev)
+    _need(D, "D", (H,), torch.float32, dev)
+    _need(h, "h", (n, H, P, N), torch.float32, dev)
+    _need(seq_start, "seq_start", (n + 1,), torch.int32, dev)
     if seq_status is not None:
-        _check(seq_status, "seq_status", (n,), torch.int32, dev)
-    shape = SeqShape(n, L, H, P, N, G, _dtype_code(x), TSV_FLAG_FORCE_GENERIC if force_generic else 0)
-    with _Launch(dev, stream) as s:
-        if y is None:
-            y = torch.empty_like(x)
-        else:
-            _check(y, "y", (L, H, P), io, dev)
-        ws, size = _workspace(lib.tree_ssd_prefill_workspace, shape, workspace, dev)
-        rc = lib.tree_ssd_prefill(ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(h),
-                                  _ptr(seq_start), _ptr(y), _ptr(seq_status), _ptr(ws) if ws is not None else None,
-                                  size, s)
-    if rc != 0:
-        raise TreeSSDError(rc, "tree_ssd_prefill")
-    return y
+        _need(seq_status, "seq_status", (n,), torch.int32, dev)
+    if y is not None:
+        _need(y, "y", (L, H, P), io, dev)
+    fields = (n, L, H, P, N, G, _dtype_code(x), TSV_FLAG_FORCE_GENERIC if force_generic else 0)
+
+    def body(s):
+        out = torch.empty_like(x) if y is None else y
+        ws, size = _workspace(_seq_workspace(*fields), workspace, dev)
+        rc = lib.tree_ssd_prefill(SeqShape(*fields), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(),
+                                  C.data_ptr(), D.data_ptr(), h.data_ptr(), seq_start.data_ptr(), out.data_ptr(),
+                                  _opt(seq_status), _opt(ws), size, s)
+        if rc != 0:
+            raise TreeSSDError(rc, "tree_ssd_prefill")
+        return out
+
+    return _launch(dev, stream, body)
 
 
 def step(x, dt, A, B, C, D, h, y=None, stream=None):
     """y [Bt,H,P] of one token of each item, and h [Bt,H,P,N] advanced by it in
     place (tree_ssd_step): x [Bt,H,P], dt [Bt,H], B, C [Bt,G,N]."""
     Bt, H, P = x.shape
-    G, N = B.shape[1], B.shape[2]
+    _, G, N = B.shape
     dev, io = x.device, x.dtype
-    _check(x, "x", (Bt, H, P), io, dev)
-    _check(dt, "dt", (Bt, H), io, dev)
-    _check(A, "A", (H,), torch.float32, dev)
-    _check(B, "B", (Bt, G, N), io, dev)
-    _check(C, "C", (Bt, G, N), io, dev)
-    _check(D, "D", (H,), torch.float32, dev)
-    _check(h, "h", (Bt, H, P, N), torch.float32, dev)
-    shape = Shape(Bt, 1, H, P, N, G, _dtype_code(x), 0, 0)
-    with _Launch(dev, stream) as s:
-        if y is None:
-            y = torch.empty_like(x)
-        else:
-            _check(y, "y", (Bt, H, P), io, dev)
-        rc = lib.tree_ssd_step(ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(h),
-                               _ptr(y), s)
-    if rc != 0:
-        raise TreeSSDError(rc, "tree_ssd_step")
-    return y
+    _need(x, "x", (Bt, H, P), io, dev)
+    _need(dt, "dt", (Bt, H), io, dev)
+    _need(A, "A", (H,), torch.float32, dev)
+    _need(B, "B", (Bt, G, N), io, dev)
+    _need(C, "C", (Bt, G, N), io, dev)
+    _need(D, "D", (H,), torch.float32, dev)
+    _need(h, "h", (Bt, H, P, N), torch.float32, dev)
+    if y is not None:
+        _need(y, "y", (Bt, H, P), io, dev)
+    code = _dtype_code(x)
+
+    def body(s):
+        out = torch.empty_like(x) if y is None else y
+        rc = lib.tree_ssd_step(Shape(Bt, 1, H, P, N, G, code, 0, 0), x.data_ptr(), dt.data_ptr(), A.data_ptr(),
+                               B.data_ptr(), C.data_ptr(), D.data_ptr(), h.data_ptr(), out.data_ptr(), s)
+        if rc != 0:
+            raise TreeSSDError(rc, "tree_ssd_step")
+        return out
+
+    return _launch(dev, stream, body)
 
 
-def _attn_shape(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, batch, rows, n_heads, scale,
-                force_generic) -> AttnShape:
-    """Checks what every attention call has of the cache, and fills tsv_attn_shape."""
-    dev = k.device
+def _attn_fields(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, batch, rows, n_heads, scale,
+                 force_generic):
+    """Checks what every attention call has of the cache: the fields of tsv_attn_shape."""
+    dev, ct = k.device, k_cache.dtype
     n_pages, Hk, page_size, D = k_cache.shape
     if k.shape[-2:] != (Hk, D):
         raise ValueError(f"k: heads and head_dim {tuple(k.shape[-2:])} != the cache's {(Hk, D)}")
-    e4m3 = k_cache.dtype == torch.float8_e4m3fn
-    if not e4m3 and k_cache.dtype != k.dtype:
-        raise TypeError(f"k_cache: dtype {k_cache.dtype} is neither {k.dtype} nor torch.float8_e4m3fn")
-    _check(k_cache, "k_cache", (n_pages, Hk, page_size, D), k_cache.dtype, dev)
-    _check(v_cache, "v_cache", (n_pages, Hk, page_size, D), k_cache.dtype, dev)
+    e4m3 = ct is torch.float8_e4m3fn
+    if not e4m3 and ct is not k.dtype:
+        raise TypeError(f"k_cache: dtype {ct} is neither {k.dtype} nor torch.float8_e4m3fn")
+    _need(k_cache, "k_cache", (n_pages, Hk, page_size, D), ct, dev)
+    _need(v_cache, "v_cache", (n_pages, Hk, page_size, D), ct, dev)
     for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
         if e4m3:
             if t is None:
                 raise ValueError(f"{name} is needed with an e4m3 cache")
-            _check(t, name, (n_pages, Hk, page_size), torch.float32, dev)
+            _need(t, name, (n_pages, Hk, page_size), torch.float32, dev)
         elif t is not None:
             raise ValueError(f"{name} goes with an e4m3 cache only")
-    _check(page_table, "page_table", (batch, page_table.shape[1]), torch.int32, dev)
-    _check(cache_len, "cache_len", (batch,), torch.int32, dev)
+    most = page_table.shape[1]
+    _need(page_table, "page_table", (batch, most), torch.int32, dev)
+    _need(cache_len, "cache_len", (batch,), torch.int32, dev)
     io = _dtype_code(k)
-    return AttnShape(batch, rows, n_heads, Hk, D, n_pages, page_size, page_table.shape[1], io,
-                     TSV_E4M3 if e4m3 else io, TSV_FLAG_FORCE_GENERIC if force_generic else 0, scale)
+    return (batch, rows, n_heads, Hk, D, n_pages, page_size, most, io, TSV_E4M3 if e4m3 else io,
+            TSV_FLAG_FORCE_GENERIC if force_generic else 0, scale)
 
 
 def attn_verify(q, k, v, parent, k_cache, v_cache, page_table, cache_len, k_scale=None, v_scale=None,
@@ -1048,41 +1068,38 @@ def attn_verify(q, k, v, parent, k_cache, v_cache, page_table, cache_len, k_scal
     v_scale [n_pages,Hk,page_size]. ``scale`` defaults to D**-0.5. One node per
     item is plain decoding."""
     Bt, T, H, D = q.shape
-    dev, io = q.device, q.dtype
-    Hk = k.shape[2]
-    _check(q, "q", (Bt, T, H, D), io, dev)
-    _check(k, "k", (Bt, T, Hk, D), io, dev)
-    _check(v, "v", (Bt, T, Hk, D), io, dev)
-    _check(parent, "parent", (Bt, T), torch.int32, dev)
+    dev, io, Hk = q.device, q.dtype, k.shape[2]
+    _need(q, "q", (Bt, T, H, D), io, dev)
+    _need(k, "k", (Bt, T, Hk, D), io, dev)
+    _need(v, "v", (Bt, T, Hk, D), io, dev)
+    _need(parent, "parent", (Bt, T), torch.int32, dev)
     if tree_status is not None:
-        _check(tree_status, "tree_status", (Bt,), torch.int32, dev)
-    shape = _attn_shape(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, T, H,
-                        D ** -0.5 if scale is None else float(scale), force_generic)
-    with _Launch(dev, stream) as s:
-        if o is None:
-            o = torch.empty_like(q)
-        else:
-            _check(o, "o", (Bt, T, H, D), io, dev)
-        ws, size = _workspace(lib.tree_attn_verify_workspace, shape, workspace, dev)
-        rc = lib.tree_attn_verify(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(parent), _ptr(k_cache),
-                                  _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(cache_len),
-                                  _ptr(o), _ptr(tree_status), _ptr(ws) if ws is not None else None, size, s)
-    if rc != 0:
-        raise TreeSSDError(rc, "tree_attn_verify")
-    return o
+        _need(tree_status, "tree_status", (Bt,), torch.int32, dev)
+    if o is not None:
+        _need(o, "o", (Bt, T, H, D), io, dev)
+    fields = _attn_fields(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, T, H,
+                          D ** -0.5 if scale is None else float(scale), force_generic)
+
+    def body(s):
+        out = torch.empty_like(q) if o is None else o
+        ws, size = _workspace(_attn_workspace(*fields), workspace, dev)
+        rc = lib.tree_attn_verify(AttnShape(*fields), q.data_ptr(), k.data_ptr(), v.data_ptr(), parent.data_ptr(),
+                                  k_cache.data_ptr(), v_cache.data_ptr(), _opt(k_scale), _opt(v_scale),
+                                  page_table.data_ptr(), cache_len.data_ptr(), out.data_ptr(), _opt(tree_status),
+                                  _opt(ws), size, s)
+        if rc != 0:
+            raise TreeSSDError(rc, "tree_attn_verify")
+        return out
+
+    return _launch(dev, stream, body)
 
 
 def attn_verify_workspace_bytes(batch, n_nodes, n_heads, n_kv_heads, head_dim, page_size, max_pages,
-                                dtype=torch.bfloat16, cache_dtype=None) -> int:
+                                dtype=torch.bfloat16, cache_dtype=None, n_pages: int = 1) -> int:
     """Bytes of workspace an ``attn_verify`` of these sizes needs."""
     io = TSV_BF16 if dtype == torch.bfloat16 else TSV_F32
-    shape = AttnShape(batch, n_nodes, n_heads, n_kv_heads, head_dim, 1, page_size, max_pages, io,
-                      TSV_E4M3 if cache_dtype == torch.float8_e4m3fn else io, 0, 1.0)
-    need = ctypes.c_uint64()
-    rc = lib.tree_attn_verify_workspace(ctypes.byref(shape), ctypes.byref(need))
-    if rc != 0:
-        raise TreeSSDError(rc, "tree_attn_verify_workspace")
-    return need.value
+    return _attn_workspace(batch, n_nodes, n_heads, n_kv_heads, head_dim, n_pages, page_size, max_pages, io,
+                           TSV_E4M3 if cache_dtype == torch.float8_e4m3fn else io, 0, 1.0)
 
 
 def attn_commit(k, v, parent, accepted, accepted_len, k_cache, v_cache, page_table, cache_len, k_scale=None,
@@ -1092,20 +1109,24 @@ def attn_commit(k, v, parent, accepted, accepted_len, k_cache, v_cache, page_tab
     Bt, T, Hk, D = k.shape
     dev, io = k.device, k.dtype
     Lmax = accepted.shape[1]
-    _check(k, "k", (Bt, T, Hk, D), io, dev)
-    _check(v, "v", (Bt, T, Hk, D), io, dev)
-    _check(parent, "parent", (Bt, T), torch.int32, dev)
-    _check(accepted, "accepted", (Bt, Lmax), torch.int32, dev)
-    _check(accepted_len, "accepted_len", (Bt,), torch.int32, dev)
+    _need(k, "k", (Bt, T, Hk, D), io, dev)
+    _need(v, "v", (Bt, T, Hk, D), io, dev)
+    _need(parent, "parent", (Bt, T), torch.int32, dev)
+    _need(accepted, "accepted", (Bt, Lmax), torch.int32, dev)
+    _need(accepted_len, "accepted_len", (Bt,), torch.int32, dev)
     if tree_status is not None:
-        _check(tree_status, "tree_status", (Bt,), torch.int32, dev)
-    shape = _attn_shape(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, T, Hk, 1.0, False)
-    with _Launch(dev, stream) as s:
-        rc = lib.tree_attn_commit(ctypes.byref(shape), _ptr(k), _ptr(v), _ptr(parent), _ptr(accepted),
-                                  _ptr(accepted_len), int(Lmax), _ptr(page_table), _ptr(cache_len), _ptr(k_cache),
-                                  _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(tree_status), s)
-    if rc != 0:
-        raise TreeSSDError(rc, "tree_attn_commit")
+        _need(tree_status, "tree_status", (Bt,), torch.int32, dev)
+    fields = _attn_fields(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, T, Hk, 1.0, False)
+
+    def body(s):
+        rc = lib.tree_attn_commit(AttnShape(*fields), k.data_ptr(), v.data_ptr(), parent.data_ptr(),
+                                  accepted.data_ptr(), accepted_len.data_ptr(), Lmax, page_table.data_ptr(),
+                                  cache_len.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _opt(k_scale),
+                                  _opt(v_scale), _opt(tree_status), s)
+        if rc != 0:
+            raise TreeSSDError(rc, "tree_attn_commit")
+
+    _launch(dev, stream, body)
 
 
 def attn_append(k, v, seq_start, k_cache, v_cache, page_table, cache_len, k_scale=None, v_scale=None,
@@ -1116,15 +1137,18 @@ def attn_append(k, v, seq_start, k_cache, v_cache, page_table, cache_len, k_scal
     L, Hk, D = k.shape
     dev, io = k.device, k.dtype
     Bt = cache_len.shape[0]
-    _check(k, "k", (L, Hk, D), io, dev)
-    _check(v, "v", (L, Hk, D), io, dev)
-    _check(seq_start, "seq_start", (Bt + 1,), torch.int32, dev)
+    _need(k, "k", (L, Hk, D), io, dev)
+    _need(v, "v", (L, Hk, D), io, dev)
+    _need(seq_start, "seq_start", (Bt + 1,), torch.int32, dev)
     if seq_status is not None:
-        _check(seq_status, "seq_status", (Bt,), torch.int32, dev)
-    shape = _attn_shape(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, L, Hk, 1.0, False)
-    with _Launch(dev, stream) as s:
-        rc = lib.tree_attn_append(ctypes.byref(shape), _ptr(k), _ptr(v), _ptr(seq_start), _ptr(page_table),
-                                  _ptr(cache_len), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                  _ptr(seq_status), s)
-    if rc != 0:
-        raise TreeSSDError(rc, "tree_attn_append")
+        _need(seq_status, "seq_status", (Bt,), torch.int32, dev)
+    fields = _attn_fields(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, L, Hk, 1.0, False)
+
+    def body(s):
+        rc = lib.tree_attn_append(AttnShape(*fields), k.data_ptr(), v.data_ptr(), seq_start.data_ptr(),
+                                  page_table.data_ptr(), cache_len.data_ptr(), k_cache.data_ptr(),
+                                  v_cache.data_ptr(), _opt(k_scale), _opt(v_scale), _opt(seq_status), s)
+        if rc != 0:
+            raise TreeSSDError(rc, "tree_attn_append")
+
+    _launch(dev, stream, body)

@@ -142,7 +142,7 @@ tsv_status tree_attn_commit(const tsv_attn_shape* s, const void* k, const void* 
     tsv_status st = check_attn(s, true);
     if (st != TSV_OK) return st;
     if (max_path_len < 0 || max_path_len > kMaxTree) return TSV_E_SHAPE;
-    if ((long long)s->batch * (kMaxTree / 16) > kMaxBlocks) return TSV_E_UNSUPPORTED;
+    if ((long long)s->batch * (kMaxTree / 2) > kMaxBlocks) return TSV_E_UNSUPPORTED;
     if (s->batch == 0 || s->n_nodes == 0) return TSV_OK;
     if (!k || !v || !parent || !accepted_len || !cache_len) return TSV_E_NULL;
     if (max_path_len > 0 && !accepted) return TSV_E_NULL;

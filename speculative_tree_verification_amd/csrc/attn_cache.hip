@@ -104,57 +104,70 @@ __device__ __forceinline__ int check_pages(const CacheWriteArgs& a, int b, int c
     return __syncthreads_or(bad) ? kStBadCache : 0;
 }
 
-// Rows r0 .. r0 + n - 1 (at most kRows) with their source rows and destination
-// sequences and positions in LDS (position -1: not written): all heads, keys
-// and values.
-constexpr int kRows = 16;
+// Row of head 0 in the cache's arrays for position `pos` of item b (its page is checked)
+__device__ __forceinline__ long long cache_place(const CacheWriteArgs& a, int b, int pos) {
+    const int page = page_of(pos, a.div), pg = a.page_table[(size_t)b * a.max_pages + page];
+    return (long long)pg * a.Hk * a.page_size + (pos - page * a.page_size);
+}
+
+// n rows, keys and values of all heads: source rows s_src, places s_dst (-1: not
+// written). A thread has its pieces of four rows of a head under way at once.
+constexpr int kAtOnce = 4;
 template <typename TIO, int LPR, bool E4M3, bool VEC>
-__device__ __forceinline__ void write_rows(const CacheWriteArgs& a, int n, const long long* s_src, const int* s_item,
-                                           const int* s_pos) {
+__device__ __forceinline__ void write_rows(const CacheWriteArgs& a, int n, const long long* s_src, const long long* s_dst) {
     const int lane = threadIdx.x % LPR, d = lane * 8, rem = a.D - d;
     const int per = 256 / LPR, work = n * a.Hk * 2;
-    for (int u0 = 0; u0 < work; u0 += per) {
-        const int u = u0 + threadIdx.x / LPR;  // row, k or v, head: heads fastest
-        const bool in = u < work;
-        const int row = in ? u / (2 * a.Hk) : 0, hv = in ? u % (2 * a.Hk) : 0;
-        const bool value = hv >= a.Hk;
-        const int hk = value ? hv - a.Hk : hv;
-        const int pos = in ? s_pos[row] : -1;
-        Quad q;
+    for (int u0 = threadIdx.x / LPR; u0 - (int)threadIdx.x / LPR < work; u0 += kAtOnce * per) {
+        Quad q[kAtOnce];
+        long long at[kAtOnce];
+        bool value[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q.v[i] = 0.f;
-        if (pos >= 0 && rem > 0)
-            q = load8<TIO, VEC>((const TIO*)(value ? a.v : a.k) + ((size_t)s_src[row] * a.Hk + hk) * a.D + d, rem);
-        float scale = 1.f;
-        bool finite = true;
-        if (E4M3) {
-            float top = 0.f;
-            int odd = 0;
+        for (int x = 0; x < kAtOnce; ++x) {
+            const int u = u0 + x * per;  // row, k or v, head: heads fastest
+            const bool in = u < work;
+            const int row = in ? u / (2 * a.Hk) : 0, hv = in ? u % (2 * a.Hk) : 0;
+            value[x] = hv >= a.Hk;
+            const int hk = value[x] ? hv - a.Hk : hv;
+            at[x] = in && rem > 0 ? s_dst[row] : -1;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                top = fmaxf(top, fabsf(q.v[i]));
-                odd |= !(fabsf(q.v[i]) <= 3.402823466e38f);  // an infinity or a NaN, which fmaxf passes over
+            for (int i = 0; i < 8; ++i) q[x].v[i] = 0.f;
+            if (at[x] >= 0) {
+                at[x] += (long long)hk * a.page_size;
+                q[x] = load8<TIO, VEC>((const TIO*)(value[x] ? a.v : a.k) + ((size_t)s_src[row] * a.Hk + hk) * a.D + d, rem);
             }
-#pragma unroll
-            for (int m = 1; m < LPR; m <<= 1) {
-                top = fmaxf(top, __shfl_xor(top, m, kWave));
-                odd |= __shfl_xor(odd, m, kWave);
-            }
-            finite = !odd;
-            scale = finite ? fmaxf(top / 448.f, 1.17549435e-38f) : __uint_as_float(0x7fc00000u);
         }
-        if (pos >= 0 && rem > 0) {
-            const int page = page_of(pos, a.div);
-            const int pg = a.page_table[(size_t)s_item[row] * a.max_pages + page];
-            const size_t at = ((size_t)pg * a.Hk + hk) * a.page_size + (pos - page * a.page_size);
-            store8<TIO, E4M3, VEC>(a, value, at, d, rem, q, scale, finite);
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x) {
+            float scale = 1.f;
+            bool finite = true;
+            if (E4M3) {
+                float top = 0.f;
+                int odd = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    top = fmaxf(top, fabsf(q[x].v[i]));
+                    odd |= !(fabsf(q[x].v[i]) <= 3.402823466e38f);  // an infinity or a NaN, which fmaxf passes over
+                }
+#pragma unroll
+                for (int m = 1; m < LPR; m <<= 1) {
+                    top = fmaxf(top, __shfl_xor(top, m, kWave));
+                    odd |= __shfl_xor(odd, m, kWave);
+                }
+                finite = !odd;
+                scale = finite ? fmaxf(top / 448.f, 1.17549435e-38f) : __uint_as_float(0x7fc00000u);
+            }
+            if (at[x] >= 0) store8<TIO, E4M3, VEC>(a, value[x], (size_t)at[x], d, rem, q[x], scale, finite);
         }
     }
 }
 
+// rows of a work-group: prompts have many; an accepted path has few, and its
+// latency is what counts (32 paths of 7 nodes: 16 rows 11.9 us, 2 rows COMMIT_US)
+constexpr int kRows = 16, kPathRows = 2;
+
 template <typename TIO, int LPR, bool E4M3, bool VEC>
 __global__ __launch_bounds__(256) void append_kernel(CacheWriteArgs a, int row_blocks) {
-    __shared__ long long s_src[kRows];
+    __shared__ long long s_src[kRows], s_dst[kRows];
     __shared__ int s_item[kRows], s_pos[kRows], s_first;
     const int tid = threadIdx.x;
     // the packing, and the sequence of this block's first row: the sequences
@@ -197,13 +210,14 @@ __global__ __launch_bounds__(256) void append_kernel(CacheWriteArgs a, int row_b
         if (tid >= i && tid < n && s_item[tid] == b && s_pos[tid] >= 0) s_pos[tid] = st ? -2 : s_pos[tid] + len;
         __syncthreads();
     }
-    write_rows<TIO, LPR, E4M3, VEC>(a, n, s_src, s_item, s_pos);
+    if (tid < n) s_dst[tid] = s_pos[tid] >= 0 ? cache_place(a, s_item[tid], s_pos[tid]) : -1;
+    __syncthreads();
+    write_rows<TIO, LPR, E4M3, VEC>(a, n, s_src, s_dst);
 }
 
 template <typename TIO, int LPR, bool E4M3, bool VEC>
 __global__ __launch_bounds__(256) void commit_kernel(CacheWriteArgs a, int chunks) {
-    __shared__ long long s_src[kRows];
-    __shared__ int s_item[kRows], s_pos[kRows];
+    __shared__ long long s_src[kPathRows], s_dst[kPathRows];
     const int tid = threadIdx.x, b = blockIdx.x / chunks, c = blockIdx.x % chunks;
     const int32_t* par = a.parent + (size_t)b * a.T;
     int bits = 0;
@@ -220,21 +234,20 @@ __global__ __launch_bounds__(256) void commit_kernel(CacheWriteArgs a, int chunk
         const int want = i == 0 ? -1 : acc[i - 1];
         if (node < 0 || node >= a.T || (i == 0 ? node != 0 : par[node] != want)) bits |= kStBadPath;
     }
-    int st = (__syncthreads_or(bits & kStBadRoot) ? kStBadRoot : 0) | (__syncthreads_or(bits & kStBadParent) ? kStBadParent : 0) |
-             (__syncthreads_or(bits & kStBadPath) ? kStBadPath : 0);
-    st |= check_pages(a, b, fits ? len : 0);
+    int st = check_pages(a, b, fits ? len : 0);
+    if (__syncthreads_or(bits))  // one barrier on the common path; more tell the errors apart
+        for (int bit = 1; bit <= kStBadPath; bit <<= 1) st |= __syncthreads_or(bits & bit) ? bit : 0;
     if (c == 0 && tid == 0 && a.status) a.status[b] = st;
     if (st) return;
-    const int n = min(kRows, len - c * kRows);
+    const int n = min(kPathRows, len - c * kPathRows);
     if (n <= 0) return;
-    if (tid < kRows) {
-        const int i = c * kRows + tid;
-        s_item[tid] = b;
-        s_src[tid] = tid < n ? (long long)b * a.T + acc[i] : 0;
-        s_pos[tid] = tid < n ? a.cache_len[b] + i : -1;
+    if (tid < n) {
+        const int i = c * kPathRows + tid;
+        s_src[tid] = (long long)b * a.T + acc[i];
+        s_dst[tid] = cache_place(a, b, a.cache_len[b] + i);
     }
     __syncthreads();
-    write_rows<TIO, LPR, E4M3, VEC>(a, n, s_src, s_item, s_pos);
+    write_rows<TIO, LPR, E4M3, VEC>(a, n, s_src, s_dst);
 }
 
 template <typename TIO, int LPR, bool E4M3, bool VEC>
@@ -245,7 +258,7 @@ hipError_t launch_one(const CacheWriteArgs& a, hipStream_t stream) {
         if (all > 0)
             hipLaunchKernelGGL((append_kernel<TIO, LPR, E4M3, VEC>), dim3(all), dim3(256), 0, stream, a, blocks);
     } else {
-        const int chunks = max(1, (min(a.Lmax, a.T) + kRows - 1) / kRows);
+        const int chunks = max(1, (min(a.Lmax, a.T) + kPathRows - 1) / kPathRows);
         hipLaunchKernelGGL((commit_kernel<TIO, LPR, E4M3, VEC>), dim3((unsigned)((long long)a.batch * chunks)), dim3(256), 0,
                            stream, a, chunks);
     }

@@ -32,7 +32,7 @@ __device__ __forceinline__ int page_of(int n, PageDiv d) { return (int)(((uint64
 // Every work-group computes the same cut from cache_len. The number of parts
 // is at most `want` over the readers plus one for each item.
 constexpr int kAttnWant = 1024;  // about four work-groups for each of the 256 compute units
-constexpr int kAttnMinKeys = 256;
+constexpr int kAttnMinKeys = 128;
 
 struct AttnPlan {
     int readers;   // work-groups that read one part
@@ -72,6 +72,11 @@ inline AttnWorkspace attn_workspace(void* ws, const AttnPlan& p, int T, int H, i
 
 __device__ __forceinline__ int usable_len(int len, int room) { return len < 0 || len > room ? 0 : len; }
 
+__device__ __forceinline__ int part_keys(const AttnPlan& plan, unsigned long long sum) {
+    const unsigned long long want = (sum * plan.readers + kAttnWant - 1) / kAttnWant;
+    return max((int)min((want + 63) / 64 * 64, 0x40000000ull), plan.min_keys);
+}
+
 struct Part {
     int ok;        // 0: no such part
     int item;
@@ -83,12 +88,43 @@ struct Part {
 };
 
 // The part `want` (or, with by_item, part 0 of item `want`), the same in all
-// NT threads. Acts as a barrier. s_red: NT / 64 + 2 ints,
+// NT threads. May act as a barrier. s_red: NT / 64 + 2 ints,
 // 8-byte aligned; s_out: one Part.
 template <int NT>
 __device__ __forceinline__ Part find_part(const int32_t* __restrict__ cache_len, int batch, int room, const AttnPlan& plan,
                                           int want, bool by_item, int* s_red, Part* s_out) {
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    if (batch <= kWave) {  // every wave by itself: one load, no barrier
+        const int raw = lane < batch ? cache_len[lane] : 0, len = usable_len(raw, room);
+        int keys = 0x40000000;
+        if (plan.split) {
+            unsigned long long sum = (unsigned)len;
+#pragma unroll
+            for (int m = 1; m < kWave; m <<= 1) sum += __shfl_xor(sum, m, kWave);
+            keys = part_keys(plan, sum);
+        }
+        const int cnt = lane < batch ? max(1, (len + keys - 1) / keys) : 0;
+        int upto = cnt;
+#pragma unroll
+        for (int m = 1; m < kWave; m <<= 1) {
+            const int o = __shfl_up(upto, m, kWave);
+            if (lane >= m) upto += o;
+        }
+        const int base = upto - cnt;
+        const bool mine = lane < batch && (by_item ? lane == want : want >= base && want < upto);
+        const unsigned long long who = __ballot(mine);
+        Part p;
+        p.ok = who != 0;
+        const int src = who ? __builtin_ctzll(who) : 0;
+        p.item = src;
+        p.base = __builtin_amdgcn_readlane(base, src);
+        p.k = by_item ? 0 : want - p.base;
+        p.n = __builtin_amdgcn_readlane(cnt, src);
+        p.len = __builtin_amdgcn_readlane(len, src);
+        p.bad_len = __builtin_amdgcn_readlane(raw, src) != p.len;
+        p.keys = keys;
+        return p;
+    }
     if (tid == 0) {
         s_out->ok = 0;
         s_red[0] = s_red[1] = 0;
@@ -103,9 +139,7 @@ __device__ __forceinline__ Part find_part(const int32_t* __restrict__ cache_len,
         if (lane == 0) atomicAdd((unsigned long long*)s_red, sum);
         __syncthreads();
         sum = *(volatile unsigned long long*)s_red;
-        const unsigned long long want_keys = (sum * plan.readers + kAttnWant - 1) / kAttnWant;
-        keys = (int)min((want_keys + 63) / 64 * 64, 0x40000000ull);
-        keys = max(keys, plan.min_keys);
+        keys = part_keys(plan, sum);
         __syncthreads();
     }
     int run = 0;

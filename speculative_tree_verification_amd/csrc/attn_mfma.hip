@@ -183,8 +183,10 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
         for (int i = 0; i < D / 16; ++i) o[i] = mma(read_columns(&s_V[w][16 * i], kVs, lane), pf, o[i]);
     };
 
-    // the tree's own keys, in the wave that has the fewest cache steps
-    if (last && !st && w == 3) {
+    // the tree's own keys, in the wave that has the fewest cache steps, while the
+    // first of the cache's are on their way
+    auto take_tree = [&]() {
+        if (!last || st || w != 3) return;
         const uint16_t* kp = (const uint16_t*)a.k + ((size_t)b * T * a.Hk + hk) * D;
         const uint16_t* vp = (const uint16_t*)a.v + ((size_t)b * T * a.Hk + hk) * D;
         const size_t stride = (size_t)a.Hk * D;
@@ -220,7 +222,7 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
                 if (strange & anc & (1u << j)) add_nonfinite<D / 16>(vp + (size_t)j * stride + 4 * lg, o);
         }
         wave_sync();
-    }
+    };
 
     // the cache: wave w has steps w, w + 4, ...
     const int k0 = pt.k * pt.keys, k1 = last ? pt.len : min(pt.len, k0 + pt.keys);
@@ -273,6 +275,7 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
             request_V(0);
             look_up(t + 4 * kStepKeys);
         }
+        take_tree();
         for (; t < k1; t += 4 * kStepKeys, set ^= 1) {
             const bool more = t + 4 * kStepKeys < k1;
             if (E4M3) {
@@ -327,8 +330,9 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
             take(s, vs);
             wave_sync();
         }
-    } else if (k1 > k0) {
-        bad = 1;  // positions without a page
+    } else {
+        bad = k1 > k0;  // positions without a page
+        take_tree();
     }
     l = row_sum(l);
     m = m == -INFINITY ? m : m * c;
@@ -408,6 +412,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
     const bool last = pt.k == pt.n - 1;
     int st = pt.bad_len ? kStBadCache : 0;
     const int first = row0 / g, last_node = min(R - 1, row0 + M - 1) / g, words = (T + 31) / 32;
+    const int k0 = pt.k * pt.keys, k1 = last ? pt.len : min(pt.len, k0 + pt.keys);
+    int page = 0;  // of this lane's key, in the first wave
+    if (w == 0 && k1 > k0 && a.n_pages > 0) page = a.page_table[(size_t)b * a.max_pages + page_of(min(k0 + lane, k1 - 1), a.div)];
     if (last) st |= tree_words<TH>(a.parent + (size_t)b * T, T, first, last_node - first + 1, words, s_par, s_anc);
     if (tid < 32) s_odd[tid] = 0;
 
@@ -497,7 +504,40 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
         }
     };
 
-    const int k0 = pt.k * pt.keys, k1 = last ? pt.len : min(pt.len, k0 + pt.keys);
+    // the tree's own keys, up to the block's last node, while the first of the
+    // cache's are on their way
+    auto take_tree = [&]() {
+        if (!last || st) return;
+        const size_t stride = (size_t)a.Hk * D;
+        const uint16_t* kp = (const uint16_t*)a.k + ((size_t)b * T * a.Hk + hk) * D;
+        const uint16_t* vp = (const uint16_t*)a.v + ((size_t)b * T * a.Hk + hk) * D;
+        for (int j0 = 0; j0 <= last_node; j0 += kTileKeys) {
+            lds_barrier();
+            for (int i = tid; i < kTileKeys * (D / 8); i += TH) {
+                const int key = i / (D / 8), c = i % (D / 8) * 8;
+                uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
+                if (j0 + key < T) {
+                    ku = gload((const uint4*)(kp + (size_t)(j0 + key) * stride + c));
+                    vu = gload((const uint4*)(vp + (size_t)(j0 + key) * stride + c));
+                }
+                if (nonfinite_bits(vu) & 0x80008000u) {
+                    atomicOr(&s_odd[(j0 + key) / 32], 1u << ((j0 + key) % 32));
+                    vu = only_finite(vu);
+                }
+                *(uint4*)&s_K[key * kKs + c] = ku;
+                *(uint4*)&s_V[key * kVs + c] = vu;
+            }
+            lds_barrier();
+            take(std::true_type(), T - j0, j0);
+        }
+        for (int x = 0; x < words; ++x) {
+            if (!s_odd[x]) continue;
+            for (int j = 0; j < 32; ++j)
+                if (s_odd[x] & s_anc[(node - first) * words + x] & (1u << j))
+                    add_nonfinite<D / 16>(vp + (size_t)(32 * x + j) * stride + 4 * lg, o);
+        }
+    };
+
     int bad = 0;
     if (k1 > k0 && a.n_pages > 0) {
         constexpr int EB = E4M3 ? 1 : 2;
@@ -506,7 +546,6 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
         const int32_t* table = a.page_table + (size_t)b * a.max_pages;
         uint4 rk[L], rv[L];
         float rks = 1.f, rvs = 1.f;
-        int page = 0;
         const bool loads = tid < kTileKeys * D * EB / 16;  // false only where half of the threads hold a whole tile
         const int prow = tid / (D * EB / 16), pcol = tid % (D * EB / 16) * 16;
         // the first wave looks up pages and rows, for all
@@ -533,11 +572,11 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
                 rvs = gload(a.v_scale + s_row[set][lane]);
             }
         };
-        look_up(k0);
         find_rows(k0, 0);
         look_up(k0 + kTileKeys);
         __syncthreads();
         request(0);
+        take_tree();
         int set = 0;
         for (int t = k0; t < k1; t += kTileKeys, set ^= 1) {
             lds_barrier();  // the last tile's reads are done
@@ -567,39 +606,10 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
             }
             take(std::false_type(), min(kTileKeys, k1 - t), 0);
         }
-    } else if (k1 > k0) {
-        bad = 1;  // positions without a page
-    }
-    // the tree's own keys, up to the block's last node
-    if (last && !st) {
-        const size_t stride = (size_t)a.Hk * D;
-        const uint16_t* kp = (const uint16_t*)a.k + ((size_t)b * T * a.Hk + hk) * D;
-        const uint16_t* vp = (const uint16_t*)a.v + ((size_t)b * T * a.Hk + hk) * D;
-        for (int j0 = 0; j0 <= last_node; j0 += kTileKeys) {
-            __syncthreads();
-            for (int i = tid; i < kTileKeys * (D / 8); i += TH) {
-                const int key = i / (D / 8), c = i % (D / 8) * 8;
-                uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
-                if (j0 + key < T) {
-                    ku = gload((const uint4*)(kp + (size_t)(j0 + key) * stride + c));
-                    vu = gload((const uint4*)(vp + (size_t)(j0 + key) * stride + c));
-                }
-                if (nonfinite_bits(vu) & 0x80008000u) {
-                    atomicOr(&s_odd[(j0 + key) / 32], 1u << ((j0 + key) % 32));
-                    vu = only_finite(vu);
-                }
-                *(uint4*)&s_K[key * kKs + c] = ku;
-                *(uint4*)&s_V[key * kVs + c] = vu;
-            }
-            __syncthreads();
-            take(std::true_type(), T - j0, j0);
-        }
-        for (int x = 0; x < words; ++x) {
-            if (!s_odd[x]) continue;
-            for (int j = 0; j < 32; ++j)
-                if (s_odd[x] & s_anc[(node - first) * words + x] & (1u << j))
-                    add_nonfinite<D / 16>(vp + (size_t)(32 * x + j) * stride + 4 * lg, o);
-        }
+    } else {
+        bad = k1 > k0;  // positions without a page
+        __syncthreads();
+        take_tree();
     }
     st |= __syncthreads_or(bad) ? kStBadCache : 0;
     if (reader == 0 && tid == 0) {
