@@ -23,7 +23,7 @@ tsv_status check_seq(const tsv_seq_shape* s) {
     if (s->n_heads % s->n_groups != 0) return TSV_E_SHAPE;
     if (s->head_dim > kMaxDim || s->d_state > kMaxDim || s->n_heads > 0xffff) return TSV_E_UNSUPPORTED;
     // every launch's grid stays inside 2^31 work-groups
-    if (tsv::prefill_blocks(s->n_seqs, s->n_tokens, s->n_heads, s->head_dim, s->d_state) > kMaxBlocks)
+    if (tsv::prefill_blocks(s) > kMaxBlocks)
         return TSV_E_UNSUPPORTED;
     return TSV_OK;
 }
@@ -58,6 +58,7 @@ tsv::CacheWriteArgs write_args(const tsv_attn_shape* s, const void* k, const voi
     a.batch = s->batch; a.T = s->n_nodes; a.Hk = s->n_kv_heads; a.D = s->head_dim;
     a.n_pages = s->n_pages; a.page_size = s->page_size; a.max_pages = s->max_pages;
     a.div = tsv::page_div(s->page_size);
+    a.heads = tsv::page_div(2 * s->n_kv_heads);
     return a;
 }
 
@@ -69,7 +70,7 @@ tsv_status tree_ssd_prefill_workspace(const tsv_seq_shape* s, uint64_t* bytes) {
     tsv_status st = check_seq(s);
     if (st != TSV_OK) return st;
     if (!bytes) return TSV_E_NULL;
-    *bytes = tsv::prefill_workspace_bytes(s->n_seqs, s->n_tokens, s->n_heads, s->head_dim, s->d_state);
+    *bytes = tsv::prefill_workspace_bytes(s);
     return TSV_OK;
 }
 
@@ -86,8 +87,7 @@ tsv_status tree_ssd_prefill(const tsv_seq_shape* s, const void* x, const void* d
     if (need > 0 && (uintptr_t)workspace % 16 != 0) return TSV_E_SHAPE;
     tsv::PrefillArgs a{x, dt, A, B, C, D, h_inout, seq_start, y, s->n_seqs, s->n_tokens, s->n_heads, s->head_dim,
                        s->d_state, s->n_groups};
-    return result(tsv::launch_prefill(a, s->in_dtype == TSV_BF16, !(s->flags & TSV_FLAG_FORCE_GENERIC), seq_status,
-                                      need > 0 ? workspace : nullptr, (hipStream_t)stream));
+    return result(tsv::launch_prefill(a, s, seq_status, need > 0 ? workspace : nullptr, (hipStream_t)stream));
 }
 
 tsv_status tree_ssd_step(const tsv_shape* s, const void* x, const void* dt, const float* A, const void* B, const void* C,

@@ -191,7 +191,5 @@ __device__ __forceinline__ int tree_words(const int32_t* __restrict__ parent, in
 }
 
 __device__ __forceinline__ float e4m3_ld(const uint8_t* p) { return __builtin_amdgcn_cvt_f32_fp8((int)*p, 0); }
-// the byte nearest to f (|f| <= 448), ties to even
-__device__ __forceinline__ uint32_t e4m3_byte(float f) { return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f, f, 0, false) & 0xffu; }
 
 }  // namespace tsv

@@ -162,12 +162,10 @@ struct PrefillArgs {
     void* y;
     int n_seqs, n_tokens, H, P, N, G;
 };
-uint64_t prefill_workspace_bytes(int n_seqs, int n_tokens, int H, int P, int N);
+uint64_t prefill_workspace_bytes(const tsv_seq_shape* s);
 // most work-groups of any launch of the prompt scan
-long long prefill_blocks(int n_seqs, int n_tokens, int H, int P, int N);
-// mfma: the bf16 MFMA kernel may be taken where the shape allows it
-hipError_t launch_prefill(const PrefillArgs& a, bool bf16, bool mfma, int32_t* status, void* workspace,
-                          hipStream_t stream);
+long long prefill_blocks(const tsv_seq_shape* s);
+hipError_t launch_prefill(const PrefillArgs& a, const tsv_seq_shape* s, int32_t* status, void* workspace, hipStream_t stream);
 
 // ---- the paged cache of attention layers
 struct PageDiv {  // n / page_size by a product (attn_common.hpp)
@@ -189,7 +187,7 @@ struct CacheWriteArgs {
     float* v_scale;
     int32_t* status;
     int batch, T, Lmax, Hk, D, n_pages, page_size, max_pages;
-    PageDiv div;
+    PageDiv div, heads;  // by page_size; by 2 Hk
 };
 hipError_t launch_cache_write(const CacheWriteArgs& a, bool bf16, bool e4m3, hipStream_t stream);
 

@@ -67,6 +67,7 @@ __global__ __launch_bounds__(256) void prefill_plain_kernel(PrefillArgs a, SeqPl
             s_dec[tid] = LOCAL ? dt * Ah : expf(dt * Ah);
         }
         __syncthreads();
+#pragma unroll 2
         for (int t = 0; t < cnt; ++t) {
             float decay = s_dec[t];
             if (LOCAL) {
@@ -74,7 +75,7 @@ __global__ __launch_bounds__(256) void prefill_plain_kernel(PrefillArgs a, SeqPl
                 decay = expf(decay);
             }
             const float wx = s_dt[t] * s_x[t][lane];
-            float y = 0.f;
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < NS; i += 4) {
                 const float4 B4 = *(const float4*)&s_B[t][w * NS + i];
@@ -84,13 +85,13 @@ __global__ __launch_bounds__(256) void prefill_plain_kernel(PrefillArgs a, SeqPl
                 st[i + 3] = fmaf(decay, st[i + 3], wx * B4.w);
                 if (!LOCAL) {
                     const float4 C4 = *(const float4*)&s_C[t][w * NS + i];
-                    y = fmaf(st[i], C4.x, y);
-                    y = fmaf(st[i + 1], C4.y, y);
-                    y = fmaf(st[i + 2], C4.z, y);
-                    y = fmaf(st[i + 3], C4.w, y);
+                    y[0] = fmaf(st[i], C4.x, y[0]);
+                    y[1] = fmaf(st[i + 1], C4.y, y[1]);
+                    y[2] = fmaf(st[i + 2], C4.z, y[2]);
+                    y[3] = fmaf(st[i + 3], C4.w, y[3]);
                 }
             }
-            if (!LOCAL) s_y[w][t][lane] = y;
+            if (!LOCAL) s_y[w][t][lane] = (y[0] + y[1]) + (y[2] + y[3]);
         }
         if (!LOCAL) {
             __syncthreads();
@@ -182,27 +183,35 @@ void launch_combine(const PrefillArgs& a, const SeqPlan& p, const SeqWorkspace& 
         hipLaunchKernelGGL((prefill_combine_kernel<1>), grid, dim3(256), 0, stream, a, p, ws, chunks);
 }
 
+// Whether the bf16 MFMA kernel takes the shape (its tensors' alignment is looked at
+// per call: the plain kernel then runs with the same segments)
+bool matrix_shape(const tsv_seq_shape* s) {
+    return s->in_dtype == TSV_BF16 && s->head_dim == 64 && (s->d_state == 64 || s->d_state == 128) &&
+           !(s->flags & TSV_FLAG_FORCE_GENERIC);
+}
+int min_seg_of(const tsv_seq_shape* s) { return matrix_shape(s) ? kMinSegMatrix : kMinSegPlain; }
+
 }  // namespace
 
-uint64_t prefill_workspace_bytes(int n_seqs, int n_tokens, int H, int P, int N) {
-    return seq_workspace_bytes(seq_plan(n_seqs, n_tokens, H), H, P, N);
+uint64_t prefill_workspace_bytes(const tsv_seq_shape* s) {
+    return seq_workspace_bytes(seq_plan(s->n_seqs, s->n_tokens, s->n_heads, min_seg_of(s)), s->n_heads, s->head_dim, s->d_state);
 }
 
-long long prefill_blocks(int n_seqs, int n_tokens, int H, int P, int N) {
-    const SeqPlan p = seq_plan(n_seqs, n_tokens, H);
-    const long long scan = (long long)p.slots * H * ((P + kWave - 1) / kWave);
-    const long long combine = (long long)n_seqs * H * (((long long)P * N + 255) / 256);
+long long prefill_blocks(const tsv_seq_shape* s) {
+    const SeqPlan p = seq_plan(s->n_seqs, s->n_tokens, s->n_heads, min_seg_of(s));
+    const long long scan = (long long)p.slots * s->n_heads * ((s->head_dim + kWave - 1) / kWave);
+    const long long combine = (long long)s->n_seqs * s->n_heads * (((long long)s->head_dim * s->d_state + 255) / 256);
     return scan > combine ? scan : combine;
 }
 
-hipError_t launch_prefill(const PrefillArgs& a, bool bf16, bool mfma, int32_t* status, void* workspace,
-                          hipStream_t stream) {
+hipError_t launch_prefill(const PrefillArgs& a, const tsv_seq_shape* s, int32_t* status, void* workspace, hipStream_t stream) {
+    const bool bf16 = s->in_dtype == TSV_BF16;
     if (status)
         hipLaunchKernelGGL(seq_status_kernel, dim3(1), dim3(256), 0, stream, a.seq_start, a.n_seqs, a.n_tokens, status);
     if (a.n_tokens > 0) {
-        const SeqPlan p = seq_plan(a.n_seqs, a.n_tokens, a.H);
+        const bool matrix = matrix_shape(s) && prefill_mfma_aligned(a);
+        const SeqPlan p = seq_plan(a.n_seqs, a.n_tokens, a.H, min_seg_of(s));
         const SeqWorkspace ws = seq_workspace(workspace, p, a.H, a.P, a.N);
-        const bool matrix = bf16 && mfma && prefill_mfma_supported(a);
         for (int pass = p.split ? 0 : 1; pass < 2; ++pass) {
             const bool local = pass == 0;
             if (matrix)

@@ -471,9 +471,9 @@ void launch_pass(const PrefillArgs& a, const SeqPlan& p, const SeqWorkspace& ws,
 
 }  // namespace
 
-bool prefill_mfma_supported(const PrefillArgs& a) {
+bool prefill_mfma_aligned(const PrefillArgs& a) {
     const uintptr_t all = (uintptr_t)a.x | (uintptr_t)a.B | (uintptr_t)a.C | (uintptr_t)a.y | (uintptr_t)a.h;
-    return a.P == kP && (a.N == 64 || a.N == 128) && all % 16 == 0;
+    return all % 16 == 0;
 }
 
 void launch_prefill_mfma(const PrefillArgs& a, const SeqPlan& p, const SeqWorkspace& ws, bool local, hipStream_t stream) {

@@ -22,9 +22,9 @@ constexpr int kStBadSeq = 32;
 
 // `seg` tokens so that all (segment, head) pairs fit the GPU at once (two
 // work-groups of two heads on each of the 256 compute units; every sequence may
-// end with a short segment), a multiple of the 64-token chunk and at least four
-// chunks (below that the second pass over the inputs costs more than the
-// parallelism gives). Many sequences fill the GPU by themselves; half of the
+// end with a short segment), a multiple of the 64-token chunk and at least min_seg
+// (four chunks for the matrix kernel: below that the second pass over the inputs
+// costs more than the parallelism gives). Many sequences fill the GPU by themselves; half of the
 // room is then the measure, so that only sequences much longer than the others
 // are cut.
 struct SeqPlan {
@@ -42,13 +42,17 @@ struct SeqPlan {
 // would cost more than it gives.
 constexpr int kSortMin = 16, kSortMax = 256;
 
-inline SeqPlan seq_plan(int n_seqs, int n_tokens, int n_heads) {
+// The plain kernel is as slow per token as its chain of operations, so it takes
+// the shortest segments.
+constexpr int kMinSegMatrix = 256, kMinSegPlain = 64;
+
+inline SeqPlan seq_plan(int n_seqs, int n_tokens, int n_heads, int min_seg) {
     constexpr long long kWant = 1024;
     long long room = kWant - (long long)n_seqs * n_heads;
     if (room < kWant / 2) room = kWant / 2;
     long long seg = ((long long)n_tokens * n_heads + room - 1) / room;
     seg = (seg + 63) / 64 * 64;
-    if (seg < 256) seg = 256;
+    if (seg < min_seg) seg = min_seg;
     if (seg > 0x7fffffc0LL) seg = 0x7fffffc0LL;
     SeqPlan p;
     p.seg = (int)seg;
@@ -88,7 +92,7 @@ inline SeqWorkspace seq_workspace(void* ws, const SeqPlan& p, int H, int P, int 
 }
 
 // bf16 MFMA kernel (prefill_mfma.hip): P 64, N 64 or 128, 16-byte aligned tensors
-bool prefill_mfma_supported(const PrefillArgs& a);
+bool prefill_mfma_aligned(const PrefillArgs& a);
 void launch_prefill_mfma(const PrefillArgs& a, const SeqPlan& p, const SeqWorkspace& ws, bool local, hipStream_t stream);
 
 struct Segment {
