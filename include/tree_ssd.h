@@ -600,8 +600,9 @@ typedef struct {
  *
  * Arithmetic: fp32 scores, maxima, sums and accumulators. bf16 inputs with D
  * 64 or 128 use bf16 MFMA; the softmax weights (times the scale of an 8-bit
- * value row) are rounded once to bf16 for the product with v. Other shapes and
- * fp32 inputs use fp32 throughout.
+ * value row) enter the product with v as two bf16 parts (16 bits) where at most
+ * 16 rows share a key head (T * H / Hk <= 16), and rounded once to bf16
+ * otherwise. Other shapes and fp32 inputs use fp32 throughout.
  */
 tsv_status tree_attn_verify(const tsv_attn_shape* s, const void* q, const void* k, const void* v,
                             const int32_t* parent, const void* k_cache, const void* v_cache,

@@ -109,18 +109,33 @@ __device__ __forceinline__ void store8(const CacheWriteArgs& a, bool value, size
     }
 }
 
+// Pages of `count` rows at cache_len[b] = len: false if they do not fit
+__device__ __forceinline__ bool page_range(const CacheWriteArgs& a, int len, int count, int* first, int* last) {
+    const int room = a.max_pages * a.page_size;
+    *first = 0;
+    *last = -1;
+    if (len < 0 || count < 0 || len > room || count > room - len) return false;
+    if (count > 0) {
+        *first = page_of(len, a.div);
+        *last = page_of(len + count - 1, a.div);
+    }
+    return true;
+}
+__device__ __forceinline__ bool pages_bad(const CacheWriteArgs& a, int b, int first, int last, int step) {
+    bool bad = false;
+    for (int i = first; i <= last; i += step) {
+        const int pg = a.page_table[(size_t)b * a.max_pages + i];
+        bad |= pg < 0 || pg >= a.n_pages;
+    }
+    return bad;
+}
+
 // Status bits of writing `count` rows at cache_len[b]: the same in all threads.
 // Acts as a barrier.
 __device__ __forceinline__ int check_pages(const CacheWriteArgs& a, int b, int count) {
-    const int room = a.max_pages * a.page_size, len = a.cache_len[b];
-    int bad = len < 0 || count < 0 || len > room || count > room - len;
-    if (!bad && count > 0) {
-        const int first = page_of(len, a.div), last = page_of(len + count - 1, a.div);
-        for (int i = first + threadIdx.x; i <= last; i += blockDim.x) {
-            const int pg = a.page_table[(size_t)b * a.max_pages + i];
-            bad |= pg < 0 || pg >= a.n_pages;
-        }
-    }
+    int first, last;
+    bool bad = !page_range(a, a.cache_len[b], count, &first, &last);
+    bad |= pages_bad(a, b, first + threadIdx.x, last, blockDim.x);
     return __syncthreads_or(bad) ? kStBadCache : 0;
 }
 
@@ -182,7 +197,7 @@ constexpr int kRows = 16, kPathRows = 2;
 template <typename TIO, int LPR, bool E4M3, bool VEC>
 __global__ __launch_bounds__(256) void append_kernel(CacheWriteArgs a, int row_blocks) {
     __shared__ long long s_src[kRows], s_dst[kRows];
-    __shared__ int s_item[kRows], s_pos[kRows], s_first;
+    __shared__ int s_item[kRows], s_pos[kRows], s_place[kRows], s_bad[kRows], s_long[kRows], s_first;
     const int tid = threadIdx.x;
     // the packing, and the sequence of this block's first row: the sequences
     // that end at or before it
@@ -209,22 +224,47 @@ __global__ __launch_bounds__(256) void append_kernel(CacheWriteArgs a, int row_b
         int q = s_first, pos = -1;
         const int r = r0 + tid;
         while (q < a.batch && a.seq_start[q + 1] <= r) ++q;
-        if (tid < n && q < a.batch && r >= a.seq_start[q]) pos = r - a.seq_start[q];  // + cache_len below
+        if (tid < n && q < a.batch && r >= a.seq_start[q]) pos = r - a.seq_start[q];  // in its sequence
         s_item[tid] = q < a.batch ? q : 0;
         s_src[tid] = r;
         s_pos[tid] = pos;
     }
+    if (tid < kRows) s_bad[tid] = s_long[tid] = 0;
     __syncthreads();
-    for (int i = 0; i < n; ++i) {
-        const int b = s_item[i];
-        if (s_pos[i] < 0 || (i > 0 && s_pos[i - 1] >= 0 && s_item[i - 1] == b)) continue;
-        const int st = check_pages(a, b, a.seq_start[b + 1] - a.seq_start[b]);
-        const int len = a.cache_len[b];
-        // thread i' owns row i': rows of item b start here
-        if (tid >= i && tid < n && s_item[tid] == b && s_pos[tid] >= 0) s_pos[tid] = st ? -2 : s_pos[tid] + len;
+    // the sequences that begin or go on in these rows: 16 threads each, all at once
+    // (16 short prompts one after another took 30 us), and then all threads for
+    // each of the few that have many pages
+    {
+        constexpr int kLong = 64;
+        const int i = tid / (256 / kRows), b = s_item[i];
+        const bool leads = i < n && s_pos[i] >= 0 && (i == 0 || s_pos[i - 1] < 0 || s_item[i - 1] != b);
+        if (leads) {
+            const int len = a.cache_len[b];
+            int first, last;
+            const bool fits = page_range(a, len, a.seq_start[b + 1] - a.seq_start[b], &first, &last);
+            if (!fits)
+                s_bad[i] = 1;
+            else if (last - first >= kLong)
+                s_long[i] = 1;
+            else if (pages_bad(a, b, first + tid % (256 / kRows), last, 256 / kRows))
+                s_bad[i] = 1;
+        }
         __syncthreads();
+        for (int j = 0; j < n; ++j) {
+            if (!s_long[j]) continue;
+            const int st = check_pages(a, s_item[j], a.seq_start[s_item[j] + 1] - a.seq_start[s_item[j]]);
+            if (tid == 0 && st) s_bad[j] = 1;
+            __syncthreads();
+        }
     }
-    if (tid < n) s_dst[tid] = s_pos[tid] >= 0 ? cache_place(a, s_item[tid], s_pos[tid]) : -1;
+    if (tid < n && s_pos[tid] >= 0) {
+        int j = tid;  // the first of this sequence's rows here
+        while (j > 0 && s_item[j - 1] == s_item[tid] && s_pos[j - 1] >= 0) --j;
+        s_place[tid] = s_bad[j] ? -1 : s_pos[tid] + a.cache_len[s_item[tid]];
+    } else if (tid < n) {
+        s_place[tid] = -1;
+    }
+    if (tid < n) s_dst[tid] = s_place[tid] >= 0 ? cache_place(a, s_item[tid], s_place[tid]) : -1;
     __syncthreads();
     write_rows<TIO, LPR, E4M3, VEC>(a, n, s_src, s_dst);
 }

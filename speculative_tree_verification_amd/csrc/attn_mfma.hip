@@ -177,10 +177,21 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
 #pragma unroll
             for (int e = 0; e < 8; ++e) p[e] *= vs[e / 4][e % 4];  // a key past the last one has the last one's
         }
-        const bf16x8 pf = as_operand(make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]),
-                                                pack_bf16x2(p[6], p[7])));
+        // weights as two bf16 parts: with the cache's bytes the bound, their rounding
+        // need not be a part of the result's error
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) o[i] = mma(read_columns(&s_V[w][16 * i], kVs, lane), pf, o[i]);
+        for (int e = 0; e < 4; ++e) {
+            hi[e] = pack_bf16x2(p[2 * e], p[2 * e + 1]);
+            lo[e] = pack_bf16x2(p[2 * e] - __uint_as_float(hi[e] << 16), p[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+        }
+        const bf16x8 pf = as_operand(make_uint4(hi[0], hi[1], hi[2], hi[3])), pl = as_operand(make_uint4(lo[0], lo[1], lo[2], lo[3]));
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const bf16x8 v = read_columns(&s_V[w][16 * i], kVs, lane);
+            o[i] = mma(v, pf, o[i]);
+            o[i] = mma(v, pl, o[i]);
+        }
     };
 
     // the tree's own keys, in the wave that has the fewest cache steps, while the

@@ -15,13 +15,18 @@ namespace {
 
 constexpr int kTok = 16;  // tokens staged at a time
 
-template <typename TIO, int NS, bool LOCAL>
+// FULL: fp32 with N == 4 NS, 16-byte aligned states. B and C are then the same
+// four cache lines for all lanes of a wave and come through the scalar cache into
+// scalar registers; broadcast from LDS they bound the kernel (a 16-byte read
+// returns 1 KB to the lanes: 51 and 65 us against 34 and 54 us for the two passes over
+// 1360 tokens, 24 heads).
+template <typename TIO, int NS, bool LOCAL, bool FULL>
 __global__ __launch_bounds__(256) void prefill_plain_kernel(PrefillArgs a, SeqPlan plan, SeqWorkspace ws, int pblocks) {
     __shared__ int s_red[4];
     __shared__ Segment s_seg;
     __shared__ int s_len[kSortMax];
-    __shared__ __attribute__((aligned(16))) float s_B[kTok][4 * NS], s_C[kTok][4 * NS];
-    __shared__ float s_x[kTok][kWave], s_y[4][kTok][kWave], s_dec[kTok], s_dt[kTok];
+    __shared__ __attribute__((aligned(16))) float s_B[FULL ? 1 : kTok][4 * NS], s_C[FULL || LOCAL ? 1 : kTok][4 * NS];
+    __shared__ float s_x[kTok][kWave], s_y[4][kTok][kWave], s_dec[kTok], s_da[kTok], s_dt[kTok];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
     int slot, hb;
     place_block(plan, a.H * pblocks, &slot, &hb);
@@ -38,63 +43,88 @@ __global__ __launch_bounds__(256) void prefill_plain_kernel(PrefillArgs a, SeqPl
     float st[NS];
     const float* from = sg.n == 1 ? a.h + ((size_t)sg.seq * a.H + h) * PN
                                   : ws.state + ((size_t)(sg.base + (sg.k ? sg.k - 1 : sg.n - 1)) * a.H + h) * PN;
+    if (LOCAL) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        const int n = w * NS + i;
-        st[i] = !LOCAL && row && n < N ? from[(size_t)p * N + n] : 0.f;
+        for (int i = 0; i < NS; ++i) st[i] = 0.f;
+    } else if (FULL) {
+#pragma unroll
+        for (int i = 0; i < NS; i += 4) {
+            const float4 v = gload((const float4*)(from + (size_t)min(p, P - 1) * N + w * NS + i));
+            st[i] = v.x; st[i + 1] = v.y; st[i + 2] = v.z; st[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) st[i] = gload(from + (size_t)min(p, P - 1) * N + min(w * NS + i, N - 1));
+#pragma unroll
+        for (int i = 0; i < NS; ++i) st[i] = w * NS + i < N ? st[i] : 0.f;
     }
     const float Ah = a.A[h], Dh = a.D[h];
     const int g = h / (a.H / a.G);
     float sum = 0.f;
+    // the next tokens' rows are loaded while these are worked on, from clamped
+    // addresses (a load under a condition would be waited for at once) and kept as
+    // loaded
+    constexpr int BI = FULL ? 0 : kTok * 4 * NS / 256, XI = kTok * kWave / 256;
+    TIO rB[BI + 1], rC[BI + 1], rx[XI], rdt;
+    auto request = [&](int t0) {
+        const int most = sg.t1 - 1;
+#pragma unroll
+        for (int i = 0; i < BI; ++i) {
+            const int e = tid + i * 256, t = e / (4 * NS), n = e % (4 * NS);
+            const size_t at = ((size_t)min(t0 + t, most) * a.G + g) * N + min(n, N - 1);
+            rB[i] = gload((const TIO*)a.B + at);
+            if (!LOCAL) rC[i] = gload((const TIO*)a.C + at);
+        }
+#pragma unroll
+        for (int i = 0; i < XI; ++i) {
+            const int e = tid + i * 256, t = e / kWave, q = pb * kWave + e % kWave;
+            rx[i] = gload((const TIO*)a.x + ((size_t)min(t0 + t, most) * a.H + h) * P + min(q, P - 1));
+        }
+        rdt = gload((const TIO*)a.dt + (size_t)min(t0 + tid % kTok, most) * a.H + h);
+    };
+    request(sg.t0);
     for (int t0 = sg.t0; t0 < sg.t1; t0 += kTok) {
         const int cnt = min(kTok, sg.t1 - t0);
-        __syncthreads();
-        for (int i = tid; i < kTok * 4 * NS; i += 256) {
-            const int t = i / (4 * NS), n = i % (4 * NS);
+        lds_barrier();
+#pragma unroll
+        for (int i = 0; i < BI; ++i) {
+            const int e = tid + i * 256, t = e / (4 * NS), n = e % (4 * NS);
             const bool in = t < cnt && n < N;
-            const size_t at = ((size_t)(t0 + t) * a.G + g) * N + n;
-            s_B[t][n] = in ? Elem<TIO>::ld((const TIO*)a.B, at) : 0.f;
-            if (!LOCAL) s_C[t][n] = in ? Elem<TIO>::ld((const TIO*)a.C, at) : 0.f;
+            s_B[t][n] = in ? Elem<TIO>::up(rB[i]) : 0.f;
+            if (!LOCAL) s_C[t][n] = in ? Elem<TIO>::up(rC[i]) : 0.f;
         }
-        for (int i = tid; i < kTok * kWave; i += 256) {
-            const int t = i / kWave, q = pb * kWave + i % kWave;
-            s_x[t][i % kWave] =
-                t < cnt && q < P ? Elem<TIO>::ld((const TIO*)a.x, ((size_t)(t0 + t) * a.H + h) * P + q) : 0.f;
+#pragma unroll
+        for (int i = 0; i < XI; ++i) {
+            const int e = tid + i * 256, t = e / kWave, q = pb * kWave + e % kWave;
+            s_x[t][e % kWave] = t < cnt && q < P ? Elem<TIO>::up(rx[i]) : 0.f;
         }
         if (tid < cnt) {
-            const float dt = Elem<TIO>::ld((const TIO*)a.dt, (size_t)(t0 + tid) * a.H + h);
+            const float dt = Elem<TIO>::up(rdt);
             s_dt[tid] = dt;
-            s_dec[tid] = LOCAL ? dt * Ah : expf(dt * Ah);
+            s_da[tid] = dt * Ah;
+            s_dec[tid] = expf(dt * Ah);
         }
-        __syncthreads();
+        lds_barrier();
+        if (t0 + kTok < sg.t1) request(t0 + kTok);
 #pragma unroll 2
         for (int t = 0; t < cnt; ++t) {
-            float decay = s_dec[t];
-            if (LOCAL) {
-                sum += decay;
-                decay = expf(decay);
-            }
+            const float decay = s_dec[t];
+            if (LOCAL) sum += s_da[t];
             const float wx = s_dt[t] * s_x[t][lane];
             float y[4] = {0.f, 0.f, 0.f, 0.f};
+            typedef const float __attribute__((address_space(4))) uniform_float;  // not written by this launch
+            const size_t at = ((size_t)(t0 + t) * a.G + g) * N + w * NS;
+            uniform_float* Bu = (uniform_float*)((const float*)a.B + at);
+            uniform_float* Cu = (uniform_float*)((const float*)a.C + at);
 #pragma unroll
-            for (int i = 0; i < NS; i += 4) {
-                const float4 B4 = *(const float4*)&s_B[t][w * NS + i];
-                st[i] = fmaf(decay, st[i], wx * B4.x);
-                st[i + 1] = fmaf(decay, st[i + 1], wx * B4.y);
-                st[i + 2] = fmaf(decay, st[i + 2], wx * B4.z);
-                st[i + 3] = fmaf(decay, st[i + 3], wx * B4.w);
-                if (!LOCAL) {
-                    const float4 C4 = *(const float4*)&s_C[t][w * NS + i];
-                    y[0] = fmaf(st[i], C4.x, y[0]);
-                    y[1] = fmaf(st[i + 1], C4.y, y[1]);
-                    y[2] = fmaf(st[i + 2], C4.z, y[2]);
-                    y[3] = fmaf(st[i + 3], C4.w, y[3]);
-                }
+            for (int i = 0; i < NS; ++i) {
+                st[i] = fmaf(decay, st[i], wx * (FULL ? Bu[i] : s_B[t][w * NS + i]));
+                if (!LOCAL) y[i % 4] = fmaf(st[i], FULL ? Cu[i] : s_C[t][w * NS + i], y[i % 4]);
             }
             if (!LOCAL) s_y[w][t][lane] = (y[0] + y[1]) + (y[2] + y[3]);
         }
         if (!LOCAL) {
-            __syncthreads();
+            lds_barrier();
             for (int i = tid; i < cnt * kWave; i += 256) {
                 const int t = i / kWave, c = i % kWave, q = pb * kWave + c;
                 if (q < P) {
@@ -106,10 +136,16 @@ __global__ __launch_bounds__(256) void prefill_plain_kernel(PrefillArgs a, SeqPl
     }
     if (!LOCAL && sg.k != sg.n - 1) return;
     float* to = LOCAL ? ws.state + ((size_t)(sg.base + sg.k) * a.H + h) * PN : a.h + ((size_t)sg.seq * a.H + h) * PN;
+    if (FULL) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        const int n = w * NS + i;
-        if (row && n < N) to[(size_t)p * N + n] = st[i];
+        for (int i = 0; i < NS; i += 4)
+            if (row) gstore((float4*)(to + (size_t)p * N + w * NS + i), make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int n = w * NS + i;
+            if (row && n < N) to[(size_t)p * N + n] = st[i];
+        }
     }
     if (LOCAL && tid == 0 && pb == 0) ws.sum[(size_t)(sg.base + sg.k) * a.H + h] = sum;
 }
@@ -160,7 +196,11 @@ template <typename TIO, int NS, bool LOCAL>
 void launch_plain_pass(const PrefillArgs& a, const SeqPlan& p, const SeqWorkspace& ws, hipStream_t stream) {
     const int pblocks = (a.P + kWave - 1) / kWave;
     const dim3 grid((unsigned)((long long)p.slots * a.H * pblocks));
-    hipLaunchKernelGGL((prefill_plain_kernel<TIO, NS, LOCAL>), grid, dim3(256), 0, stream, a, p, ws, pblocks);
+    const bool full = sizeof(TIO) == 4 && a.N == 4 * NS && (uintptr_t)a.h % 16 == 0;
+    if (full && sizeof(TIO) == 4)
+        hipLaunchKernelGGL((prefill_plain_kernel<TIO, NS, LOCAL, sizeof(TIO) == 4>), grid, dim3(256), 0, stream, a, p, ws, pblocks);
+    else
+        hipLaunchKernelGGL((prefill_plain_kernel<TIO, NS, LOCAL, false>), grid, dim3(256), 0, stream, a, p, ws, pblocks);
 }
 
 template <typename TIO, bool LOCAL>

@@ -357,6 +357,27 @@ def test_append_bad_items_are_not_written(bnd):
         same(c, want)
 
 
+def test_append_many_short_sequences_and_a_long_one(bnd):
+    """Rows of many sequences in one work-group, some of them bad; and a sequence of 150 pages, a late one bad."""
+    lens = [(3 * b) % 4 for b in range(60)] + [150, 150, 2]
+    n, bad = len(lens), {3, 17, 18, 42, 61}
+    c = U.cache(26, n, [5] * n, 2, 64, 1, BF, E4, room=160)
+    k, v = nodes(26, 1, sum(lens), 2, 2, 64, BF)[1:]
+    for b in bad - {61}:
+        c["page_table"][b, 5] = -1
+    c["page_table"][61, 5 + 140] = c["k_cache"].shape[0]
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    rows = [(b, i) for b in range(n) if b not in bad for i in range(lens[b])]
+    src = torch.tensor([starts[b] + i for b, i in rows])
+    want = expect(c, [t[0][src] for t in (k, v)], [(b, 5 + i) for b, i in rows], "append")
+    st = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    args, scales = U.cache_args(c)
+    bnd.attn_append(k[0], v[0], torch.tensor(starts, dtype=torch.int32, device="cuda"), *args, **scales, seq_status=st)
+    torch.cuda.synchronize()
+    assert st.tolist() == [64 if b in bad and lens[b] else 0 for b in range(n)]
+    same(c, want)
+
+
 def test_rows_that_are_not_finite_read_back_as_nan(bnd):
     c = U.cache(24, 1, [0], 1, 64, 16, BF, E4, room=4)
     k = torch.ones(4, 1, 64, dtype=BF, device="cuda")
