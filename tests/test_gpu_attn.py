@@ -113,6 +113,17 @@ def test_many_items(bnd):
     check(bnd, q, k, v, par, c, BF, "300 items", only=range(0, 300, 13))
 
 
+@pytest.mark.parametrize("T", [1, 20])
+@pytest.mark.parametrize("n", [64, 65, 300])
+def test_many_items_split(bnd, n, T):
+    """Items on both sides of the search's one-wave form, some of them cut into parts."""
+    lens = [(11 * b) % 20 for b in range(n)]
+    lens[1], lens[n - 2] = 3000, 900
+    c = U.cache(7, n, lens, 1, 64, 16, BF, BF)
+    q, k, v = nodes(7, n, T, 2, 1, 64, BF)
+    check(bnd, q, k, v, U.trees(7, n, T), c, BF, f"{n} items, T={T}", only=[0, 1, 2, n // 2, n - 2, n - 1])
+
+
 @pytest.mark.parametrize("dtype,cdtype", TYPES)
 def test_large_scores(bnd, dtype, cdtype):
     """Scores far apart: the running maximum moves, weights underflow."""

@@ -1,0 +1,97 @@
+"""GPU: the prompt scan, the tree pass, the commit and the single-token step of an
+SSM layer as one decoding loop uses them, and a layer of each kind at once.
+
+Prompts of different lengths make the states; draft trees are verified over them
+and the accepted paths committed, twice; then one token follows without a draft.
+Every output has to be that of the item's own token sequence (prompt, accepted
+nodes, token) run from its start, in fp64. The bounds are those of the tree pass
+and its commit. (The attention layer's loop is in tests/test_gpu_attn.py.)
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from oracle import sequence as S
+from tests import seq_util as U
+from tests.gpu_util import TOL, say, slice_err
+from speculative_tree_verification_amd import workloads as W
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def bnd():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from speculative_tree_verification_amd import binding
+    return binding
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_ssm_layer_from_prompt_to_token(bnd, dtype):
+    n, H, P, N, G, T = 3, 4, 64, 128, 1, 15
+    lens = [70, 0, 131]
+    d = U.ssd(71, sum(lens), n, H, P, N, G, dtype, dt_bias=-4.0)
+    h0 = U.f64(d["h"])
+    h = d["h"].clone()
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    bnd.prefill(d["x"], d["dt"], d["A"], d["B"], d["C"], d["D"], h, torch.tensor(starts, dtype=torch.int32, device="cuda"))
+    past = [{k: U.f64(d[k][starts[b]:starts[b + 1]]) for k in ("x", "dt", "B", "C")} for b in range(n)]
+    A, D = U.f64(d["A"]), U.f64(d["D"])
+    tol = TOL[W.BF16 if dtype == BF else W.F32]
+    g = torch.Generator().manual_seed(72)
+    for step in range(2):
+        t = U.ssd(73 + step, n * T, n, H, P, N, G, dtype, dt_bias=-4.0)
+        x, dt, B, C = (t[k].view(n, T, *t[k].shape[1:]) for k in ("x", "dt", "B", "C"))
+        par = U.trees(75 + step, n, T)
+        y = bnd.verify(x, dt, d["A"], B, C, d["D"], h, par.cuda())
+        draft, target = (torch.randint(0, 2, (n, T), generator=g, dtype=torch.int32).cuda() for _ in range(2))
+        acc, count, _, st = bnd.accept_greedy(par.cuda(), draft, target, 6)
+        torch.cuda.synchronize()
+        yg, e = U.f64(y), {k: U.f64(v) for k, v in (("x", x), ("dt", dt), ("B", B), ("C", C))}
+        for b in range(n):
+            for i in (0, 5, T - 1):  # some nodes: the prompt, the accepted tokens and the node's root path
+                path = S.root_path(par[b].numpy(), i)
+                seq = {k: np.concatenate([past[b][k], e[k][b, path]]) for k in past[b]}
+                ref = S.scan(seq["x"], seq["dt"], A, seq["B"], seq["C"], D, h0[b])[0][-1]
+                assert slice_err(yg[b, i], ref) <= tol, (step, b, i)
+        bnd.commit(x, dt, d["A"], B, h, par.cuda(), acc, count)
+        for b in range(n):
+            path = acc[b, :int(count[b])].cpu().numpy()
+            past[b] = {k: np.concatenate([past[b][k], e[k][b, path]]) for k in past[b]}
+    t = U.ssd(79, n, n, H, P, N, G, dtype, dt_bias=-4.0)
+    y = U.f64(bnd.step(t["x"], t["dt"], d["A"], t["B"], t["C"], d["D"], h))
+    worst = 0.0
+    for b in range(n):
+        seq = {k: np.concatenate([past[b][k], U.f64(t[k][b:b + 1])]) for k in past[b]}
+        ref, hr, _, _ = S.scan(seq["x"], seq["dt"], A, seq["B"], seq["C"], D, h0[b])
+        assert slice_err(y[b], ref[-1]) <= tol
+        worst = max(worst, slice_err(U.f64(h[b]), hr))
+        assert worst <= 1e-4
+    say(f"[hybrid] ssm {dtype}: state error {worst:.1e} after prompt, two trees and a token")
+
+
+def test_two_calls_at_once_on_two_streams(bnd):
+    """Calls on two streams share nothing but their read-only inputs."""
+    d = U.ssd(81, 900, 1, 4, 64, 128, 1, BF, dt_bias=-4.0)
+    seq = torch.tensor([0, 900], dtype=torch.int32, device="cuda")
+    names = ("x", "dt", "A", "B", "C", "D")
+    c = U.cache(82, 2, [3000, 40], 2, 64, 16, BF, BF)
+    args, _ = U.cache_args(c)
+    g = torch.Generator().manual_seed(83)
+    q, k, v = (torch.randn(2, 9, m, 64, generator=g).to(BF).cuda() for m in (4, 2, 2))
+    par = U.trees(84, 2, 9).cuda()
+    want_h = d["h"].clone()
+    want = bnd.prefill(*(d[m] for m in names), want_h, seq), bnd.attn_verify(q, k, v, par, *args)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(4):
+        for s in streams:
+            h = d["h"].clone()
+            s.wait_stream(torch.cuda.current_stream())
+            got.append((bnd.prefill(*(d[m] for m in names), h, seq, stream=s), bnd.attn_verify(q, k, v, par, *args, stream=s), h))
+    torch.cuda.synchronize()
+    for y, o, h in got:
+        assert torch.equal(y, want[0]) and torch.equal(o, want[1]) and torch.equal(h, want_h)

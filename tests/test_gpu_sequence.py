@@ -88,6 +88,24 @@ def test_prefill_segments(bnd, dtype, H, P, N, G, lens):
     check_prefill(bnd, d, lens, dtype)
 
 
+@pytest.mark.parametrize("H,N,G,lens", [(64, 64, 8, [70, 1, 64, 0, 129, 33, 65, 5, 90]), (80, 128, 1, [65, 130, 0, 63, 1, 100, 64]),
+                                        (64, 128, 2, [600, 130])])
+def test_prefill_two_heads_a_work_group(bnd, H, N, G, lens):
+    """Enough heads and sequences that a work-group takes two heads, with and without segments."""
+    d = U.ssd(51 + N, sum(lens) + 3, len(lens), H, 64, N, G, BF)
+    check_prefill(bnd, d, lens, BF, start0=1)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,longest", [(16, 40), (37, 70), (200, 9), (256, 5), (257, 5), (20, 600)])
+def test_prefill_longest_first(bnd, dtype, n, longest):
+    """16 to 256 sequences are dealt out by falling length, with equal and empty ones among them."""
+    lens = [(13 * i + 5) % (longest + 1) for i in range(n)]
+    lens[n // 2] = longest
+    d = U.ssd(61 + n, sum(lens) + 1, n, 4, 64, 64, 2, dtype, dt_bias=-4.0)
+    check_prefill(bnd, d, lens, dtype)
+
+
 def test_prefill_many_sequences(bnd):
     """More sequences than threads of the search for a segment."""
     lens = [(7 * i) % 4 for i in range(700)]
