@@ -45,13 +45,17 @@ __device__ __forceinline__ Two swap16(float v) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return {__uint_as_float(r[0]), __uint_as_float(r[1])};
 }
+template <int RW = 16>
 __device__ __forceinline__ float row_max(float v) {
     const Two h = swap32(v);
+    if (RW == 32) return fmaxf(h.a, h.b);
     const Two q = swap16(fmaxf(h.a, h.b));
     return fmaxf(q.a, q.b);
 }
+template <int RW = 16>
 __device__ __forceinline__ float row_sum(float v) {
     const Two h = swap32(v);
+    if (RW == 32) return h.a + h.b;
     const Two q = swap16(h.a + h.b);
     return q.a + q.b;
 }
@@ -87,16 +91,15 @@ __device__ __forceinline__ uint4 only_finite(uint4 u) {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// v: the node's values from this lane's first d on; o[i] holds d = 16 i + r
-template <int NO>
-__device__ __forceinline__ void add_nonfinite(const uint16_t* v, f32x4* o) {
+// v: the node's values from this lane's first d on; o's element e holds d = e / 4 * STEP + e % 4
+template <int NO, int STEP = 16, class Acc>
+__device__ __forceinline__ void add_nonfinite(const uint16_t* v, Acc* o) {
+    constexpr int NR = sizeof(Acc) / 4;
 #pragma unroll
-    for (int i = 0; i < NO; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const uint16_t b = gload(v + 16 * i + r);
-            if ((b & 0x7f80) == 0x7f80) o[i][r] += bf16_bits_to_f32(b);
-        }
+    for (int i = 0; i < NO * NR; ++i) {
+        const uint16_t b = gload(v + i / 4 * STEP + i % 4);
+        if ((b & 0x7f80) == 0x7f80) o[i / NR][i % NR] += bf16_bits_to_f32(b);
+    }
 }
 
 // ---------------------------------------------------------------- rows
@@ -114,7 +117,7 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
     static_assert(sizeof(s_V) >= 4 * 16 * kOs * sizeof(float), "outputs take the place of V");
     const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int l16 = lane & 15, lg = lane >> 4;
-    const int lid = xcd_block(blockIdx.x, gridDim.x), hk = lid % a.Hk, part = lid / a.Hk;
+    const int hk = blockIdx.x % a.Hk, part = blockIdx.x / a.Hk;
     const Part pt = find_part<256>(a.cache_len, a.batch, a.room, plan, part, false, s_red, &s_part);
     if (!pt.ok) return;
     const int b = pt.item, T = a.T, H = a.H, g = H / a.Hk, R = T * g;
@@ -403,12 +406,17 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
 }
 
 // ---------------------------------------------------------------- tiles
-// NW waves of 16 rows
+// NW waves of RW rows. Of a product's result, 16 x 16 or 32 x 32, a lane holds one
+// column in pieces of four rows: its element e is in row e / 4 * (4 G) + 4 g + e % 4,
+// with G = 64 / RW lanes per column, this lane the g-th of them.
 constexpr float kSlack = 8.f;  // of the exponents, powers of two
 
-template <int ND, bool E4M3, int NW>
-__global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(AttnArgs a, AttnPlan plan, AttnWorkspace ws, int row_blocks) {
-    constexpr int D = ND * 32, TH = 64 * NW, M = 16 * NW, kKs = D + 8, kVs = D + 16;
+template <int ND, bool E4M3, int NW, int RW>
+__global__ __launch_bounds__(64 * NW, RW == 32 ? 2 : 3) void attn_tiles_kernel(AttnArgs a, AttnPlan plan, AttnWorkspace ws, int row_blocks) {
+    typedef typename std::conditional<RW == 32, f32x16, f32x4>::type Acc;
+    constexpr int D = ND * 32, TH = 64 * NW, M = RW * NW, G = kWave / RW, NR = RW * RW / kWave;
+    constexpr int KS = 512 / RW;  // keys, or d, of one instruction
+    constexpr int kKs = D + 8, kVs = D + RW;
     __shared__ __attribute__((aligned(8))) int s_red[NW + 2];
     __shared__ Part s_part;
     __shared__ __attribute__((aligned(16))) uint16_t s_K[kTileKeys * kKs], s_V[kTileKeys * kVs];
@@ -418,9 +426,11 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
     __shared__ uint32_t s_odd[32];  // nodes whose values are not all finite
     extern __shared__ uint32_t s_anc[];  // [nodes of the block][words of T bits]
     const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int l16 = lane & 15, lg = lane >> 4;
-    const int lid = xcd_block(blockIdx.x, gridDim.x), reader = lid % plan.readers, part = lid / plan.readers;
-    const int hk = reader / row_blocks, rb = reader % row_blocks;
+    const int lr = lane & (RW - 1), lg = lane / RW;
+    // the row blocks that read one part of a key head run on one XCD; the parts
+    // that there are come first, so neighbours go to different ones
+    const int turn = blockIdx.x / 8, rb = turn % row_blocks, unit = turn / row_blocks * 8 + blockIdx.x % 8;
+    const int hk = unit % a.Hk, part = unit / a.Hk;
     const Part pt = find_part<TH>(a.cache_len, a.batch, a.room, plan, part, false, s_red, &s_part);
     if (!pt.ok) return;
     const int b = pt.item, T = a.T, H = a.H, g = H / a.Hk, R = T * g, row0 = rb * M;
@@ -434,12 +444,12 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
     if (tid < 32) s_odd[tid] = 0;
 
     // this lane's row
-    const int row = row0 + 16 * w + l16, node = min(row, R - 1) / g;
-    bf16x8 q[ND];
+    const int row = row0 + RW * w + lr, node = min(row, R - 1) / g;
+    bf16x8 q[D / KS];
     {
         const uint16_t* qp = (const uint16_t*)a.q + (((size_t)b * T + node) * H + hk * g + min(row, R - 1) % g) * D + 8 * lg;
 #pragma unroll
-        for (int i = 0; i < ND; ++i) q[i] = query_operand(a, gload((const uint4*)(qp + 32 * i)));
+        for (int i = 0; i < D / KS; ++i) q[i] = query_operand(a, gload((const uint4*)(qp + KS * i)));
     }
     const float c = score_factor(a);
     // The weights are 2^(c score - base). base is a maximum that moves, and all sums
@@ -447,74 +457,86 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
     // in fp32, and most tiles need neither their rows' maximum nor a rescaling
     // (moved for every new maximum: 164 us against 159, 32 trees of 63 nodes)
     float base = -FLT_MAX, l = 0.f;
-    f32x4 o[D / 16];
+    Acc o[D / RW];
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < D / RW; ++i) o[i] = Acc{};
 
     // One tile of keys in LDS, `limit` of them: scores, softmax, product. TREE: keys
     // j0 + ... of the tree, by ancestors
     auto take = [&](auto tree, int limit, int j0) {
         constexpr bool TREE = decltype(tree)::value, SCALED = E4M3 && !TREE;
-        f32x4 s[4];
+        constexpr int NX = kTileKeys / RW;
+        Acc s[NX];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) s[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int x = 0; x < NX; ++x) s[x] = Acc{};
         // (fences: the compiler would read all of K, or of V, into registers first)
 #pragma unroll
-        for (int i = 0; i < ND; ++i) {
+        for (int i = 0; i < D / KS; ++i) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) s[x] = mma(*(const bf16x8*)&s_K[(16 * x + l16) * kKs + 32 * i + 8 * lg], q[i], s[x]);
-            if (i % 2) __builtin_amdgcn_sched_barrier(0);
+            for (int x = 0; x < NX; ++x) s[x] = mma(*(const bf16x8*)&s_K[(RW * x + lr) * kKs + KS * i + 8 * lg], q[i], s[x]);
+            if ((i + 1) * NX % 8 == 0) __builtin_amdgcn_sched_barrier(0);
         }
+        float sc[RW];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            if (SCALED) s[x] *= *(const f32x4*)&s_ks[16 * x + 4 * lg];
+        for (int e = 0; e < RW; ++e) sc[e] = s[e / NR][e % NR];
+#pragma unroll
+        for (int e = 0; e < RW; e += 4) {
+            const int j = e * G + 4 * lg;  // the key of element e
+            if (SCALED) {
+                const f32x4 ks = *(const f32x4*)&s_ks[j];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sc[e + r] *= ks[r];
+            }
             if (TREE) {
-                const int j = 16 * x + 4 * lg;
                 const uint32_t bits = s_anc[(node - first) * words + min((j0 + j) / 32, words - 1)] >> ((j0 + j) % 32);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) s[x][r] = j + r < limit && (bits >> r & 1) ? s[x][r] : -INFINITY;
+                for (int r = 0; r < 4; ++r) sc[e + r] = j + r < limit && (bits >> r & 1) ? sc[e + r] : -INFINITY;
             }
         }
         if (!TREE && limit < kTileKeys) {
             const int left = limit - 4 * lg;
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) s[x][r] = 16 * x + r < left ? s[x][r] : -INFINITY;
+            for (int e = 0; e < RW; ++e) sc[e] = e / 4 * 4 * G + e % 4 < left ? sc[e] : -INFINITY;
         }
-        const float mx = max3(max3(max3(s[0][0], s[0][1], s[0][2]), s[0][3], s[1][0]),
-                              max3(max3(s[1][1], s[1][2], s[1][3]), s[2][0], s[2][1]),
-                              max3(max3(s[2][2], s[2][3], s[3][0]), max3(s[3][1], s[3][2], s[3][3]), s[3][3]));
+        float mx = max3(sc[0], sc[1], sc[2]), my = max3(sc[3], sc[4], sc[5]);
+#pragma unroll
+        for (int e = 6; e < RW - 2; e += 4) {
+            mx = max3(mx, sc[e], sc[e + 1]);
+            my = max3(my, sc[e + 2], sc[e + 3]);
+        }
+        mx = max3(mx, my, sc[RW - 2]);
+        mx = max3(mx, sc[RW - 1], mx);
         if (__ballot(fmaf(mx, c, -base) > kSlack)) {
-            const float to = max3(row_max(mx) * c, base, base), al = __builtin_amdgcn_exp2f(base - to);
+            const float to = max3(row_max<RW>(mx) * c, base, base), al = __builtin_amdgcn_exp2f(base - to);
             l *= al;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) o[i] *= al;
+            for (int i = 0; i < D / RW; ++i) o[i] *= al;
             base = to;
         }
-        uint32_t u[8];
+        uint32_t u[RW / 2];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int e = 0; e < RW; e += 4) {
             f32x4 p;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                p[r] = __builtin_amdgcn_exp2f(fmaf(s[x][r], c, -base));
-                l += p[r];  // of this lane's keys; the four lanes of a row meet at the end
+                p[r] = __builtin_amdgcn_exp2f(fmaf(sc[e + r], c, -base));
+                l += p[r];  // of this lane's keys; the lanes of a row meet at the end
             }
             if (SCALED) {
-                const f32x4 vs = *(const f32x4*)&s_vs[16 * x + 4 * lg];
+                const f32x4 vs = *(const f32x4*)&s_vs[e * G + 4 * lg];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) p[r] *= vs[r];  // a key past the last one has the last one's
             }
-            u[2 * x] = pack_bf16x2(p[0], p[1]);
-            u[2 * x + 1] = pack_bf16x2(p[2], p[3]);
+            u[e / 2] = pack_bf16x2(p[0], p[1]);
+            u[e / 2 + 1] = pack_bf16x2(p[2], p[3]);
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < kTileKeys / KS; ++x) {
             const bf16x8 pf = as_operand(make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]));
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const bf16x8 v = read_columns(&s_V[32 * x * kVs + 16 * i], kVs, lane);
+            for (int i = 0; i < D / RW; ++i) {
+                const uint16_t* tile = &s_V[KS * x * kVs + RW * i];
+                const bf16x8 v = RW == 32 ? read_columns32(tile, kVs, lane) : read_columns(tile, kVs, lane);
                 o[i] = mma(v, pf, o[i]);
                 if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
@@ -551,7 +573,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
             if (!s_odd[x]) continue;
             for (int j = 0; j < 32; ++j)
                 if (s_odd[x] & s_anc[(node - first) * words + x] & (1u << j))
-                    add_nonfinite<D / 16>(vp + (size_t)(32 * x + j) * stride + 4 * lg, o);
+                    add_nonfinite<D / RW, 4 * G>(vp + (size_t)(32 * x + j) * stride + 4 * lg, o);
         }
     };
 
@@ -629,20 +651,23 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
         take_tree();
     }
     st |= __syncthreads_or(bad) ? kStBadCache : 0;
-    if (reader == 0 && tid == 0) {
+    if (hk == 0 && rb == 0 && tid == 0) {
         if (pt.n > 1)
             ws.bits[part] = st;
         else if (a.status)
             a.status[b] = st;
     }
     if (pt.n == 1 && st) return;
-    l = row_sum(l);
+    l = row_sum<RW>(l);
     if (row >= R) return;
     const size_t at = (size_t)node * H + hk * g + row % g;
     if (pt.n > 1) {
         float* to = ws.o + ((size_t)part * T * H + at) * D + 4 * lg;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) *(f32x4*)(to + 16 * i) = o[i];
+        for (int e = 0; e < D / G; e += 4) {
+            const Acc& v = o[e / NR];
+            *(f32x4*)(to + e * G) = f32x4{v[e % NR], v[e % NR + 1], v[e % NR + 2], v[e % NR + 3]};
+        }
         if (lg == 0) {
             ws.ml[((size_t)part * T * H + at) * 2] = base;
             ws.ml[((size_t)part * T * H + at) * 2 + 1] = l;
@@ -651,15 +676,18 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 4 : 3) void attn_tiles_kernel(At
         const float inv = 1.f / l;
         uint16_t* to = (uint16_t*)a.o + ((size_t)b * T * H + at) * D + 4 * lg;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-            gstore((uint2*)(to + 16 * i),
-                   make_uint2(pack_bf16x2(o[i][0] * inv, o[i][1] * inv), pack_bf16x2(o[i][2] * inv, o[i][3] * inv)));
+        for (int e = 0; e < D / G; e += 4) {
+            const Acc& v = o[e / NR];
+            gstore((uint2*)(to + e * G), make_uint2(pack_bf16x2(v[e % NR] * inv, v[e % NR + 1] * inv),
+                                                    pack_bf16x2(v[e % NR + 2] * inv, v[e % NR + 3] * inv)));
+        }
     }
 }
 
 template <int ND, bool E4M3>
 void launch_nd(const AttnArgs& a, const AttnPlan& p, const AttnWorkspace& ws, int block_rows, int row_blocks, hipStream_t stream) {
-    const dim3 grid((unsigned)((long long)p.parts * p.readers));
+    const long long units = (long long)p.parts * a.Hk;
+    const dim3 grid((unsigned)(block_rows == 16 ? units : (units + 7) / 8 * 8 * row_blocks));
     const int g = a.H / a.Hk;
     const unsigned words = (a.T + 31) / 32;
     const unsigned nodes = min(a.T, (block_rows + g - 2) / g + 1);
@@ -667,9 +695,9 @@ void launch_nd(const AttnArgs& a, const AttnPlan& p, const AttnWorkspace& ws, in
     if (block_rows == 16)
         hipLaunchKernelGGL((attn_rows_kernel<ND, E4M3>), grid, dim3(256), 0, stream, a, p, ws);
     else if (block_rows == 64)
-        hipLaunchKernelGGL((attn_tiles_kernel<ND, E4M3, 4>), grid, dim3(256), lds, stream, a, p, ws, row_blocks);
+        hipLaunchKernelGGL((attn_tiles_kernel<ND, E4M3, 4, 16>), grid, dim3(256), lds, stream, a, p, ws, row_blocks);
     else
-        hipLaunchKernelGGL((attn_tiles_kernel<ND, E4M3, 8>), grid, dim3(512), lds, stream, a, p, ws, row_blocks);
+        hipLaunchKernelGGL((attn_tiles_kernel<ND, E4M3, 4, 32>), grid, dim3(256), lds, stream, a, p, ws, row_blocks);
 }
 
 }  // namespace

@@ -394,7 +394,7 @@ long long attn_verify_blocks(const tsv_attn_shape* s) {
     for (int matrix = 0; matrix <= (int)matrix_shape(s); ++matrix) {
         int br, rb;
         const AttnPlan p = plan_of(s, matrix, &br, &rb);
-        const long long n = (long long)p.parts * p.readers;
+        const long long n = (long long)p.parts * p.readers + 8 * rb;  // (the tile kernel rounds its units up to eight)
         if (n > most) most = n;
     }
     return most;
