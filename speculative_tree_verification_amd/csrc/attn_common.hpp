@@ -31,22 +31,23 @@ __device__ __forceinline__ int page_of(int n, PageDiv d) { return (int)(((uint64
 // the long ones are: the parts are of equal length whatever the table's room.
 // Every work-group computes the same cut from cache_len. The number of parts
 // is at most `want` over the readers plus one for each item.
-constexpr int kAttnWant = 1024;  // about four work-groups for each of the 256 compute units
 constexpr int kAttnMinKeys = 128;
 
 struct AttnPlan {
     int readers;   // work-groups that read one part
+    int want;      // work-groups wanted
     int min_keys;  // smallest part
     int parts;     // upper bound of parts over all items
     bool split;    // whether an item may have more than one
 };
 
-inline AttnPlan attn_plan(int batch, long long room, int readers, int min_keys) {
+inline AttnPlan attn_plan(int batch, long long room, int readers, int min_keys, int want) {
     AttnPlan p;
     p.readers = readers;
+    p.want = want;
     p.min_keys = min_keys;
     p.split = room > min_keys;
-    p.parts = batch + (p.split ? kAttnWant / readers : 0);
+    p.parts = batch + (p.split ? want / readers : 0);
     return p;
 }
 
@@ -73,7 +74,7 @@ inline AttnWorkspace attn_workspace(void* ws, const AttnPlan& p, int T, int H, i
 __device__ __forceinline__ int usable_len(int len, int room) { return len < 0 || len > room ? 0 : len; }
 
 __device__ __forceinline__ int part_keys(const AttnPlan& plan, unsigned long long sum) {
-    const unsigned long long want = (sum * plan.readers + kAttnWant - 1) / kAttnWant;
+    const unsigned long long want = (sum * plan.readers + plan.want - 1) / plan.want;
     return max((int)min((want + 63) / 64 * 64, 0x40000000ull), plan.min_keys);
 }
 

@@ -202,13 +202,16 @@ __global__ __launch_bounds__(256) void attn_plain_kernel(AttnArgs a, AttnPlan pl
     }
 }
 
-// Lanes take 4 elements of a row each, so a wave reads PW = 64 / LPR parts at
-// once, four times that before it adds; the parts' maxima and sums are a lane's
-// each, 64 at a time, with a running maximum over them. Many rows go to a wave
-// each, RW one after another where that leaves enough work-groups (the search for
-// the item's parts costs as much as a row: 66 -> 37 us for the 63-node trees of
-// 32 items); of few rows (one new token over a long cache, 128 parts) each has a
-// work-group, whose waves split its parts (RW 0: 38 -> 10 us).
+// Lanes take 4 elements of a row each, LPR lanes a row.
+//   RW 0  few rows (one new token over a long cache: up to 130 parts): each has a
+//         work-group, whose waves split its parts (38 -> 7 us)
+//   RW 1  each has a wave, which reads PW = 64 / LPR parts at once, four times
+//         that before it adds; the parts' maxima and sums are a lane's each, 64 at
+//         a time, with a running maximum over them
+//   RW 4  many rows: few parts each, and the work per row counts. LPR lanes read
+//         the row's parts by themselves, four at once, for RW rows one after
+//         another (the search for the item's parts costs as much as a row). 64512
+//         rows of 1 to 6 parts: 16 us, and 34 us read as by RW 1
 template <typename TIO, int LPR, int RW>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnPlan plan, AttnWorkspace ws, int blocks) {
     constexpr int PW = kWave / LPR;
@@ -231,6 +234,62 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnPlan pla
     }
     if (rb == 0 && tid == 0 && a.status) a.status[pt.item] = 0;
     const int d = lane % LPR * 4, sub = lane / LPR;
+    const bool whole = D % 4 == 0 && (uintptr_t)a.o % (4 * sizeof(TIO)) == 0;  // pieces of four, aligned
+    auto piece = [&](const float* p) { return d >= D ? make_float4(0.f, 0.f, 0.f, 0.f) : whole ? ld4<true>(p, 4) : ld4<false>(p, D - d); };
+    auto finish = [&](int row, float4 o, float l) {
+        const float f[4] = {o.x / l, o.y / l, o.z / l, o.w / l};
+        TIO* to = (TIO*)a.o + ((size_t)pt.item * rows + row) * D + d;
+        if (whole && d < D) {
+            if constexpr (sizeof(TIO) == 4)
+                *(float4*)to = make_float4(f[0], f[1], f[2], f[3]);
+            else
+                *(uint2*)to = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (d + e < D) Elem<TIO>::st(to, e, f[e]);
+        }
+    };
+    if (RW > 1) {
+        for (int i = 0; i < RW; ++i) {
+            const int row = ((rb * 4 + w) * RW + i) * PW + sub;
+            if (row >= rows) return;
+            const float* ml = ws.ml + ((size_t)pt.base * rows + row) * 2;
+            const float* po = ws.o + ((size_t)pt.base * rows + row) * D + d;
+            float m = -INFINITY, l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k0 = 0; k0 < n; k0 += 4) {
+                float mk[4], lk[4];
+                float4 v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    mk[u] = -INFINITY;
+                    lk[u] = 0.f;
+                    v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k0 + u >= n) continue;
+                    mk[u] = ml[(size_t)(k0 + u) * rows * 2];
+                    lk[u] = ml[(size_t)(k0 + u) * rows * 2 + 1];
+                    v[u] = piece(po + (size_t)(k0 + u) * rows * D);
+                }
+                const float mn = fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), m);
+                const float base = mn == -INFINITY ? 0.f : mn, old = exp2f(m - base);
+                l *= old;
+                o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float f = exp2f(mk[u] - base);
+                    l = fmaf(f, lk[u], l);
+                    o.x = fmaf(f, v[u].x, o.x);
+                    o.y = fmaf(f, v[u].y, o.y);
+                    o.z = fmaf(f, v[u].z, o.z);
+                    o.w = fmaf(f, v[u].w, o.w);
+                }
+                m = mn;
+            }
+            finish(row, o, l);
+        }
+        return;
+    }
     const int per = SHARED ? (n + 3) / 4 : n, first = SHARED ? w * per : 0, end = min(n, first + per);
     for (int i = 0; i < (SHARED ? 1 : RW); ++i) {
         const int row = SHARED ? rb : (rb * 4 + w) * RW + i;
@@ -264,7 +323,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnPlan pla
                 for (int u = 0; u < 4; ++u) {
                     const int k = k0 + u * PW + sub;
                     v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (k < cnt && d < D) v[u] = ld4<false>(po + (size_t)(c0 + k) * rows * D, D - d);
+                    if (k < cnt) v[u] = piece(po + (size_t)(c0 + k) * rows * D);
                     f[u] = __shfl(al, min(k, kWave - 1), kWave);
                 }
 #pragma unroll
@@ -307,13 +366,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnPlan pla
                 o.w = fmaf(f, t.w, o.w);
             }
         }
-        if (sub == 0) {
-            const float f[4] = {o.x / l, o.y / l, o.z / l, o.w / l};
-            TIO* to = (TIO*)a.o + ((size_t)pt.item * rows + row) * D + d;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (d + e < D) Elem<TIO>::st(to, e, f[e]);
-        }
+        if (sub == 0) finish(row, o, l);
     }
 }
 
@@ -332,8 +385,9 @@ template <typename TIO, int LPR>
 void launch_join_lpr(const AttnArgs& a, const AttnPlan& p, const AttnWorkspace& ws, hipStream_t stream) {
     const int rows = a.T * a.H;
     const long long all = (long long)a.batch * rows;
-    const int rw = all <= kAttnWant ? 0 : all <= 16 * kAttnWant ? 1 : 4;
-    const int blocks = rw == 0 ? rows : (rows + 4 * rw - 1) / (4 * rw);
+    const int rw = all <= 1024 ? 0 : all <= 16384 ? 1 : 4;
+    const int per = rw == 4 ? 16 * (kWave / LPR) : rw == 1 ? 4 : 1;  // rows of a work-group
+    const int blocks = (rows + per - 1) / per;
     const dim3 grid((unsigned)((long long)a.batch * blocks));
     if (rw == 0)
         hipLaunchKernelGGL((attn_join_kernel<TIO, LPR, 0>), grid, dim3(256), 0, stream, a, p, ws, blocks);
@@ -370,10 +424,28 @@ int block_rows_of(const tsv_attn_shape* s, bool matrix) {
     return r128 * 5 > r64 * 6 ? 64 : 128;
 }
 
+// Work-groups wanted, for x of them that would run without any split (an item's
+// last part is half empty on average, so about want + x / 2 parts are whole).
+//   tiles  two fit a compute unit: whole rounds of 512, so that no round is nearly
+//          empty, with want at least x (32 trees of 63 nodes, x = 512: 153 us for
+//          512, 133 for 768, 138 for 1024, and the join rises with want). From
+//          1024 on the items fill the GPU, and only the longest are cut.
+//   rows   few parts while they fill one round, for the join's sake (a cache of
+//          65533, x = 8: 58 us for 512, 62 for 1024), small ones where many
+//          items of different lengths share the GPU (64 items, x = 512: 122 us for
+//          1024, 118 for 2048)
+int want_of(bool matrix, int block_rows, long long x) {
+    if (!matrix) return 1024;
+    if (block_rows == 16) return x <= 128 ? 512 : x >= 512 ? 2048 : (int)(4 * x);
+    return x >= 1024 ? 1024 : (int)((3 * x / 2 + 511) / 512 * 512 - x / 2);
+}
+
 AttnPlan plan_of(const tsv_attn_shape* s, bool matrix, int* block_rows, int* row_blocks) {
     *block_rows = block_rows_of(s, matrix);
     *row_blocks = (int)(((long long)s->n_nodes * (s->n_heads / s->n_kv_heads) + *block_rows - 1) / *block_rows);
-    return attn_plan(s->batch, (long long)s->max_pages * s->page_size, s->n_kv_heads * *row_blocks, kAttnMinKeys);
+    const int readers = s->n_kv_heads * *row_blocks;
+    return attn_plan(s->batch, (long long)s->max_pages * s->page_size, readers, kAttnMinKeys,
+                     want_of(matrix, *block_rows, (long long)s->batch * readers));
 }
 
 }  // namespace
