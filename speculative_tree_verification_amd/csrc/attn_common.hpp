@@ -39,6 +39,7 @@ struct AttnPlan {
     int min_keys;  // smallest part
     int parts;     // upper bound of parts over all items
     bool split;    // whether an item may have more than one
+    bool sorted;   // work-groups take the whole parts first, then the items' last ones by falling length
 };
 
 inline AttnPlan attn_plan(int batch, long long room, int readers, int min_keys, int want) {
@@ -47,6 +48,7 @@ inline AttnPlan attn_plan(int batch, long long room, int readers, int min_keys, 
     p.want = want;
     p.min_keys = min_keys;
     p.split = room > min_keys;
+    p.sorted = false;
     p.parts = batch + (p.split ? want / readers : 0);
     return p;
 }
@@ -88,7 +90,7 @@ struct Part {
     int keys;      // positions per part
 };
 
-// The part `want` (or, with by_item, part 0 of item `want`), the same in all
+// The part whose turn is `want` (or, with by_item, part 0 of item `want`), the same in all
 // NT threads. May act as a barrier. s_red: NT / 64 + 2 ints,
 // 8-byte aligned; s_out: one Part.
 template <int NT>
@@ -105,22 +107,33 @@ __device__ __forceinline__ Part find_part(const int32_t* __restrict__ cache_len,
             keys = part_keys(plan, sum);
         }
         const int cnt = lane < batch ? max(1, (len + keys - 1) / keys) : 0;
-        int upto = cnt;
+        const int first = plan.sorted && lane < batch ? cnt - 1 : cnt;  // the parts in the items' order
+        int upto = first;
 #pragma unroll
         for (int m = 1; m < kWave; m <<= 1) {
             const int o = __shfl_up(upto, m, kWave);
             if (lane >= m) upto += o;
         }
-        const int base = upto - cnt;
-        const bool mine = lane < batch && (by_item ? lane == want : want >= base && want < upto);
+        const int turn = upto - first, base = plan.sorted ? turn + lane : turn;
+        const int late = want - __builtin_amdgcn_readlane(upto, kWave - 1);  // place among the last parts
+        bool mine = lane < batch && (by_item ? lane == want : want >= turn && want < upto);
+        if (plan.sorted && !by_item && late >= 0) {
+            const int rest = len - (cnt - 1) * keys;
+            int rank = 0;
+            for (int j = 0; j < batch; ++j) {
+                const int other = __builtin_amdgcn_readlane(rest, j);
+                rank += other > rest || (other == rest && j < lane);
+            }
+            mine = lane < batch && rank == late;
+        }
         const unsigned long long who = __ballot(mine);
         Part p;
         p.ok = who != 0;
         const int src = who ? __builtin_ctzll(who) : 0;
         p.item = src;
         p.base = __builtin_amdgcn_readlane(base, src);
-        p.k = by_item ? 0 : want - p.base;
         p.n = __builtin_amdgcn_readlane(cnt, src);
+        p.k = by_item ? 0 : plan.sorted && late >= 0 ? p.n - 1 : want - __builtin_amdgcn_readlane(turn, src);
         p.len = __builtin_amdgcn_readlane(len, src);
         p.bad_len = __builtin_amdgcn_readlane(raw, src) != p.len;
         p.keys = keys;
