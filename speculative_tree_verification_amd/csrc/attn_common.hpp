@@ -90,6 +90,22 @@ struct Part {
     int keys;      // positions per part
 };
 
+// The same in scalar registers
+__device__ __forceinline__ Part uniform(const Part& p) {
+    Part u;
+#define TSV_U(f) u.f = __builtin_amdgcn_readfirstlane(p.f)
+    TSV_U(ok);
+    TSV_U(item);
+    TSV_U(k);
+    TSV_U(n);
+    TSV_U(base);
+    TSV_U(len);
+    TSV_U(bad_len);
+    TSV_U(keys);
+#undef TSV_U
+    return u;
+}
+
 // The part whose turn is `want` (or, with by_item, part 0 of item `want`), the same in all
 // NT threads. May act as a barrier. s_red: NT / 64 + 2 ints,
 // 8-byte aligned; s_out: one Part.

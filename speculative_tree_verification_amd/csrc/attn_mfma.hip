@@ -431,8 +431,9 @@ __global__ __launch_bounds__(64 * NW, RW == 32 ? 2 : 3) void attn_tiles_kernel(A
     // that there are come first, so neighbours go to different ones
     const int turn = blockIdx.x / 8, rb = turn % row_blocks, unit = turn / row_blocks * 8 + blockIdx.x % 8;
     const int hk = unit % a.Hk;
-    const Part pt = find_part<TH>(a.cache_len, a.batch, a.room, plan, unit / a.Hk, false, s_red, &s_part);
+    Part pt = find_part<TH>(a.cache_len, a.batch, a.room, plan, unit / a.Hk, false, s_red, &s_part);
     if (!pt.ok) return;
+    pt = uniform(pt);
     const int part = pt.base + pt.k;
     const int b = pt.item, T = a.T, H = a.H, g = H / a.Hk, R = T * g, row0 = rb * M;
     const bool last = pt.k == pt.n - 1;
