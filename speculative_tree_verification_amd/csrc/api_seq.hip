@@ -5,7 +5,7 @@
 #include <math.h>
 
 #include "attn_common.hpp"
-#include "launch.hpp"
+#include "seq_launch.hpp"
 
 namespace {
 

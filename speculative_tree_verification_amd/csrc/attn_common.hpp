@@ -4,7 +4,7 @@
 #include <type_traits>
 
 #include "common.hpp"
-#include "launch.hpp"
+#include "seq_launch.hpp"
 
 namespace tsv {
 

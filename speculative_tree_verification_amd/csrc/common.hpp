@@ -115,7 +115,6 @@ struct Elem;
 template <>
 struct Elem<float> {
     static __device__ __forceinline__ float ld(const float* p, size_t i) { return gload(p + i); }
-    static __device__ __forceinline__ float up(float v) { return v; }
     static __device__ __forceinline__ void st(float* p, size_t i, float v) { gstore(p + i, v); }
 };
 
@@ -124,7 +123,6 @@ struct Elem<uint16_t> {
     static __device__ __forceinline__ float ld(const uint16_t* p, size_t i) {
         return bf16_bits_to_f32(gload(p + i));
     }
-    static __device__ __forceinline__ float up(uint16_t v) { return bf16_bits_to_f32(v); }
     static __device__ __forceinline__ void st(uint16_t* p, size_t i, float v) {
         gstore(p + i, f32_to_bf16_bits(v));
     }

@@ -90,16 +90,16 @@ __global__ __launch_bounds__(256) void prefill_plain_kernel(PrefillArgs a, SeqPl
         for (int i = 0; i < BI; ++i) {
             const int e = tid + i * 256, t = e / (4 * NS), n = e % (4 * NS);
             const bool in = t < cnt && n < N;
-            s_B[t][n] = in ? Elem<TIO>::up(rB[i]) : 0.f;
-            if (!LOCAL) s_C[t][n] = in ? Elem<TIO>::up(rC[i]) : 0.f;
+            s_B[t][n] = in ? to_f32(rB[i]) : 0.f;
+            if (!LOCAL) s_C[t][n] = in ? to_f32(rC[i]) : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
             const int e = tid + i * 256, t = e / kWave, q = pb * kWave + e % kWave;
-            s_x[t][e % kWave] = t < cnt && q < P ? Elem<TIO>::up(rx[i]) : 0.f;
+            s_x[t][e % kWave] = t < cnt && q < P ? to_f32(rx[i]) : 0.f;
         }
         if (tid < cnt) {
-            const float dt = Elem<TIO>::up(rdt);
+            const float dt = to_f32(rdt);
             s_dt[tid] = dt;
             s_da[tid] = dt * Ah;
             s_dec[tid] = expf(dt * Ah);

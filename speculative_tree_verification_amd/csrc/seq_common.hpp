@@ -14,7 +14,7 @@
 #pragma once
 
 #include "common.hpp"
-#include "launch.hpp"
+#include "seq_launch.hpp"
 
 namespace tsv {
 
@@ -75,6 +75,9 @@ __device__ __forceinline__ void place_block(const SeqPlan& plan, int HB, int* sl
         *hb = lid % HB;
     }
 }
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(uint16_t bf16) { return bf16_bits_to_f32(bf16); }
 
 // The states of all slots, then the log-decay sums.
 struct SeqWorkspace {

@@ -10,7 +10,7 @@
 // used, and the state streams past the caches (nontemporal), which it would
 // only sweep. The sum over n is a butterfly over the row's lanes.
 #include "common.hpp"
-#include "launch.hpp"
+#include "seq_launch.hpp"
 
 namespace tsv {
 namespace {
