@@ -21,26 +21,56 @@ struct Quad {
     float v[8];
 };
 
+// A row's piece as it is loaded
 template <typename TIO, bool VEC>
-__device__ __forceinline__ Quad load8(const TIO* p, int rem) {
-    Quad q;
-    if (VEC) {
-        if (sizeof(TIO) == 2) {
-            const uint4 u = gload((const uint4*)p);
-            const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
+struct Raw {
+    TIO e[8];
+};
+template <>
+struct Raw<uint16_t, true> {
+    uint4 u;
+};
+template <>
+struct Raw<float, true> {
+    float4 a, b;
+};
+
+template <typename TIO, bool VEC>
+__device__ __forceinline__ Raw<TIO, VEC> load8(const TIO* p, int rem) {
+    Raw<TIO, VEC> q;
+    if constexpr (!VEC) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                q.v[2 * i] = __uint_as_float(wd[i] << 16);
-                q.v[2 * i + 1] = __uint_as_float(wd[i] & 0xffff0000u);
-            }
-        } else {
-            const float4 a = gload((const float4*)p), b = gload((const float4*)p + 1);
-            q.v[0] = a.x; q.v[1] = a.y; q.v[2] = a.z; q.v[3] = a.w;
-            q.v[4] = b.x; q.v[5] = b.y; q.v[6] = b.z; q.v[7] = b.w;
+        for (int i = 0; i < 8; ++i) q.e[i] = i < rem ? gload(p + i) : TIO(0);
+    } else if constexpr (sizeof(TIO) == 2) {
+        q.u = gload((const uint4*)p);
+    } else {
+        q.a = gload((const float4*)p);
+        q.b = gload((const float4*)p + 1);
+    }
+    return q;
+}
+
+template <typename TIO, bool VEC>
+__device__ __forceinline__ Quad floats(const Raw<TIO, VEC>& r) {
+    Quad q;
+    if constexpr (!VEC) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(TIO) == 2)
+                q.v[i] = bf16_bits_to_f32(r.e[i]);
+            else
+                q.v[i] = r.e[i];
+        }
+    } else if constexpr (sizeof(TIO) == 2) {
+        const uint32_t wd[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            q.v[2 * i] = __uint_as_float(wd[i] << 16);
+            q.v[2 * i + 1] = __uint_as_float(wd[i] & 0xffff0000u);
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q.v[i] = i < rem ? Elem<TIO>::ld(p, i) : 0.f;
+        q.v[0] = r.a.x; q.v[1] = r.a.y; q.v[2] = r.a.z; q.v[3] = r.a.w;
+        q.v[4] = r.b.x; q.v[5] = r.b.y; q.v[6] = r.b.z; q.v[7] = r.b.w;
     }
     return q;
 }
@@ -145,48 +175,49 @@ __device__ __forceinline__ long long cache_place(const CacheWriteArgs& a, int b,
     return (long long)pg * a.Hk * a.page_size + (pos - page * a.page_size);
 }
 
-// n rows, keys and values of all heads: source rows s_src, places s_dst (-1: not
-// written). A thread has its pieces of four rows of a head under way at once.
-constexpr int kAtOnce = 4;
-template <typename TIO, int LPR, bool E4M3, bool VEC>
-__device__ __forceinline__ void write_rows(const CacheWriteArgs& a, int n, const long long* s_src, const long long* s_dst) {
-    const int lane = threadIdx.x % LPR, d = lane * 8, rem = a.D - d;
-    const int per = 256 / LPR, work = n * a.Hk * 2;
-    for (int u0 = threadIdx.x / LPR; u0 - (int)threadIdx.x / LPR < work; u0 += kAtOnce * per) {
-        Quad q[kAtOnce];
-        long long at[kAtOnce];
-        bool value[kAtOnce];
+// n rows, keys and values of all heads, LPR lanes a row of a head, 256 / LPR such
+// rows, heads fastest, in a step; `fetch` loads a thread's pieces of K steps from
+// u0 on (source row src(row); negative: none), `flush` writes them to s_dst (-1:
+// not written).
+template <typename TIO, int LPR, bool VEC, int K, class Src>
+__device__ __forceinline__ void fetch(const CacheWriteArgs& a, int n, int u0, Src src, Raw<TIO, VEC> (&q)[K]) {
+    const int d = threadIdx.x % LPR * 8, rem = a.D - d;
 #pragma unroll
-        for (int x = 0; x < kAtOnce; ++x) {
-            const int u = u0 + x * per;  // row, k or v, head: heads fastest
-            const bool in = u < work;
-            const int row = in ? page_of(u, a.heads) : 0, hv = in ? u - row * 2 * a.Hk : 0;
-            value[x] = hv >= a.Hk;
-            const int hk = value[x] ? hv - a.Hk : hv;
-            at[x] = in && rem > 0 ? s_dst[row] : -1;
+    for (int x = 0; x < K; ++x) {
+        const int u = u0 + x * (256 / LPR);
+        const bool in = u < n * a.Hk * 2;
+        const int row = in ? page_of(u, a.heads) : 0, hv = in ? u - row * 2 * a.Hk : 0;
+        const bool value = hv >= a.Hk;
+        const long long r = in && rem > 0 ? src(row) : -1;
+        q[x] = Raw<TIO, VEC>{};
+        if (r >= 0) q[x] = load8<TIO, VEC>((const TIO*)(value ? a.v : a.k) + ((size_t)r * a.Hk + (value ? hv - a.Hk : hv)) * a.D + d, rem);
+    }
+}
+template <typename TIO, int LPR, bool E4M3, bool VEC, int K>
+__device__ __forceinline__ void flush(const CacheWriteArgs& a, int n, int u0, const long long* s_dst, const Raw<TIO, VEC> (&q)[K]) {
+    const int d = threadIdx.x % LPR * 8, rem = a.D - d;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[x].v[i] = 0.f;
-            if (at[x] >= 0) {
-                at[x] += (long long)hk * a.page_size;
-                q[x] = load8<TIO, VEC>((const TIO*)(value[x] ? a.v : a.k) + ((size_t)s_src[row] * a.Hk + hk) * a.D + d, rem);
-            }
+    for (int x = 0; x < K; ++x) {
+        const int u = u0 + x * (256 / LPR);
+        const bool in = u < n * a.Hk * 2;
+        const int row = in ? page_of(u, a.heads) : 0, hv = in ? u - row * 2 * a.Hk : 0;
+        const bool value = hv >= a.Hk;
+        const long long at = in && rem > 0 ? s_dst[row] : -1;
+        const Quad f = floats<TIO, VEC>(q[x]);
+        float scale = 1.f;
+        bool finite = true;
+        if (E4M3) {
+            // magnitudes compare as their bits do; an infinity or a NaN is above all
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f.v[i]) & 0x7fffffffu);
+#pragma unroll
+            for (int m = 1; m < LPR; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m, kWave));
+            finite = top < 0x7f800000u;
+            scale = finite ? fmaxf(__uint_as_float(top) / 448.f, 1.17549435e-38f) : __uint_as_float(0x7fc00000u);
         }
-#pragma unroll
-        for (int x = 0; x < kAtOnce; ++x) {
-            float scale = 1.f;
-            bool finite = true;
-            if (E4M3) {
-                // magnitudes compare as their bits do; an infinity or a NaN is above all
-                uint32_t top = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(q[x].v[i]) & 0x7fffffffu);
-#pragma unroll
-                for (int m = 1; m < LPR; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m, kWave));
-                finite = top < 0x7f800000u;
-                scale = finite ? fmaxf(__uint_as_float(top) / 448.f, 1.17549435e-38f) : __uint_as_float(0x7fc00000u);
-            }
-            if (at[x] >= 0) store8<TIO, E4M3, VEC>(a, value[x], (size_t)at[x], d, rem, q[x], scale, finite);
-        }
+        if (at >= 0)
+            store8<TIO, E4M3, VEC>(a, value, (size_t)(at + (long long)(value ? hv - a.Hk : hv) * a.page_size), d, rem, f, scale, finite);
     }
 }
 
@@ -196,14 +227,21 @@ constexpr int kRows = 16, kPathRows = 2;
 
 template <typename TIO, int LPR, bool E4M3, bool VEC>
 __global__ __launch_bounds__(256) void append_kernel(CacheWriteArgs a, int row_blocks) {
-    __shared__ long long s_src[kRows], s_dst[kRows];
-    __shared__ int s_item[kRows], s_pos[kRows], s_place[kRows], s_bad[kRows], s_long[kRows], s_first;
+    __shared__ long long s_dst[kRows];
+    __shared__ int s_item[kRows], s_pos[kRows], s_place[kRows], s_bad[kRows], s_long[kRows], s_first, s_red[4];
     const int tid = threadIdx.x;
     // the packing, and the sequence of this block's first row: the sequences
     // that end at or before it
     const int r0 = blockIdx.x * kRows;
+    const bool rows = (int)blockIdx.x < row_blocks;
+    const int n = rows ? min(kRows, a.T - r0) : 0;
+    // the rows are on their way while their places are found
+    constexpr int K = VEC && sizeof(TIO) == 2 ? 8 : 4, kStep = K * (256 / LPR);
+    Raw<TIO, VEC> q[K];
+    const auto src = [&](int row) { return (long long)r0 + row; };
+    fetch<TIO, LPR, VEC>(a, n, tid / LPR, src, q);
     if (tid == 0) s_first = 0;
-    __syncthreads();
+    lds_barrier();
     int bad = 0, before = 0;
     for (int q = tid; q < a.batch; q += 256) {
         const int lo = a.seq_start[q], hi = a.seq_start[q + 1];
@@ -211,26 +249,24 @@ __global__ __launch_bounds__(256) void append_kernel(CacheWriteArgs a, int row_b
         before += hi <= r0;
     }
     if (before) atomicAdd(&s_first, before);
-    bad = __syncthreads_or(bad);
-    if ((int)blockIdx.x >= row_blocks) {  // a block for each item's status
+    bad = lds_sync_or<256>(bad, s_red);
+    if (!rows) {  // a block for each item's status
         const int b = blockIdx.x - row_blocks;
         const int st = bad ? kStBadSeqRows : check_pages(a, b, a.seq_start[b + 1] - a.seq_start[b]);
         if (tid == 0) a.status[b] = st;
         return;
     }
     if (bad) return;
-    const int n = min(kRows, a.T - r0);
     if (tid < kRows) {
-        int q = s_first, pos = -1;
+        int b = s_first, pos = -1;
         const int r = r0 + tid;
-        while (q < a.batch && a.seq_start[q + 1] <= r) ++q;
-        if (tid < n && q < a.batch && r >= a.seq_start[q]) pos = r - a.seq_start[q];  // in its sequence
-        s_item[tid] = q < a.batch ? q : 0;
-        s_src[tid] = r;
+        while (b < a.batch && a.seq_start[b + 1] <= r) ++b;
+        if (tid < n && b < a.batch && r >= a.seq_start[b]) pos = r - a.seq_start[b];  // in its sequence
+        s_item[tid] = b < a.batch ? b : 0;
         s_pos[tid] = pos;
     }
     if (tid < kRows) s_bad[tid] = s_long[tid] = 0;
-    __syncthreads();
+    lds_barrier();
     // the sequences that begin or go on in these rows: 16 threads each, all at once
     // (16 short prompts one after another took 30 us), and then all threads for
     // each of the few that have many pages
@@ -249,7 +285,7 @@ __global__ __launch_bounds__(256) void append_kernel(CacheWriteArgs a, int row_b
             else if (pages_bad(a, b, first + tid % (256 / kRows), last, 256 / kRows))
                 s_bad[i] = 1;
         }
-        __syncthreads();
+        lds_barrier();
         for (int j = 0; j < n; ++j) {
             if (!s_long[j]) continue;
             const int st = check_pages(a, s_item[j], a.seq_start[s_item[j] + 1] - a.seq_start[s_item[j]]);
@@ -265,8 +301,11 @@ __global__ __launch_bounds__(256) void append_kernel(CacheWriteArgs a, int row_b
         s_place[tid] = -1;
     }
     if (tid < n) s_dst[tid] = s_place[tid] >= 0 ? cache_place(a, s_item[tid], s_place[tid]) : -1;
-    __syncthreads();
-    write_rows<TIO, LPR, E4M3, VEC>(a, n, s_src, s_dst);
+    lds_barrier();
+    for (int u0 = tid / LPR; u0 - tid / LPR < n * a.Hk * 2; u0 += kStep) {
+        if (u0 != tid / LPR) fetch<TIO, LPR, VEC>(a, n, u0, src, q);
+        flush<TIO, LPR, E4M3, VEC>(a, n, u0, s_dst, q);
+    }
 }
 
 template <typename TIO, int LPR, bool E4M3, bool VEC>
@@ -301,7 +340,12 @@ __global__ __launch_bounds__(256) void commit_kernel(CacheWriteArgs a, int chunk
         s_dst[tid] = cache_place(a, b, a.cache_len[b] + i);
     }
     __syncthreads();
-    write_rows<TIO, LPR, E4M3, VEC>(a, n, s_src, s_dst);
+    constexpr int K = 4, kStep = K * (256 / LPR);
+    Raw<TIO, VEC> q[K];
+    for (int u0 = tid / LPR; u0 - tid / LPR < n * a.Hk * 2; u0 += kStep) {
+        fetch<TIO, LPR, VEC>(a, n, u0, [&](int row) { return s_src[row]; }, q);
+        flush<TIO, LPR, E4M3, VEC>(a, n, u0, s_dst, q);
+    }
 }
 
 template <typename TIO, int LPR, bool E4M3, bool VEC>
