@@ -175,6 +175,18 @@ __device__ __forceinline__ long long cache_place(const CacheWriteArgs& a, int b,
     return (long long)pg * a.Hk * a.page_size + (pos - page * a.page_size);
 }
 
+// Largest value of each N <= 16 neighbouring lanes, in all of them
+template <int N>
+__device__ __forceinline__ uint32_t max_of(uint32_t v) {
+#define TSV_MAX_DPP(ctrl) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xf, 0xf, true))
+    if (N >= 2) TSV_MAX_DPP(0xb1);    // quad_perm [1,0,3,2]
+    if (N >= 4) TSV_MAX_DPP(0x4e);    // quad_perm [2,3,0,1]
+    if (N >= 8) TSV_MAX_DPP(0x141);   // row_half_mirror
+    if (N >= 16) TSV_MAX_DPP(0x140);  // row_mirror
+#undef TSV_MAX_DPP
+    return v;
+}
+
 // n rows, keys and values of all heads, LPR lanes a row of a head, 256 / LPR such
 // rows, heads fastest, in a step; `fetch` loads a thread's pieces of K steps from
 // u0 on (source row src(row); negative: none), `flush` writes them to s_dst (-1:
@@ -212,7 +224,8 @@ __device__ __forceinline__ void flush(const CacheWriteArgs& a, int n, int u0, co
 #pragma unroll
             for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f.v[i]) & 0x7fffffffu);
 #pragma unroll
-            for (int m = 1; m < LPR; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m, kWave));
+            for (int m = 16; m < LPR; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m, kWave));
+            top = max_of<LPR < 16 ? LPR : 16>(top);
             finite = top < 0x7f800000u;
             scale = finite ? fmaxf(__uint_as_float(top) / 448.f, 1.17549435e-38f) : __uint_as_float(0x7fc00000u);
         }
