@@ -602,7 +602,8 @@ typedef struct {
  * 64 or 128 use bf16 MFMA; the softmax weights (times the scale of an 8-bit
  * value row) enter the product with v as two bf16 parts (16 bits) where at most
  * 16 rows share a key head (T * H / Hk <= 16), and rounded once to bf16
- * otherwise. Other shapes and fp32 inputs use fp32 throughout.
+ * otherwise. fp32 inputs use fp32 throughout, with D 64 or 128 on fp32 MFMA;
+ * other shapes, and tensors that are not 16-byte aligned, use a plain fp32 kernel.
  */
 tsv_status tree_attn_verify(const tsv_attn_shape* s, const void* q, const void* k, const void* v,
                             const int32_t* parent, const void* k_cache, const void* v_cache,

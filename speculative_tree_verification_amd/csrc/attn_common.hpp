@@ -201,6 +201,10 @@ __device__ __forceinline__ Part find_part(const int32_t* __restrict__ cache_len,
 void launch_attn_mfma(const AttnArgs& a, bool e4m3, const AttnPlan& p, const AttnWorkspace& ws, int block_rows, int row_blocks,
                       hipStream_t stream);
 
+// fp32 MFMA kernel (attn_f32.hip): block_rows 16 or 64
+void launch_attn_f32(const AttnArgs& a, bool e4m3, const AttnPlan& p, const AttnWorkspace& ws, int block_rows, int row_blocks,
+                     hipStream_t stream);
+
 // Status bits of the tree, and each of `rows` rows' ancestors as bit words
 // (row i is node first + i); s_par: T ints. Acts as a barrier.
 template <int NT>

@@ -1,0 +1,69 @@
+// attn_lanes.hpp -- what the matrix kernels of the attention share: a row's
+// statistics over lanes, the scores' factor, the cache's rows.
+#pragma once
+
+#include "attn_common.hpp"
+
+namespace tsv {
+
+constexpr int kTileKeys = 64;  // keys of a tile that a work-group shares in LDS
+constexpr float kSlack = 8.f;  // a maximum moves when a weight would pass 2^kSlack
+
+// max of three, as the instruction: fmaxf first makes each product's result quiet.
+// The compiler counts the cycles that a matrix product's result needs before an
+// instruction may read it, but not for assembly: a chain of these therefore starts
+// from `settled`, which reads each accumulator through the compiler.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+// The largest of the accumulators' first elements
+template <int N, class Acc>
+__device__ __forceinline__ float settled(const Acc* s) {
+    float m = s[0][0];
+#pragma unroll
+    for (int x = 1; x < N; ++x) m = fmaxf(m, s[x][0]);
+    return N == 1 ? fmaxf(m, m) : m;
+}
+// Largest of / sum over the four lanes (16 apart) that hold a row's keys: halves
+// and rows of 16 lanes change places with a copy of themselves
+struct Two {
+    float a, b;
+};
+__device__ __forceinline__ Two swap32(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return {__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+__device__ __forceinline__ Two swap16(float v) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return {__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+template <int RW = 16>
+__device__ __forceinline__ float row_max(float v) {
+    const Two h = swap32(v);
+    if (RW == 32) return fmaxf(h.a, h.b);
+    const Two q = swap16(fmaxf(h.a, h.b));
+    return fmaxf(q.a, q.b);
+}
+template <int RW = 16>
+__device__ __forceinline__ float row_sum(float v) {
+    const Two h = swap32(v);
+    if (RW == 32) return h.a + h.b;
+    const Two q = swap16(h.a + h.b);
+    return q.a + q.b;
+}
+
+// Row index of position `pos` of an item in the cache's arrays, or -1 for a page
+// out of range. `page` is what the table holds for it.
+__device__ __forceinline__ bool page_ok(const AttnArgs& a, int page) { return (uint32_t)page < (uint32_t)a.n_pages; }
+__device__ __forceinline__ uint32_t cache_row(const AttnArgs& a, int page, int hk, int pos) {
+    const int off = pos - page_of(pos, a.div) * a.page_size;
+    return ((uint32_t)page * a.Hk + hk) * a.page_size + off;
+}
+
+// Scores stay as the product gives them, and their factor enters the exponent's
+// multiply-add: it has to be positive, so a negative one turns q's signs (exact),
+// and 0 becomes the smallest normal number (a masked score of -inf stays one).
+__device__ __forceinline__ float score_factor(const AttnArgs& a) { return fmaxf(fabsf(a.scale_log2), 1.17549435e-38f); }
+}  // namespace tsv

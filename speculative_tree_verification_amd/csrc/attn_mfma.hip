@@ -17,63 +17,17 @@
 // and the page of a key is looked up one step before its row is loaded.
 #include <cfloat>
 
-#include "attn_common.hpp"
+#include "attn_lanes.hpp"
 #include "mfma_util.hpp"
 
 namespace tsv {
 namespace {
 
 constexpr int kStepKeys = 32;  // keys of a wave's step in the row kernel
-constexpr int kTileKeys = 64;  // keys of a shared tile in the tile kernel
-
-// max of three, as the instruction: fmaxf first makes each product's result quiet
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-    return r;
-}
-// Largest of / sum over the four lanes (16 apart) that hold a row's keys: halves
-// and rows of 16 lanes change places with a copy of themselves
-struct Two {
-    float a, b;
-};
-__device__ __forceinline__ Two swap32(float v) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return {__uint_as_float(r[0]), __uint_as_float(r[1])};
-}
-__device__ __forceinline__ Two swap16(float v) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return {__uint_as_float(r[0]), __uint_as_float(r[1])};
-}
-template <int RW = 16>
-__device__ __forceinline__ float row_max(float v) {
-    const Two h = swap32(v);
-    if (RW == 32) return fmaxf(h.a, h.b);
-    const Two q = swap16(fmaxf(h.a, h.b));
-    return fmaxf(q.a, q.b);
-}
-template <int RW = 16>
-__device__ __forceinline__ float row_sum(float v) {
-    const Two h = swap32(v);
-    if (RW == 32) return h.a + h.b;
-    const Two q = swap16(h.a + h.b);
-    return q.a + q.b;
-}
-
-// Row index of position `pos` of an item in the cache's arrays, or -1 for a page
-// out of range. `page` is what the table holds for it.
-__device__ __forceinline__ bool page_ok(const AttnArgs& a, int page) { return (uint32_t)page < (uint32_t)a.n_pages; }
-__device__ __forceinline__ uint32_t cache_row(const AttnArgs& a, int page, int hk, int pos) {
-    const int off = pos - page_of(pos, a.div) * a.page_size;
-    return ((uint32_t)page * a.Hk + hk) * a.page_size + off;
-}
 
 __device__ __forceinline__ bf16x8 as_operand(uint4 u) { return __builtin_bit_cast(bf16x8, u); }
 
-// Scores stay as the product gives them, and their factor enters the exponent's
-// multiply-add: it has to be positive, so a negative one turns q's signs (exact),
-// and 0 becomes the smallest normal number (a masked score of -inf stays one).
-__device__ __forceinline__ float score_factor(const AttnArgs& a) { return fmaxf(fabsf(a.scale_log2), 1.17549435e-38f); }
+// q with the sign of the scores' factor
 __device__ __forceinline__ bf16x8 query_operand(const AttnArgs& a, uint4 u) {
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
     return as_operand(make_uint4(u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip));
@@ -161,8 +115,8 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
     // softmax and product of 32 keys: s the raw scores (masked: -inf), vs the factor
     // of each value row; V in this wave's LDS
     auto take = [&](const f32x4* s, const f32x4* vs) {
-        const float mn = max3(row_max(max3(max3(s[0][0], s[0][1], s[0][2]), max3(s[0][3], s[1][0], s[1][1]),
-                                           max3(s[1][2], s[1][3], s[1][3]))), m, m);
+        const float top = settled<2>(s);
+        const float mn = max3(row_max(max3(max3(top, s[0][1], s[0][2]), max3(top, s[0][3], s[1][1]), max3(top, s[1][2], s[1][3]))), m, m);
         const float base = mn == -INFINITY ? 0.f : mn * c;
         if (__ballot(mn > m)) {  // some row's maximum moved
             const float al = __builtin_amdgcn_exp2f(fmaf(m, c, -base));
@@ -409,8 +363,6 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
 // NW waves of RW rows. Of a product's result, 16 x 16 or 32 x 32, a lane holds one
 // column in pieces of four rows: its element e is in row e / 4 * (4 G) + 4 g + e % 4,
 // with G = 64 / RW lanes per column, this lane the g-th of them.
-constexpr float kSlack = 8.f;  // of the exponents, powers of two
-
 template <int ND, bool E4M3, int NW, int RW>
 __global__ __launch_bounds__(64 * NW, RW == 32 ? 2 : 3) void attn_tiles_kernel(AttnArgs a, AttnPlan plan, AttnWorkspace ws, int row_blocks) {
     typedef typename std::conditional<RW == 32, f32x16, f32x4>::type Acc;
@@ -500,14 +452,20 @@ __global__ __launch_bounds__(64 * NW, RW == 32 ? 2 : 3) void attn_tiles_kernel(A
 #pragma unroll
             for (int e = 0; e < RW; ++e) sc[e] = e / 4 * 4 * G + e % 4 < left ? sc[e] : -INFINITY;
         }
-        float mx = max3(sc[0], sc[1], sc[2]), my = max3(sc[3], sc[4], sc[5]);
+        float mx = sc[0];
 #pragma unroll
-        for (int e = 6; e < RW - 2; e += 4) {
-            mx = max3(mx, sc[e], sc[e + 1]);
-            my = max3(my, sc[e + 2], sc[e + 3]);
+        for (int x = 1; x < NX; ++x) mx = fmaxf(mx, sc[x * NR]);  // (`settled`, after the masks)
+        float my = mx;
+#pragma unroll
+        for (int x = 0; x < NX; ++x) {
+            mx = max3(mx, sc[x * NR + 1], sc[x * NR + 2]);
+#pragma unroll
+            for (int e = 3; e < NR; e += 4) {
+                my = max3(my, sc[x * NR + e], sc[x * NR + (e + 1 < NR ? e + 1 : e)]);
+                if (e + 2 < NR) mx = max3(mx, sc[x * NR + e + 2], sc[x * NR + (e + 3 < NR ? e + 3 : e + 2)]);
+            }
         }
-        mx = max3(mx, my, sc[RW - 2]);
-        mx = max3(mx, sc[RW - 1], mx);
+        mx = max3(mx, my, my);
         if (__ballot(fmaf(mx, c, -base) > kSlack)) {
             const float to = max3(row_max<RW>(mx) * c, base, base), al = __builtin_amdgcn_exp2f(base - to);
             l *= al;

@@ -1,7 +1,7 @@
 // attn_verify.hip -- attention of a packed tree's nodes over the paged cache:
 // the plain fp32 kernel (any head_dim up to 256, any types), the join of the
-// parts, and the choice of the kernel. The bf16 MFMA kernels are in
-// attn_mfma.hip.
+// parts, and the choice of the kernel. The kernels on matrix instructions are in
+// attn_mfma.hip (bf16) and attn_f32.hip.
 //
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(scale log2(e) q_i . k_j - m_i)
 // over the cache's positions and node i's ancestors, in one pass with a running
@@ -407,19 +407,21 @@ void launch_join(const AttnArgs& a, const AttnPlan& p, const AttnWorkspace& ws, 
         launch_join_lpr<TIO, 64>(a, p, ws, stream);
 }
 
-// Whether the bf16 kernels take the shape: 32-bit row numbers into the pool, and
+// Whether the matrix kernels take the shape: 32-bit row numbers into the pool, and
 // 16-byte rows of 64 or 128 elements (their alignment is looked at per call)
 bool matrix_shape(const tsv_attn_shape* s) {
-    return s->in_dtype == TSV_BF16 && (s->head_dim == 64 || s->head_dim == 128) && !(s->flags & TSV_FLAG_FORCE_GENERIC) &&
+    return (s->head_dim == 64 || s->head_dim == 128) && !(s->flags & TSV_FLAG_FORCE_GENERIC) &&
            (long long)s->n_pages * s->n_kv_heads * s->page_size < (1LL << 32);
 }
 
-// Rows of a work-group: 16 (attn_rows_kernel), 64 or 128 (attn_tiles_kernel, 128
-// unless that leaves a fifth more rows empty than 64 would), 8 (plain)
+// Rows of a work-group: 16 (attn_rows_kernel, attn_f32_kernel), 64 (both tile
+// kernels) or 128 (attn_tiles_kernel, unless that leaves a fifth more rows empty than
+// 64 would), 8 (plain)
 int block_rows_of(const tsv_attn_shape* s, bool matrix) {
     if (!matrix) return kRows;
     const int R = s->n_nodes * (s->n_heads / s->n_kv_heads);
     if (R <= 16) return 16;
+    if (s->in_dtype == TSV_F32) return 64;
     const int r64 = (R + 63) / 64 * 64, r128 = (R + 127) / 128 * 128;
     return r128 * 5 > r64 * 6 ? 64 : 128;
 }
@@ -483,7 +485,9 @@ hipError_t launch_attn_verify(const AttnArgs& a, const tsv_attn_shape* s, void* 
     const AttnPlan p = plan_of(s, matrix, &block_rows, &row_blocks);
     const AttnWorkspace ws = attn_workspace(workspace, p, a.T, a.H, a.D);
     const bool bf16 = s->in_dtype == TSV_BF16, e4m3 = s->cache_dtype == TSV_E4M3;
-    if (matrix)
+    if (matrix && !bf16)
+        launch_attn_f32(a, e4m3, p, ws, block_rows, row_blocks, stream);
+    else if (matrix)
         launch_attn_mfma(a, e4m3, p, ws, block_rows, row_blocks, stream);
     else if (bf16 && e4m3)
         launch_plain<uint16_t, uint8_t>(a, p, ws, row_blocks, stream);

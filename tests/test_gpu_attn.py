@@ -99,6 +99,47 @@ def test_trees(bnd, T, kind, H, Hk):
     check(bnd, *nodes(T, 2, T, H, Hk, 64, BF), U.trees(T, 2, T, kind), c, BF, f"tree {kind} T={T} H={H}/{Hk}")
 
 
+@pytest.mark.parametrize("T,kind", [(2, "chain"), (16, "star"), (17, "random"), (63, "random"), (65, "random"), (130, "chain")])
+@pytest.mark.parametrize("H,Hk,D,cdtype", [(4, 1, 64, F32), (2, 2, 64, E4), (8, 2, 128, F32), (5, 1, 128, E4)])
+def test_trees_f32(bnd, T, kind, H, Hk, D, cdtype):
+    """The fp32 kernels' trees: blocks of rows, nodes past a tile, an empty cache."""
+    c = U.cache(T, 2, [37, 0], Hk, D, 16, F32, cdtype)
+    check(bnd, *nodes(T, 2, T, H, Hk, D, F32), U.trees(T, 2, T, kind), c, F32, f"fp32 tree {kind} T={T} H={H}/{Hk} D={D} {cdtype}")
+
+
+def test_largest_tree_f32(bnd):
+    c = U.cache(4, 1, [90], 1, 64, 16, F32, F32)
+    check(bnd, *nodes(4, 1, 1024, 2, 1, 64, F32), U.trees(4, 1, 1024), c, F32, "1024 nodes, fp32")
+
+
+@pytest.mark.parametrize("cdtype", [F32, E4])
+@pytest.mark.parametrize("page", [1, 7, 24, 1000])
+@pytest.mark.parametrize("T", [1, 40])
+def test_pages_f32(bnd, cdtype, page, T):
+    c = U.cache(page, 2, [333, 64], 2, 128, page, F32, cdtype)
+    check(bnd, *nodes(page, 2, T, 4, 2, 128, F32), U.trees(T, 2, T), c, F32, f"fp32 page {page} T={T} {cdtype}")
+
+
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T", [1, 21])
+def test_plain_kernel(bnd, dtype, cdtype, D, T):
+    """The plain kernel where the matrix kernels would be taken, with a split."""
+    c = U.cache(14, 3, [2600, 0, 90], 2, D, 16, dtype, cdtype)
+    check(bnd, *nodes(14, 3, T, 6, 2, D, dtype), U.trees(14, 3, T), c, dtype, f"plain {dtype} {cdtype} D={D} T={T}",
+          force_generic=True)
+
+
+@pytest.mark.parametrize("T", [1, 21])
+def test_unaligned_f32(bnd, T):
+    """fp32 tensors that are not 16-byte aligned take the plain kernel."""
+    c = U.cache(15, 2, [150, 9], 2, 64, 16, F32, F32)
+    q, k, v = nodes(15, 2, T, 4, 2, 64, F32)
+    u = torch.empty(q.numel() + 1, device="cuda")[1:].view(q.shape).copy_(q)
+    assert u.data_ptr() % 16 != 0
+    check(bnd, u, k, v, U.trees(15, 2, T), c, F32, f"unaligned fp32 T={T}")
+
+
 def test_largest_tree(bnd):
     c = U.cache(4, 1, [90], 1, 64, 16, BF, BF)
     check(bnd, *nodes(4, 1, 1024, 2, 1, 64, BF), U.trees(4, 1, 1024), c, BF, "1024 nodes")
@@ -154,6 +195,21 @@ def test_masked_nodes_that_are_not_finite(bnd, dtype, value):
         assert torch.equal(o[0, others], clean[0, others]), name
         if name == "v" or value != value:
             assert not torch.isfinite(o[0, below].float()).any(), name
+
+
+def test_bad_pages_f32(bnd):
+    """A page out of range stops its own item only, whatever part it is in."""
+    for T in (1, 30):
+        c = U.cache(16, 3, [2000, 1500, 20], 2, 64, 16, F32, F32)
+        q, k, v = nodes(16, 3, T, 4, 2, 64, F32)
+        par = U.trees(16, 3, T).cuda()
+        args, _ = U.cache_args(c)
+        want = bnd.attn_verify(q, k, v, par, *args)
+        c["page_table"][1, 70] = c["k_cache"].shape[0]
+        o, st = torch.full_like(q, 5.0), torch.zeros(3, dtype=torch.int32, device="cuda")
+        bnd.attn_verify(q, k, v, par, *args, o=o, tree_status=st)
+        assert st.tolist() == [0, 64, 0]
+        assert (o[1] == 5.0).all() and torch.equal(o[0], want[0]) and torch.equal(o[2], want[2])
 
 
 def test_bad_items_keep_their_output(bnd):
