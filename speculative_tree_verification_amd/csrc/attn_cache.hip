@@ -11,7 +11,10 @@
 // largest value, one store of 8 bytes (e4m3) or 16. The division is a true one,
 // so that the stored byte is the nearest to row / scale. A work-group first
 // checks everything that its rows' items need (path, lengths, pages), so that
-// an item with a status bit is left whole.
+// an item with a status bit is left whole; in append the rows are on their way
+// meanwhile. 16 prompts, 16378 rows of 8 heads of 128 into e4m3 (102 MB): 30 us,
+// 3.4 TB/s, half of it the vector work (fetching after the search 31.6 us against
+// 30.0, the butterfly through LDS 30.0 against 29.0).
 #include "attn_common.hpp"
 
 namespace tsv {
@@ -83,7 +86,7 @@ __device__ __forceinline__ void store8(const CacheWriteArgs& a, bool value, size
         // v / scale to the nearest float from the nearest reciprocal: a product, its
         // exact remainder, and one correction (Markstein) give the quotient that the
         // division instruction sequence gives, in a quarter of the operations (the
-        // divisions were the bound: 44.9 us for 16378 rows of 8 heads, 33 us so).
+        // divisions were the bound: 44.9 us for 16378 rows of 8 heads, then 33 us).
         // Below 2^-100 the remainder may leave the floats' range.
         float t[8];
         if (scale >= 7.8886090522e-31f || !finite) {

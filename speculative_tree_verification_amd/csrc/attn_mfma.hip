@@ -2,17 +2,23 @@
 // instructions (head_dim 64 or 128, cache in bf16 or e4m3).
 //
 // Both kernels form the scores transposed, S^T = K Q^T (16 keys x 16 rows a
-// tile): a lane then holds the keys 4 (l / 16) + r of one row l % 16, so that the
-// softmax statistics of a row are a reduction in registers and over four lanes,
-// the factor of a rescaling is one value per lane, and two tiles of weights are
-// the operand of the next product, O^T = V^T P^T, as they are. V^T comes from LDS
-// through the transposing read, in the same order of keys.
+// tile, or 32 x 32): a lane then holds the keys 4 (l / 16) + r of one row l % 16, so
+// that the softmax statistics of a row are a reduction in registers and over four
+// lanes, the factor of a rescaling is one value per lane, and two tiles of weights
+// are the operand of the next product, O^T = V^T P^T, as they are. V^T comes from
+// LDS through the transposing read, in the same order of keys.
 //   rows   up to 16 rows (node, query head) share a key head: one new token, or a
 //          small tree. Four waves take 32 keys each in turn and meet at the end;
 //          K goes from memory into the operand registers directly. Bound by the
-//          cache's bytes.
-//   tiles  more rows: a wave has 16 rows of its own, and 64 keys at a time are
-//          shared in LDS by 4 or 8 waves. Bound by matrix and vector work.
+//          cache's bytes: 65533 positions, 8 key heads of 128, 51 us (5.2 TB/s);
+//          64 items of 17 to 8190 positions in e4m3, 111 us (5.0 TB/s).
+//   tiles  more rows: a wave has 16 or 32 rows of its own, and 64 keys at a time
+//          are shared in LDS by four waves. 32 rows halve the LDS reads of a row
+//          (and keep two waves a SIMD). Bound by matrix and vector work, which
+//          hardly overlap: 32 trees of 63 nodes over 300 to 4099 positions, 32
+//          query heads, 123 us (0.6 PFLOP/s; matrix unit busy 32% of the time, vector
+//          issue 37%). Tried and not kept there: two LDS buffers and one barrier a
+//          tile (127 to 145 us), requests while the scores' product runs (124 us).
 // In both, the loads of the next keys are under way while these are worked on,
 // and the page of a key is looked up one step before its row is loaded.
 #include <cfloat>

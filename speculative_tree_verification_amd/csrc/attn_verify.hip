@@ -11,8 +11,9 @@
 // Plain kernel: a work-group takes kRows rows (node, query head) of one key
 // head and one part; its waves take 64 keys each in turn. Scores: a lane per
 // key, the rows' q from LDS (the same for all lanes). Values: lanes over the
-// head_dim, weights from LDS. Bound by the vector ALU (4 D operations per row
-// and key, no matrix instructions).
+// head_dim, weights from LDS. Bound by the vector ALU and the LDS broadcasts (4 D
+// operations per row and key): 4 trees of 63 nodes over 2200 positions, 32 heads of
+// 128, 721 us where attn_f32.hip takes 119.
 #include "attn_common.hpp"
 
 namespace tsv {

@@ -36,7 +36,7 @@ struct SeqPlan {
 
 // Many sequences of different lengths are taken longest first, so that no long
 // one starts last: 32 prompts of 1 to 1531 tokens, 64 heads, took 237 us in
-// their own order and 177 us so. Work-groups that share B and C (the heads of
+// their own order and 179 us so. Work-groups that share B and C (the heads of
 // a slot) stay on one XCD, and slots go to the XCDs forwards and backwards in
 // turn. With few sequences there is nothing to deal, and past 256 the search
 // would cost more than it gives.
