@@ -416,15 +416,19 @@ bool matrix_shape(const tsv_attn_shape* s) {
 }
 
 // Rows of a work-group: 16 (attn_rows_kernel, attn_f32_kernel), 64 (both tile
-// kernels) or 128 (attn_tiles_kernel, unless that leaves a fifth more rows empty than
-// 64 would), 8 (plain)
+// kernels), 128 (attn_tiles_kernel) or 8 (plain). Of bf16 trees, 128 rows cost less
+// per row (caches of 2200 positions, 8 key heads: 16 items of 252 rows 68 us against
+// 83, 32 items of 92 rows 82 against 102), but not if that leaves a fifth more rows
+// empty (48 items of 180 rows 194 against 171), and not where few items have to fill
+// the GPU, whose time is latency (1 item of 252 rows 27 against 21, 4 items 38
+// against 35; 8 items 53 against 55).
 int block_rows_of(const tsv_attn_shape* s, bool matrix) {
     if (!matrix) return kRows;
     const int R = s->n_nodes * (s->n_heads / s->n_kv_heads);
     if (R <= 16) return 16;
     if (s->in_dtype == TSV_F32) return 64;
     const int r64 = (R + 63) / 64 * 64, r128 = (R + 127) / 128 * 128;
-    return r128 * 5 > r64 * 6 ? 64 : 128;
+    return r128 * 5 > r64 * 6 || (long long)s->batch * s->n_kv_heads <= 64 ? 64 : 128;
 }
 
 // Work-groups wanted, for x of them that would run without any split (an item's

@@ -140,6 +140,39 @@ def test_unaligned_f32(bnd, T):
     check(bnd, u, k, v, U.trees(15, 2, T), c, F32, f"unaligned fp32 T={T}")
 
 
+MANY = [(9, 32, 8, 31, "random"), (17, 8, 4, 63, "random"), (66, 2, 1, 255, "chain"), (33, 6, 2, 41, "star"), (10, 8, 8, 128, "random")]
+
+
+@pytest.mark.parametrize("n,H,Hk,T,kind", MANY)
+@pytest.mark.parametrize("D,cdtype", [(64, BF), (128, BF), (64, E4), (128, E4)])
+def test_trees_of_many_items(bnd, n, H, Hk, T, kind, D, cdtype):
+    """Enough items and rows for the largest blocks of rows; caches that are empty, end inside a tile, or are cut."""
+    lens = [(41 * b) % 130 for b in range(n)]
+    lens[1], lens[2], lens[3] = 2600, 64, 700
+    c = U.cache(n, n, lens, Hk, D, 16, BF, cdtype)
+    check(bnd, *nodes(n, n, T, H, Hk, D, BF), U.trees(n, n, T, kind), c, BF, f"{n} items T={T} {kind} H={H}/{Hk} D={D} {cdtype}",
+          only=[0, 1, 3, n - 1] if T < 100 else [1, n - 1])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_masked_nodes_of_many_items(bnd, value):
+    """A node's value reaches its descendants in its own item only."""
+    n, T, bad = 9, 33, 5
+    par = U.trees(18, n, T)
+    c = U.cache(18, n, [50 + b for b in range(n)], 8, 64, 16, BF, BF)
+    q, k, v = nodes(18, n, T, 32, 8, 64, BF)
+    args, _ = U.cache_args(c)
+    clean = bnd.attn_verify(q, k, v, par.cuda(), *args)
+    below = [i for i in range(T) if bad in S.root_path(par[4].numpy(), i)]
+    others = [i for i in range(T) if i not in below]
+    vv = v.clone()
+    vv[4, bad] = value
+    o = bnd.attn_verify(q, k, vv, par.cuda(), *args)
+    assert torch.equal(o[4, others], clean[4, others]) and not torch.isfinite(o[4, below].float()).any()
+    keep = [b for b in range(n) if b != 4]
+    assert torch.equal(o[keep], clean[keep])
+
+
 def test_largest_tree(bnd):
     c = U.cache(4, 1, [90], 1, 64, 16, BF, BF)
     check(bnd, *nodes(4, 1, 1024, 2, 1, 64, BF), U.trees(4, 1, 1024), c, BF, "1024 nodes")
