@@ -77,7 +77,7 @@ __device__ __forceinline__ int usable_len(int len, int room) { return len < 0 ||
 
 __device__ __forceinline__ int part_keys(const AttnPlan& plan, unsigned long long sum) {
     const unsigned long long want = (sum * plan.readers + plan.want - 1) / plan.want;
-    return max((int)min((want + 63) / 64 * 64, 0x40000000ull), plan.min_keys);
+    return max((int)min((want + 63) / 64 * 64, 0x7fffffc0ull), plan.min_keys);
 }
 
 struct Part {
@@ -115,14 +115,14 @@ __device__ __forceinline__ Part find_part(const int32_t* __restrict__ cache_len,
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     if (batch <= kWave) {  // every wave by itself: one load, no barrier
         const int raw = lane < batch ? cache_len[lane] : 0, len = usable_len(raw, room);
-        int keys = 0x40000000;
+        int keys = 0x7fffffc0;  // above any length
         if (plan.split) {
             unsigned long long sum = (unsigned)len;
 #pragma unroll
             for (int m = 1; m < kWave; m <<= 1) sum += __shfl_xor(sum, m, kWave);
             keys = part_keys(plan, sum);
         }
-        const int cnt = lane < batch ? max(1, (len + keys - 1) / keys) : 0;
+        const int cnt = lane < batch ? max(1, (int)(((uint32_t)len + keys - 1) / keys)) : 0;
         const int first = plan.sorted && lane < batch ? cnt - 1 : cnt;  // the parts in the items' order
         int upto = first;
 #pragma unroll
@@ -160,7 +160,7 @@ __device__ __forceinline__ Part find_part(const int32_t* __restrict__ cache_len,
         s_red[0] = s_red[1] = 0;
     }
     __syncthreads();
-    int keys = 0x40000000;
+    int keys = 0x7fffffc0;  // above any length
     if (plan.split) {
         unsigned long long sum = 0;
         for (int b = tid; b < batch; b += NT) sum += usable_len(cache_len[b], room);
@@ -177,7 +177,7 @@ __device__ __forceinline__ Part find_part(const int32_t* __restrict__ cache_len,
         const int b = b0 + tid;
         const int raw = b < batch ? cache_len[b] : 0;
         const int len = usable_len(raw, room);
-        const int cnt = b < batch ? max(1, (len + keys - 1) / keys) : 0;
+        const int cnt = b < batch ? max(1, (int)(((uint32_t)len + keys - 1) / keys)) : 0;
         int total;
         const int base = run + block_exclusive_scan<NT>(cnt, s_red, &total);
         if (b < batch && (by_item ? b == want : want >= base && want < base + cnt)) {
