@@ -903,25 +903,29 @@ def _raw_stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _need(t, name: str, shape, dtype, dev):
-    """_check with its common case first: these calls run once per layer and token."""
-    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or t.device != dev \
-            or not t.is_contiguous():
-        _check(t, name, shape, dtype, dev)
+def _need(t, name: str, shape, dtype, at: int):
+    """_check with its common case first, `at` the device's index (-1: no GPU):
+    these calls run once per layer and token."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == at and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _check(t, name, shape, dtype, torch.device("cuda", at) if at >= 0 else torch.device("cpu"))
 
 
-def _launch(dev, stream, body):
+def _launch(at, stream, body):
     """body(raw stream) with the tensors' device current (the library launches
     on the current device) and, for a given stream, torch's current stream
     being that one, so that the buffers that body makes belong to it."""
-    if dev.type != "cuda":
-        raise ValueError(f"tensors must be on a GPU, got {dev}")
+    if at < 0:
+        raise ValueError("tensors must be on a GPU")
     if stream is None:
-        if dev.index == _current_device():
-            return body(_raw_stream(dev.index))
-        with torch.cuda.device(dev):
-            return body(_raw_stream(dev.index))
-    with torch.cuda.device(dev), _on_stream(stream):
+        if at == _current_device():
+            return body(_raw_stream(at))
+        with torch.cuda.device(at):
+            return body(_raw_stream(at))
+    with torch.cuda.device(at), _on_stream(stream):
         return body(stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream))
 
 
@@ -947,10 +951,10 @@ def _attn_workspace(*fields) -> int:
     return need.value
 
 
-def _workspace(need: int, given, dev):
+def _workspace(need: int, given, at):
     """(tensor or None, bytes): what the caller gave, or one made here."""
     if given is not None:
-        if given.device != dev or not given.is_contiguous():
+        if given.get_device() != at or not given.is_contiguous():
             raise ValueError("workspace must be contiguous and on the tensors' device")
         size = given.numel() * given.element_size()
         if size < need:
@@ -958,7 +962,7 @@ def _workspace(need: int, given, dev):
         return given, size
     if need == 0:
         return None, 0
-    return torch.empty(need, dtype=torch.uint8, device=dev), need
+    return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", at)), need
 
 
 def prefill_workspace_bytes(n_seqs, n_tokens, n_heads, head_dim, d_state, n_groups=1, dtype=torch.bfloat16) -> int:
@@ -976,24 +980,24 @@ def prefill(x, dt, A, B, C, D, h, seq_start, y=None, seq_status=None, workspace=
     overlap need one each."""
     L, H, P = x.shape
     _, G, N = B.shape
-    n, dev, io = h.shape[0], x.device, x.dtype
-    _need(x, "x", (L, H, P), io, dev)
-    _need(dt, "dt", (L, H), io, dev)
-    _need(A, "A", (H,), torch.float32, dev)
-    _need(B, "B", (L, G, N), io, dev)
-    _need(C, "C", (L, G, N), io, dev)
-    _need(D, "D", (H,), torch.float32, dev)
-    _need(h, "h", (n, H, P, N), torch.float32, dev)
-    _need(seq_start, "seq_start", (n + 1,), torch.int32, dev)
+    n, at, io = h.shape[0], x.get_device(), x.dtype
+    _need(x, "x", (L, H, P), io, at)
+    _need(dt, "dt", (L, H), io, at)
+    _need(A, "A", (H,), torch.float32, at)
+    _need(B, "B", (L, G, N), io, at)
+    _need(C, "C", (L, G, N), io, at)
+    _need(D, "D", (H,), torch.float32, at)
+    _need(h, "h", (n, H, P, N), torch.float32, at)
+    _need(seq_start, "seq_start", (n + 1,), torch.int32, at)
     if seq_status is not None:
-        _need(seq_status, "seq_status", (n,), torch.int32, dev)
+        _need(seq_status, "seq_status", (n,), torch.int32, at)
     if y is not None:
-        _need(y, "y", (L, H, P), io, dev)
+        _need(y, "y", (L, H, P), io, at)
     fields = (n, L, H, P, N, G, _dtype_code(x), TSV_FLAG_FORCE_GENERIC if force_generic else 0)
 
     def body(s):
         out = torch.empty_like(x) if y is None else y
-        ws, size = _workspace(_seq_workspace(*fields), workspace, dev)
+        ws, size = _workspace(_seq_workspace(*fields), workspace, at)
         rc = lib.tree_ssd_prefill(SeqShape(*fields), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(),
                                   C.data_ptr(), D.data_ptr(), h.data_ptr(), seq_start.data_ptr(), out.data_ptr(),
                                   _opt(seq_status), _opt(ws), size, s)
@@ -1001,7 +1005,7 @@ def prefill(x, dt, A, B, C, D, h, seq_start, y=None, seq_status=None, workspace=
             raise TreeSSDError(rc, "tree_ssd_prefill")
         return out
 
-    return _launch(dev, stream, body)
+    return _launch(at, stream, body)
 
 
 def step(x, dt, A, B, C, D, h, y=None, stream=None):
@@ -1009,16 +1013,16 @@ def step(x, dt, A, B, C, D, h, y=None, stream=None):
     place (tree_ssd_step): x [Bt,H,P], dt [Bt,H], B, C [Bt,G,N]."""
     Bt, H, P = x.shape
     _, G, N = B.shape
-    dev, io = x.device, x.dtype
-    _need(x, "x", (Bt, H, P), io, dev)
-    _need(dt, "dt", (Bt, H), io, dev)
-    _need(A, "A", (H,), torch.float32, dev)
-    _need(B, "B", (Bt, G, N), io, dev)
-    _need(C, "C", (Bt, G, N), io, dev)
-    _need(D, "D", (H,), torch.float32, dev)
-    _need(h, "h", (Bt, H, P, N), torch.float32, dev)
+    at, io = x.get_device(), x.dtype
+    _need(x, "x", (Bt, H, P), io, at)
+    _need(dt, "dt", (Bt, H), io, at)
+    _need(A, "A", (H,), torch.float32, at)
+    _need(B, "B", (Bt, G, N), io, at)
+    _need(C, "C", (Bt, G, N), io, at)
+    _need(D, "D", (H,), torch.float32, at)
+    _need(h, "h", (Bt, H, P, N), torch.float32, at)
     if y is not None:
-        _need(y, "y", (Bt, H, P), io, dev)
+        _need(y, "y", (Bt, H, P), io, at)
     code = _dtype_code(x)
 
     def body(s):
@@ -1029,31 +1033,31 @@ def step(x, dt, A, B, C, D, h, y=None, stream=None):
             raise TreeSSDError(rc, "tree_ssd_step")
         return out
 
-    return _launch(dev, stream, body)
+    return _launch(at, stream, body)
 
 
 def _attn_fields(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, batch, rows, n_heads, scale,
                  force_generic):
     """Checks what every attention call has of the cache: the fields of tsv_attn_shape."""
-    dev, ct = k.device, k_cache.dtype
+    at, ct = k.get_device(), k_cache.dtype
     n_pages, Hk, page_size, D = k_cache.shape
     if k.shape[-2:] != (Hk, D):
         raise ValueError(f"k: heads and head_dim {tuple(k.shape[-2:])} != the cache's {(Hk, D)}")
     e4m3 = ct is torch.float8_e4m3fn
     if not e4m3 and ct is not k.dtype:
         raise TypeError(f"k_cache: dtype {ct} is neither {k.dtype} nor torch.float8_e4m3fn")
-    _need(k_cache, "k_cache", (n_pages, Hk, page_size, D), ct, dev)
-    _need(v_cache, "v_cache", (n_pages, Hk, page_size, D), ct, dev)
+    _need(k_cache, "k_cache", (n_pages, Hk, page_size, D), ct, at)
+    _need(v_cache, "v_cache", (n_pages, Hk, page_size, D), ct, at)
     for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
         if e4m3:
             if t is None:
                 raise ValueError(f"{name} is needed with an e4m3 cache")
-            _need(t, name, (n_pages, Hk, page_size), torch.float32, dev)
+            _need(t, name, (n_pages, Hk, page_size), torch.float32, at)
         elif t is not None:
             raise ValueError(f"{name} goes with an e4m3 cache only")
     most = page_table.shape[1]
-    _need(page_table, "page_table", (batch, most), torch.int32, dev)
-    _need(cache_len, "cache_len", (batch,), torch.int32, dev)
+    _need(page_table, "page_table", (batch, most), torch.int32, at)
+    _need(cache_len, "cache_len", (batch,), torch.int32, at)
     io = _dtype_code(k)
     return (batch, rows, n_heads, Hk, D, n_pages, page_size, most, io, TSV_E4M3 if e4m3 else io,
             TSV_FLAG_FORCE_GENERIC if force_generic else 0, scale)
@@ -1068,21 +1072,21 @@ def attn_verify(q, k, v, parent, k_cache, v_cache, page_table, cache_len, k_scal
     v_scale [n_pages,Hk,page_size]. ``scale`` defaults to D**-0.5. One node per
     item is plain decoding."""
     Bt, T, H, D = q.shape
-    dev, io, Hk = q.device, q.dtype, k.shape[2]
-    _need(q, "q", (Bt, T, H, D), io, dev)
-    _need(k, "k", (Bt, T, Hk, D), io, dev)
-    _need(v, "v", (Bt, T, Hk, D), io, dev)
-    _need(parent, "parent", (Bt, T), torch.int32, dev)
+    at, io, Hk = q.get_device(), q.dtype, k.shape[2]
+    _need(q, "q", (Bt, T, H, D), io, at)
+    _need(k, "k", (Bt, T, Hk, D), io, at)
+    _need(v, "v", (Bt, T, Hk, D), io, at)
+    _need(parent, "parent", (Bt, T), torch.int32, at)
     if tree_status is not None:
-        _need(tree_status, "tree_status", (Bt,), torch.int32, dev)
+        _need(tree_status, "tree_status", (Bt,), torch.int32, at)
     if o is not None:
-        _need(o, "o", (Bt, T, H, D), io, dev)
+        _need(o, "o", (Bt, T, H, D), io, at)
     fields = _attn_fields(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, T, H,
                           D ** -0.5 if scale is None else float(scale), force_generic)
 
     def body(s):
         out = torch.empty_like(q) if o is None else o
-        ws, size = _workspace(_attn_workspace(*fields), workspace, dev)
+        ws, size = _workspace(_attn_workspace(*fields), workspace, at)
         rc = lib.tree_attn_verify(AttnShape(*fields), q.data_ptr(), k.data_ptr(), v.data_ptr(), parent.data_ptr(),
                                   k_cache.data_ptr(), v_cache.data_ptr(), _opt(k_scale), _opt(v_scale),
                                   page_table.data_ptr(), cache_len.data_ptr(), out.data_ptr(), _opt(tree_status),
@@ -1091,7 +1095,7 @@ def attn_verify(q, k, v, parent, k_cache, v_cache, page_table, cache_len, k_scal
             raise TreeSSDError(rc, "tree_attn_verify")
         return out
 
-    return _launch(dev, stream, body)
+    return _launch(at, stream, body)
 
 
 def attn_verify_workspace_bytes(batch, n_nodes, n_heads, n_kv_heads, head_dim, page_size, max_pages,
@@ -1107,15 +1111,15 @@ def attn_commit(k, v, parent, accepted, accepted_len, k_cache, v_cache, page_tab
     """Write the accepted paths' rows of k, v [Bt,T,Hk,D] into the cache behind
     its cache_len positions (tree_attn_commit; cache_len is not changed)."""
     Bt, T, Hk, D = k.shape
-    dev, io = k.device, k.dtype
+    at, io = k.get_device(), k.dtype
     Lmax = accepted.shape[1]
-    _need(k, "k", (Bt, T, Hk, D), io, dev)
-    _need(v, "v", (Bt, T, Hk, D), io, dev)
-    _need(parent, "parent", (Bt, T), torch.int32, dev)
-    _need(accepted, "accepted", (Bt, Lmax), torch.int32, dev)
-    _need(accepted_len, "accepted_len", (Bt,), torch.int32, dev)
+    _need(k, "k", (Bt, T, Hk, D), io, at)
+    _need(v, "v", (Bt, T, Hk, D), io, at)
+    _need(parent, "parent", (Bt, T), torch.int32, at)
+    _need(accepted, "accepted", (Bt, Lmax), torch.int32, at)
+    _need(accepted_len, "accepted_len", (Bt,), torch.int32, at)
     if tree_status is not None:
-        _need(tree_status, "tree_status", (Bt,), torch.int32, dev)
+        _need(tree_status, "tree_status", (Bt,), torch.int32, at)
     fields = _attn_fields(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, T, Hk, 1.0, False)
 
     def body(s):
@@ -1126,7 +1130,7 @@ def attn_commit(k, v, parent, accepted, accepted_len, k_cache, v_cache, page_tab
         if rc != 0:
             raise TreeSSDError(rc, "tree_attn_commit")
 
-    _launch(dev, stream, body)
+    _launch(at, stream, body)
 
 
 def attn_append(k, v, seq_start, k_cache, v_cache, page_table, cache_len, k_scale=None, v_scale=None,
@@ -1135,13 +1139,13 @@ def attn_append(k, v, seq_start, k_cache, v_cache, page_table, cache_len, k_scal
     the cache behind its cache_len positions (tree_attn_append; cache_len is
     not changed)."""
     L, Hk, D = k.shape
-    dev, io = k.device, k.dtype
+    at, io = k.get_device(), k.dtype
     Bt = cache_len.shape[0]
-    _need(k, "k", (L, Hk, D), io, dev)
-    _need(v, "v", (L, Hk, D), io, dev)
-    _need(seq_start, "seq_start", (Bt + 1,), torch.int32, dev)
+    _need(k, "k", (L, Hk, D), io, at)
+    _need(v, "v", (L, Hk, D), io, at)
+    _need(seq_start, "seq_start", (Bt + 1,), torch.int32, at)
     if seq_status is not None:
-        _need(seq_status, "seq_status", (Bt,), torch.int32, dev)
+        _need(seq_status, "seq_status", (Bt,), torch.int32, at)
     fields = _attn_fields(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, L, Hk, 1.0, False)
 
     def body(s):
@@ -1151,4 +1155,4 @@ def attn_append(k, v, seq_start, k_cache, v_cache, page_table, cache_len, k_scal
         if rc != 0:
             raise TreeSSDError(rc, "tree_attn_append")
 
-    _launch(dev, stream, body)
+    _launch(at, stream, body)
