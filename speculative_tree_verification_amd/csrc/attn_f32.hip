@@ -105,9 +105,9 @@ __global__ __launch_bounds__(256, 2) void attn_f32_kernel(AttnArgs a, AttnPlan p
                 for (int r = 0; r < 4; ++r) s[x][r] = j + r < limit ? s[x][r] : -INFINITY;
             }
         }
-        float mx = settled<NX>(s);
+        float mx = max3(max3(s[0][0], s[0][1], s[0][2]), s[0][3], s[0][3]);
 #pragma unroll
-        for (int x = 0; x < NX; ++x) mx = max3(max3(mx, s[x][1], s[x][1]), s[x][2], s[x][3]);
+        for (int x = 1; x < NX; ++x) mx = max3(max3(mx, s[x][0], s[x][1]), s[x][2], s[x][3]);
         if (__ballot(fmaf(mx, c, -base) > kSlack)) {
             const float to = max3(row_max(mx) * c, base, base), al = __builtin_amdgcn_exp2f(base - to);
             l *= al;

@@ -9,22 +9,13 @@ namespace tsv {
 constexpr int kTileKeys = 64;  // keys of a tile that a work-group shares in LDS
 constexpr float kSlack = 8.f;  // a maximum moves when a weight would pass 2^kSlack
 
-// max of three, as the instruction: fmaxf first makes each product's result quiet.
-// The compiler counts the cycles that a matrix product's result needs before an
-// instruction may read it, but not for assembly: a chain of these therefore starts
-// from `settled`, which reads each accumulator through the compiler.
+// max of three, one instruction (v_maximum3_f32). A NaN among them stays, where
+// fmaxf would first make each product's result quiet; a row whose maximum is a NaN
+// has a key with a NaN score and is NaN whatever its maximum. An instruction of the
+// compiler's and not assembly: only for its own does it count the cycles that a
+// matrix product's result needs before it may be read.
 __device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-    return r;
-}
-// The largest of the accumulators' first elements
-template <int N, class Acc>
-__device__ __forceinline__ float settled(const Acc* s) {
-    float m = s[0][0];
-#pragma unroll
-    for (int x = 1; x < N; ++x) m = fmaxf(m, s[x][0]);
-    return N == 1 ? fmaxf(m, m) : m;
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 // Largest of / sum over the four lanes (16 apart) that hold a row's keys: halves
 // and rows of 16 lanes change places with a copy of themselves

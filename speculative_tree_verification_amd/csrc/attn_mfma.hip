@@ -121,8 +121,8 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
     // softmax and product of 32 keys: s the raw scores (masked: -inf), vs the factor
     // of each value row; V in this wave's LDS
     auto take = [&](const f32x4* s, const f32x4* vs) {
-        const float top = settled<2>(s);
-        const float mn = max3(row_max(max3(max3(top, s[0][1], s[0][2]), max3(top, s[0][3], s[1][1]), max3(top, s[1][2], s[1][3]))), m, m);
+        const float top = max3(max3(s[0][0], s[0][1], s[0][2]), max3(s[0][3], s[1][0], s[1][1]), max3(s[1][1], s[1][2], s[1][3]));
+        const float mn = max3(row_max(top), m, m);
         const float base = mn == -INFINITY ? 0.f : mn * c;
         if (__ballot(mn > m)) {  // some row's maximum moved
             const float al = __builtin_amdgcn_exp2f(fmaf(m, c, -base));
@@ -458,18 +458,11 @@ __global__ __launch_bounds__(64 * NW, RW == 32 ? 2 : 3) void attn_tiles_kernel(A
 #pragma unroll
             for (int e = 0; e < RW; ++e) sc[e] = e / 4 * 4 * G + e % 4 < left ? sc[e] : -INFINITY;
         }
-        float mx = sc[0];
+        float mx = sc[0], my = sc[1];
 #pragma unroll
-        for (int x = 1; x < NX; ++x) mx = fmaxf(mx, sc[x * NR]);  // (`settled`, after the masks)
-        float my = mx;
-#pragma unroll
-        for (int x = 0; x < NX; ++x) {
-            mx = max3(mx, sc[x * NR + 1], sc[x * NR + 2]);
-#pragma unroll
-            for (int e = 3; e < NR; e += 4) {
-                my = max3(my, sc[x * NR + e], sc[x * NR + (e + 1 < NR ? e + 1 : e)]);
-                if (e + 2 < NR) mx = max3(mx, sc[x * NR + e + 2], sc[x * NR + (e + 3 < NR ? e + 3 : e + 2)]);
-            }
+        for (int e = 2; e < RW; e += 4) {
+            mx = max3(mx, sc[e], sc[e + 1]);
+            if (e + 2 < RW) my = max3(my, sc[e + 2], sc[e + 3]);
         }
         mx = max3(mx, my, my);
         if (__ballot(fmaf(mx, c, -base) > kSlack)) {

@@ -331,6 +331,27 @@ def test_verify_on_a_side_stream_and_in_a_graph(bnd):
     c["cache_len"].copy_(old)
 
 
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T", [1, 3, 33])
+@pytest.mark.parametrize("L", [64, 128, 1000])
+def test_scores_of_few_channels(bnd, dtype, cdtype, D, T, L):
+    """Four channels alone carry scores of several hundred, of either sign: those that the fp32 products of 4
+    channels a step take in the last one. A maximum that lacks them lets the weights overflow or vanish."""
+    q, k, v = nodes(D + T, 1, T, 4, 1, D, dtype)
+    c = U.cache(L, 1, [L], 1, D, 16, dtype, F32 if cdtype == E4 else cdtype)
+    big = [D - 13, D - 9, D - 5, D - 1]
+    for t, by in ((q, 16.0), (k, 5.0), (c["k_cache"], 5.0)):
+        kept = t[..., big] * by
+        t *= 0.01
+        t[..., big] = kept
+    if cdtype == E4:
+        for m in "kv":
+            by, sc = U.quantise(torch.nan_to_num(c[m + "_cache"].cpu().float()))
+            c[m + "_cache"], c[m + "_scale"] = by.cuda(), sc.cuda()
+    check(bnd, q, k, v, U.trees(T, 1, T), c, dtype, f"few channels {dtype} {cdtype} D={D} T={T} L={L}", scale=1.0)
+
+
 # ---------------------------------------------------------------- writes
 def expect(c, rows, at, what):
     """The cache with rows ([m,Hk,D] k, v) written at (item, position)s, as header and torch's types define it."""
