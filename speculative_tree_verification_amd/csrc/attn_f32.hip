@@ -109,7 +109,8 @@ __global__ __launch_bounds__(256, 2) void attn_f32_kernel(AttnArgs a, AttnPlan p
 #pragma unroll
         for (int x = 1; x < NX; ++x) mx = max3(max3(mx, s[x][0], s[x][1]), s[x][2], s[x][3]);
         if (__ballot(fmaf(mx, c, -base) > kSlack)) {
-            const float to = max3(row_max(mx) * c, base, base), al = __builtin_amdgcn_exp2f(base - to);
+            const float top = row_max(mx);  // a row moves by its own scores alone: its bits do not follow from its neighbours'
+            const float to = fmaf(top, c, -base) > kSlack ? top * c : base, al = __builtin_amdgcn_exp2f(base - to);
             l *= al;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) o[i] *= al;

@@ -466,7 +466,8 @@ __global__ __launch_bounds__(64 * NW, RW == 32 ? 2 : 3) void attn_tiles_kernel(A
         }
         mx = max3(mx, my, my);
         if (__ballot(fmaf(mx, c, -base) > kSlack)) {
-            const float to = max3(row_max<RW>(mx) * c, base, base), al = __builtin_amdgcn_exp2f(base - to);
+            const float top = row_max<RW>(mx);  // a row moves by its own scores alone: its bits do not follow from its neighbours'
+            const float to = fmaf(top, c, -base) > kSlack ? top * c : base, al = __builtin_amdgcn_exp2f(base - to);
             l *= al;
 #pragma unroll
             for (int i = 0; i < D / RW; ++i) o[i] *= al;

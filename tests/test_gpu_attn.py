@@ -352,6 +352,27 @@ def test_scores_of_few_channels(bnd, dtype, cdtype, D, T, L):
     check(bnd, q, k, v, U.trees(T, 1, T), c, dtype, f"few channels {dtype} {cdtype} D={D} T={T} L={L}", scale=1.0)
 
 
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_masked_nodes_of_few_rows(bnd, dtype, cdtype, D, value):
+    """A node that is not finite reaches its descendants only, 16 rows a key head."""
+    par = torch.tensor([[-1, 0, 1, 0]], dtype=torch.int32)
+    c = U.cache(43, 1, [130], 2, D, 16, dtype, cdtype)
+    q, k, v = nodes(44, 1, 4, 8, 2, D, dtype)
+    args, scales = U.cache_args(c)
+    clean = bnd.attn_verify(q, k, v, par.cuda(), *args, **scales)
+    for name in "kv":
+        kk, vv = k.clone(), v.clone()
+        (kk if name == "k" else vv)[0, 1] = value
+        o = bnd.attn_verify(q, kk, vv, par.cuda(), *args, **scales)
+        assert torch.equal(o[0, [0, 3]], clean[0, [0, 3]]), name
+        if name == "v":
+            assert ((o[0, [1, 2]] == value) | (torch.isnan(o[0, [1, 2]]) & (value != value))).all()
+        elif value != value:
+            assert torch.isnan(o[0, [1, 2]]).all()
+
+
 # ---------------------------------------------------------------- writes
 def expect(c, rows, at, what):
     """The cache with rows ([m,Hk,D] k, v) written at (item, position)s, as header and torch's types define it."""
