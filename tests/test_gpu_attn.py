@@ -354,6 +354,20 @@ def test_scores_of_few_channels(bnd, dtype, cdtype, D, T, L):
 
 @pytest.mark.parametrize("dtype,cdtype", TYPES)
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T", [1, 3])
+def test_large_scores_of_few_rows(bnd, dtype, cdtype, D, T):
+    """At most 16 rows a key head: their own kernels' maxima, factors and join of the waves."""
+    c = U.cache(40 + D, 3, [700, 90, 3000], 1, D, 16, dtype, cdtype)
+    q, k, v = nodes(41 + T, 3, T, 4, 1, D, dtype)
+    par = U.trees(42, 3, T, "chain")
+    what = f"few rows {dtype} {cdtype} D={D} T={T}"
+    check(bnd, q * 64, k, v, par, c, dtype, f"{what} large")
+    check(bnd, q * 8, k, v, par, c, dtype, f"{what} negative", scale=-0.3)
+    check(bnd, q, k, v, par, c, dtype, f"{what} 0", scale=0.0)
+
+
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
 def test_masked_nodes_of_few_rows(bnd, dtype, cdtype, D, value):
     """A node that is not finite reaches its descendants only, 16 rows a key head."""
