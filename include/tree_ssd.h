@@ -604,6 +604,9 @@ typedef struct {
  * 16 rows share a key head (T * H / Hk <= 16), and rounded once to bf16
  * otherwise. fp32 inputs use fp32 throughout, with D 64 or 128 on fp32 MFMA;
  * other shapes, and tensors that are not 16-byte aligned, use a plain fp32 kernel.
+ * A key or a value that is not finite reaches the nodes that see it and no
+ * others. An infinite value gives an infinity there, unless its weight is 0 in
+ * fp32 (then the element may be finite, infinite or NaN).
  */
 tsv_status tree_attn_verify(const tsv_attn_shape* s, const void* q, const void* k, const void* v,
                             const int32_t* parent, const void* k_cache, const void* v_cache,

@@ -236,6 +236,11 @@ __global__ __launch_bounds__(256, 2) void attn_f32_kernel(AttnArgs a, AttnPlan p
         int set = 0;
         for (int t = k0; t < k1; t += kTileKeys, set ^= 1) {
             lds_barrier();  // the last tile's reads are done
+            if (t + kTileKeys > k1) {  // past the last key its row was read again: 0, for a value that is not finite
+#pragma unroll
+                for (int i = 0; i < L; ++i)
+                    if (prow + i * RR >= k1 - t) rv[i] = make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 put(&s_K[(prow + i * RR) * kS + pcol / EB], rk[i]);
@@ -243,7 +248,7 @@ __global__ __launch_bounds__(256, 2) void attn_f32_kernel(AttnArgs a, AttnPlan p
             }
             if (E4M3 && w == 0) {
                 s_ks[lane] = rks;
-                s_vs[lane] = rvs;
+                s_vs[lane] = t + lane < k1 ? rvs : 0.f;
             }
             find_rows(t + kTileKeys, set ^ 1);
             lds_barrier();

@@ -140,15 +140,19 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
         l += sum;  // of this lane's keys; the four lanes of a row meet at the end
         if (E4M3 && vs) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] *= vs[e / 4][e % 4];  // a key past the last one has the last one's
+            for (int e = 0; e < 8; ++e) p[e] *= vs[e / 4][e % 4];  // (0 of a key past the last one)
         }
         // weights as two bf16 parts: with the cache's bytes the bound, their rounding
-        // need not be a part of the result's error
+        // need not be a part of the result's error. The upper 16 bits, and what is left
+        // with 2^-23 of the weight: both parts are positive, so that an infinite value
+        // times them is one infinity (0 times it, or a part of the other sign, makes a NaN)
         uint32_t hi[4], lo[4];
+        constexpr float kUp = 1.f + 0x1p-23f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            hi[e] = pack_bf16x2(p[2 * e], p[2 * e + 1]);
-            lo[e] = pack_bf16x2(p[2 * e] - __uint_as_float(hi[e] << 16), p[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+            hi[e] = __builtin_amdgcn_perm(__float_as_uint(p[2 * e + 1]), __float_as_uint(p[2 * e]), 0x07060302u);
+            lo[e] = pack_bf16x2(fmaf(p[2 * e], kUp, -__uint_as_float(hi[e] << 16)),
+                                fmaf(p[2 * e + 1], kUp, -__uint_as_float(hi[e] & 0xffff0000u)));
         }
         const bf16x8 pf = as_operand(make_uint4(hi[0], hi[1], hi[2], hi[3])), pl = as_operand(make_uint4(lo[0], lo[1], lo[2], lo[3]));
 #pragma unroll
@@ -257,7 +261,7 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
             if (E4M3) {
                 if (lane < kStepKeys) {
                     s_ks[w][lane] = rks;
-                    s_vs[w][lane] = rvs;
+                    s_vs[w][lane] = t + lane < k1 ? rvs : 0.f;
                 }
                 wave_sync();
             }
@@ -301,6 +305,10 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (t + 16 * (e / 4) + 4 * lg + e % 4 >= k1) s[e / 4][e % 4] = -INFINITY;
+                // past the last key its row was read again: 0 in its place, since the weight 0
+                // would make a NaN of a value that is not finite
+                for (int i = (k1 - t) * (D / 8) + lane; i < kStepKeys * (D / 8); i += kWave)
+                    *(uint4*)&s_V[w][i / (D / 8) * kVs + i % (D / 8) * 8] = make_uint4(0, 0, 0, 0);
             }
             wave_sync();
             take(s, vs);
@@ -485,7 +493,7 @@ __global__ __launch_bounds__(64 * NW, RW == 32 ? 2 : 3) void attn_tiles_kernel(A
             if (SCALED) {
                 const f32x4 vs = *(const f32x4*)&s_vs[e * G + 4 * lg];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) p[r] *= vs[r];  // a key past the last one has the last one's
+                for (int r = 0; r < 4; ++r) p[r] *= vs[r];  // (0 of a key past the last one)
             }
             u[e / 2] = pack_bf16x2(p[0], p[1]);
             u[e / 2 + 1] = pack_bf16x2(p[2], p[3]);
@@ -579,6 +587,11 @@ __global__ __launch_bounds__(64 * NW, RW == 32 ? 2 : 3) void attn_tiles_kernel(A
         int set = 0;
         for (int t = k0; t < k1; t += kTileKeys, set ^= 1) {
             lds_barrier();  // the last tile's reads are done
+            if (t + kTileKeys > k1) {  // past the last key: as in the row kernel
+#pragma unroll
+                for (int i = 0; i < L; ++i)
+                    if (prow + i * RR >= k1 - t) rv[i] = make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 if (!loads) break;
@@ -595,7 +608,7 @@ __global__ __launch_bounds__(64 * NW, RW == 32 ? 2 : 3) void attn_tiles_kernel(A
             }
             if (E4M3 && w == 0) {
                 s_ks[lane] = rks;
-                s_vs[lane] = rvs;
+                s_vs[lane] = t + lane < k1 ? rvs : 0.f;
             }
             find_rows(t + kTileKeys, set ^ 1);
             lds_barrier();

@@ -387,6 +387,30 @@ def test_masked_nodes_of_few_rows(bnd, dtype, cdtype, D, value):
             assert torch.isnan(o[0, [1, 2]]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T", [1, 3, 33])
+@pytest.mark.parametrize("L", [1, 63, 64, 130, 1000])
+@pytest.mark.parametrize("generic", [False, True])
+def test_infinite_values_of_the_cache(bnd, dtype, D, T, L, generic):
+    """One infinite element of the last position, or of the first: that element of every output is the infinity, in
+    every kernel and at every length; the others do not change."""
+    c = U.cache(45, 1, [L], 1, D, 16, dtype, dtype)
+    q, k, v = nodes(46, 1, T, 4, 1, D, dtype)
+    par = U.trees(47, 1, T).cuda()
+    args, _ = U.cache_args(c)
+    clean = bnd.attn_verify(q, k, v, par, *args, force_generic=generic)
+    for pos, d, value in ((L - 1, 5, float("inf")), (0, D - 1, -float("inf"))):
+        at = int(c["page_table"][0, pos // 16]), 0, pos % 16, d
+        kept = float(c["v_cache"][at])
+        c["v_cache"][at] = value
+        o = bnd.attn_verify(q, k, v, par, *args, force_generic=generic)
+        c["v_cache"][at] = kept
+        assert (o[..., d] == value).all(), (pos, o[..., d])
+        rest = [x for x in range(D) if x != d]
+        assert torch.equal(o[..., rest], clean[..., rest])
+
+
 # ---------------------------------------------------------------- writes
 def expect(c, rows, at, what):
     """The cache with rows ([m,Hk,D] k, v) written at (item, position)s, as header and torch's types define it."""
