@@ -87,14 +87,15 @@ __device__ __forceinline__ void store8(const CacheWriteArgs& a, bool value, size
         // exact remainder, and one correction (Markstein) give the quotient that the
         // division instruction sequence gives, in a quarter of the operations (the
         // divisions were the bound: 44.9 us for 16378 rows of 8 heads, then 33 us).
-        // Below 2^-100 the remainder may leave the floats' range.
+        // The remainder is formed negated, so that an exact 0 in the correction has
+        // the quotient's sign: -0 stays -0. Below 2^-100 it may leave the floats' range.
         float t[8];
         if (scale >= 7.8886090522e-31f || !finite) {
             const float r = 1.f / scale;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float q0 = q.v[i] * r;
-                t[i] = fmaf(fmaf(-q0, scale, q.v[i]), r, q0);
+                t[i] = fmaf(-fmaf(q0, scale, -q.v[i]), r, q0);
             }
         } else {
 #pragma unroll

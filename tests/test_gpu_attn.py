@@ -569,6 +569,25 @@ def test_rows_that_are_not_finite_read_back_as_nan(bnd):
     assert torch.isnan(back[1:3]).all() and ((back[[0, 3]] - 1).abs() <= 2.0 ** -23).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_bytes_of_zeros_and_small_values(bnd, dtype):
+    """Zeros of either sign, values far below the row's largest, and rows near the ends of the types' range: the
+    bytes of the rounded quotients."""
+    c = U.cache(25, 1, [0], 1, 64, 16, dtype, E4, room=12)
+    g = torch.Generator().manual_seed(27)
+    k = torch.randn(12, 1, 64, generator=g)
+    k[0, 0, ::2] = -0.0
+    k[1], k[2, 0, 1:] = -0.0, -0.0
+    k[3] *= torch.logspace(-38, 0, 64)
+    k[4:] *= torch.logspace(-40, 37, 8)[:, None, None]
+    k = k.to(dtype).cuda()
+    want = expect(c, [k, -k], [(0, i) for i in range(12)], "append")
+    args, scales = U.cache_args(c)
+    bnd.attn_append(k, -k, torch.tensor([0, 12], dtype=torch.int32, device="cuda"), *args, **scales)
+    torch.cuda.synchronize()
+    same(c, want)
+
+
 def test_prompt_trees_and_tokens_together(bnd):
     """A layer's life: prompts enter the cache, trees are verified over it and their accepted paths committed,
     then single tokens follow; every output is that of the tokens' own sequence."""
