@@ -471,7 +471,9 @@ tsv_status tree_ssd_snapshot_commit(const tsv_shape* s, const float* states, flo
  * Sequences around the tree: the prompt scan and the single-token step, which
  * make and advance the state h0 that a tree is verified from. The recurrence
  * is that of tree_ssd_verify; along a sequence every token has the one before
- * it as its parent.
+ * it as its parent. These calls and those of the paged cache below return
+ * TSV_E_UNSUPPORTED where a launch would have 2^32 threads or more (2^24
+ * work-groups: about one for each item or 16 rows, and head).
  * ------------------------------------------------------------------------ */
 
 /* Per-item status bit: seq_start is not 0 <= seq_start[0] <= seq_start[1] <=

@@ -11,7 +11,9 @@ namespace {
 
 constexpr int kMaxTree = 1024;
 constexpr int kMaxDim = 256;
-constexpr long long kMaxBlocks = 0x7fffffffLL;
+// A launch counts its threads in 32 bits, and all of these have work-groups of
+// 256: one more work-group than this would run as a grid of what is left over
+constexpr long long kMaxBlocks = 0xffffffffLL / 256;
 
 bool dtype_ok(int d) { return d == TSV_F32 || d == TSV_BF16; }
 
@@ -22,9 +24,7 @@ tsv_status check_seq(const tsv_seq_shape* s) {
     if (s->n_heads < 1 || s->head_dim < 1 || s->d_state < 1 || s->n_groups < 1) return TSV_E_SHAPE;
     if (s->n_heads % s->n_groups != 0) return TSV_E_SHAPE;
     if (s->head_dim > kMaxDim || s->d_state > kMaxDim || s->n_heads > 0xffff) return TSV_E_UNSUPPORTED;
-    // every launch's grid stays inside 2^31 work-groups
-    if (tsv::prefill_blocks(s) > kMaxBlocks)
-        return TSV_E_UNSUPPORTED;
+    if (tsv::prefill_blocks(s, s->head_dim * s->d_state % 4 == 0) > kMaxBlocks) return TSV_E_UNSUPPORTED;
     return TSV_OK;
 }
 
@@ -87,6 +87,7 @@ tsv_status tree_ssd_prefill(const tsv_seq_shape* s, const void* x, const void* d
     if (need > 0 && (uintptr_t)workspace % 16 != 0) return TSV_E_SHAPE;
     tsv::PrefillArgs a{x, dt, A, B, C, D, h_inout, seq_start, y, s->n_seqs, s->n_tokens, s->n_heads, s->head_dim,
                        s->d_state, s->n_groups};
+    if (tsv::prefill_blocks(s, tsv::prefill_states_vec(a, workspace)) > kMaxBlocks) return TSV_E_UNSUPPORTED;
     return result(tsv::launch_prefill(a, s, seq_status, need > 0 ? workspace : nullptr, (hipStream_t)stream));
 }
 
@@ -98,7 +99,7 @@ tsv_status tree_ssd_step(const tsv_shape* s, const void* x, const void* dt, cons
     if (s->n_heads < 1 || s->head_dim < 1 || s->d_state < 1 || s->n_groups < 1) return TSV_E_SHAPE;
     if (s->n_heads % s->n_groups != 0) return TSV_E_SHAPE;
     if (s->head_dim > kMaxDim || s->d_state > kMaxDim || s->n_heads > 0xffff) return TSV_E_UNSUPPORTED;
-    if ((long long)s->batch * s->n_heads * 64 > kMaxBlocks) return TSV_E_UNSUPPORTED;
+    if (tsv::step_blocks(s) > kMaxBlocks) return TSV_E_UNSUPPORTED;
     if (s->batch == 0 || s->n_nodes == 0) return TSV_OK;
     if (!x || !dt || !A || !B || !C || !D || !h_inout || !y) return TSV_E_NULL;
     tsv::StepArgs a{x, dt, A, B, C, D, h_inout, y, s->batch, s->n_heads, s->head_dim, s->d_state, s->n_groups};
@@ -142,7 +143,7 @@ tsv_status tree_attn_commit(const tsv_attn_shape* s, const void* k, const void* 
     tsv_status st = check_attn(s, true);
     if (st != TSV_OK) return st;
     if (max_path_len < 0 || max_path_len > kMaxTree) return TSV_E_SHAPE;
-    if ((long long)s->batch * (kMaxTree / 2) > kMaxBlocks) return TSV_E_UNSUPPORTED;
+    if (tsv::commit_blocks(s->batch, s->n_nodes, max_path_len) > kMaxBlocks) return TSV_E_UNSUPPORTED;
     if (s->batch == 0 || s->n_nodes == 0) return TSV_OK;
     if (!k || !v || !parent || !accepted_len || !cache_len) return TSV_E_NULL;
     if (max_path_len > 0 && !accepted) return TSV_E_NULL;
@@ -161,7 +162,7 @@ tsv_status tree_attn_append(const tsv_attn_shape* s, const void* k, const void* 
                             float* k_scale, float* v_scale, int32_t* seq_status, void* stream) {
     tsv_status st = check_attn(s, false);
     if (st != TSV_OK) return st;
-    if ((long long)s->batch + s->n_nodes > kMaxBlocks) return TSV_E_UNSUPPORTED;
+    if (tsv::append_blocks(s->n_nodes, s->batch) > kMaxBlocks) return TSV_E_UNSUPPORTED;
     if (s->batch == 0) return TSV_OK;
     if (!seq_start || !cache_len) return TSV_E_NULL;
     if (s->n_nodes > 0 && (!k || !v)) return TSV_E_NULL;

@@ -368,12 +368,12 @@ __global__ __launch_bounds__(256) void commit_kernel(CacheWriteArgs a, int chunk
 template <typename TIO, int LPR, bool E4M3, bool VEC>
 hipError_t launch_one(const CacheWriteArgs& a, hipStream_t stream) {
     if (a.seq_start) {
-        const int blocks = (a.T + kRows - 1) / kRows;
-        const int all = blocks + (a.status ? a.batch : 0);
+        const int blocks = (int)append_blocks(a.T, 0);
+        const int all = (int)append_blocks(a.T, a.status ? a.batch : 0);
         if (all > 0)
             hipLaunchKernelGGL((append_kernel<TIO, LPR, E4M3, VEC>), dim3(all), dim3(256), 0, stream, a, blocks);
     } else {
-        const int chunks = max(1, (min(a.Lmax, a.T) + kPathRows - 1) / kPathRows);
+        const int chunks = (int)commit_blocks(1, a.T, a.Lmax);
         hipLaunchKernelGGL((commit_kernel<TIO, LPR, E4M3, VEC>), dim3((unsigned)((long long)a.batch * chunks)), dim3(256), 0,
                            stream, a, chunks);
     }
@@ -391,6 +391,11 @@ hipError_t launch_type(const CacheWriteArgs& a, hipStream_t stream) {
 }
 
 }  // namespace
+
+long long commit_blocks(int batch, int T, int max_path_len) {
+    return (long long)batch * max(1, (min(max_path_len, T) + kPathRows - 1) / kPathRows);
+}
+long long append_blocks(int n_rows, int items) { return ((long long)n_rows + kRows - 1) / kRows + items; }
 
 hipError_t launch_cache_write(const CacheWriteArgs& a, bool bf16, bool e4m3, hipStream_t stream) {
     if (bf16) return e4m3 ? launch_type<uint16_t, true>(a, stream) : launch_type<uint16_t, false>(a, stream);

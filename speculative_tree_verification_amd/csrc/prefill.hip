@@ -214,9 +214,12 @@ void launch_plain(const PrefillArgs& a, const SeqPlan& p, const SeqWorkspace& ws
         launch_plain_pass<TIO, 64, LOCAL>(a, p, ws, stream);
 }
 
+// Work-groups of the combining pass for a sequence's head
+int combine_chunks(int P, int N, bool vec) { return (P * N + 256 * (vec ? 4 : 1) - 1) / (256 * (vec ? 4 : 1)); }
+
 void launch_combine(const PrefillArgs& a, const SeqPlan& p, const SeqWorkspace& ws, hipStream_t stream) {
-    const bool vec = a.P * a.N % 4 == 0 && (uintptr_t)a.h % 16 == 0 && (uintptr_t)ws.state % 16 == 0;
-    const int chunks = (a.P * a.N + 256 * (vec ? 4 : 1) - 1) / (256 * (vec ? 4 : 1));
+    const bool vec = prefill_states_vec(a, ws.state);
+    const int chunks = combine_chunks(a.P, a.N, vec);
     const dim3 grid((unsigned)((long long)a.n_seqs * a.H * chunks));
     if (vec)
         hipLaunchKernelGGL((prefill_combine_kernel<4>), grid, dim3(256), 0, stream, a, p, ws, chunks);
@@ -237,10 +240,14 @@ uint64_t prefill_workspace_bytes(const tsv_seq_shape* s) {
     return seq_workspace_bytes(seq_plan(s->n_seqs, s->n_tokens, s->n_heads, matrix_shape(s)), s->n_heads, s->head_dim, s->d_state);
 }
 
-long long prefill_blocks(const tsv_seq_shape* s) {
+bool prefill_states_vec(const PrefillArgs& a, const void* workspace) {
+    return a.P * a.N % 4 == 0 && (uintptr_t)a.h % 16 == 0 && (uintptr_t)workspace % 16 == 0;
+}
+
+long long prefill_blocks(const tsv_seq_shape* s, bool states_vec) {
     const SeqPlan p = seq_plan(s->n_seqs, s->n_tokens, s->n_heads, matrix_shape(s));
     const long long scan = (long long)p.slots * s->n_heads * ((s->head_dim + kWave - 1) / kWave);
-    const long long combine = (long long)s->n_seqs * s->n_heads * (((long long)s->head_dim * s->d_state + 255) / 256);
+    const long long combine = p.split ? (long long)s->n_seqs * s->n_heads * combine_chunks(s->head_dim, s->d_state, states_vec) : 0;
     return scan > combine ? scan : combine;
 }
 

@@ -18,6 +18,7 @@ struct StepArgs {
     void* y;
     int batch, H, P, N, G;
 };
+long long step_blocks(const tsv_shape* s);  // work-groups
 hipError_t launch_step(const StepArgs& a, bool bf16, hipStream_t stream);
 
 struct PrefillArgs {
@@ -33,8 +34,10 @@ struct PrefillArgs {
     int n_seqs, n_tokens, H, P, N, G;
 };
 uint64_t prefill_workspace_bytes(const tsv_seq_shape* s);
+// whether the states are taken 4 elements at a time by the combining pass
+bool prefill_states_vec(const PrefillArgs& a, const void* workspace);
 // most work-groups of any launch of the prompt scan
-long long prefill_blocks(const tsv_seq_shape* s);
+long long prefill_blocks(const tsv_seq_shape* s, bool states_vec);
 hipError_t launch_prefill(const PrefillArgs& a, const tsv_seq_shape* s, int32_t* status, void* workspace, hipStream_t stream);
 
 // ---- the paged cache of attention layers
@@ -59,6 +62,9 @@ struct CacheWriteArgs {
     int batch, T, Lmax, Hk, D, n_pages, page_size, max_pages;
     PageDiv div, heads;  // by page_size; by 2 Hk
 };
+// work-groups: of accepted paths; of n_rows rows and, with a status, its items
+long long commit_blocks(int batch, int T, int max_path_len);
+long long append_blocks(int n_rows, int items);
 hipError_t launch_cache_write(const CacheWriteArgs& a, bool bf16, bool e4m3, hipStream_t stream);
 
 struct AttnArgs {

@@ -85,10 +85,13 @@ __global__ __launch_bounds__(256) void step_kernel(StepArgs a, int slices) {
     }
 }
 
+// lanes of a state row of N elements; work-groups of a state of P rows
+constexpr int row_lanes(int N) { return N <= 64 ? 16 : N <= 128 ? 32 : 64; }
+constexpr int row_slices(int P, int lanes) { return (P + kWave / lanes * kStepRows * 4 - 1) / (kWave / lanes * kStepRows * 4); }
+
 template <typename TIO, int LPR>
 hipError_t launch_lpr(const StepArgs& a, bool vec, hipStream_t stream) {
-    constexpr int RPB = kWave / LPR * kStepRows * 4;
-    const int slices = (a.P + RPB - 1) / RPB;
+    const int slices = row_slices(a.P, LPR);
     const dim3 grid((unsigned)((long long)a.batch * a.H * slices));
     if (vec)
         hipLaunchKernelGGL((step_kernel<TIO, LPR, true>), grid, dim3(256), 0, stream, a, slices);
@@ -101,12 +104,16 @@ template <typename TIO>
 hipError_t launch_io(const StepArgs& a, hipStream_t stream) {
     const bool vec = a.N % 4 == 0 && (uintptr_t)a.h % 16 == 0 && (uintptr_t)a.B % (4 * sizeof(TIO)) == 0 &&
                      (uintptr_t)a.C % (4 * sizeof(TIO)) == 0;
-    if (a.N <= 64) return launch_lpr<TIO, 16>(a, vec, stream);
-    if (a.N <= 128) return launch_lpr<TIO, 32>(a, vec, stream);
+    if (row_lanes(a.N) == 16) return launch_lpr<TIO, 16>(a, vec, stream);
+    if (row_lanes(a.N) == 32) return launch_lpr<TIO, 32>(a, vec, stream);
     return launch_lpr<TIO, 64>(a, vec, stream);
 }
 
 }  // namespace
+
+long long step_blocks(const tsv_shape* s) {
+    return (long long)s->batch * s->n_heads * row_slices(s->head_dim, row_lanes(s->d_state));
+}
 
 hipError_t launch_step(const StepArgs& a, bool bf16, hipStream_t stream) {
     return bf16 ? launch_io<uint16_t>(a, stream) : launch_io<float>(a, stream);

@@ -186,3 +186,30 @@ def test_binding_refuses_before_the_library():
         B.attn_append(k, k, start, c.transpose(0, 1), c, table, n)
     with pytest.raises(ValueError, match="e4m3"):
         B.attn_append(k, k, start, c, c, table, n, k_scale=torch.zeros(2, 2, 16))
+
+
+MOST = (2 ** 32 - 1) // 256  # work-groups of 256 threads whose threads are counted in 32 bits
+
+
+@pytest.mark.parametrize("name,call", [
+    ("step", lambda n: L.tree_ssd_step(ctypes.byref(B.Shape(n, 1, 1, 1, 1, 1, 1, 0, 0)), *[FAKE] * 8, None)),
+    ("step, two work-groups a state", lambda n: L.tree_ssd_step(ctypes.byref(B.Shape(n // 2 + 1, 1, 1, 64, 128, 1, 1, 0, 0)), *[FAKE] * 8, None)),
+    ("prefill", lambda n: prefill(seq(n_seqs=n, n_tokens=n, n_heads=1, head_dim=1, d_state=1))),
+    ("prefill, states of 8 work-groups", lambda n: prefill(seq(n_seqs=n // 8 + 1, n_tokens=2000, n_heads=1))),
+    ("prefill, states that are not aligned", lambda n: prefill(seq(n_seqs=n // 32 + 1, n_tokens=2000, n_heads=1), [FAKE] * 6 + [ctypes.c_void_p(0x1004)] + [FAKE] * 2)),
+    ("verify", lambda n: verify(attn(batch=n, n_nodes=1, n_heads=1, n_kv_heads=1))),
+    ("verify, join", lambda n: verify(attn(batch=n // 8 + 1, n_nodes=128, n_heads=1, n_kv_heads=1, max_pages=100))),
+    ("commit", lambda n: commit(attn(batch=n), lmax=2)),
+    ("commit, long paths", lambda n: commit(attn(batch=n // 4 + 1), lmax=8)),
+    ("append", lambda n: append(attn(batch=2, n_nodes=16 * n)))])
+def test_grids_past_32_bits_of_threads_are_refused(name, call):
+    assert call(MOST + 1) == UNSUPPORTED, name
+
+
+def test_sizes_below_the_largest_grid_are_not_refused():
+    n = ctypes.c_uint64()
+    # 100,000 prompts of 80 heads without a cut; 20,000 with one
+    for s in (seq(n_seqs=100000, n_tokens=200, n_heads=80), seq(n_seqs=20000, n_tokens=100000, n_heads=80)):
+        assert L.tree_ssd_prefill_workspace(ctypes.byref(s), ctypes.byref(n)) == OK
+    assert commit(attn(batch=MOST // 4), lmax=8, ptrs=[None] * 11) == NULL  # past the size checks
+    assert append(attn(batch=2, n_nodes=16 * (MOST - 2)), ptrs=[None] * 9) == NULL
