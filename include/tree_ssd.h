@@ -483,7 +483,7 @@ tsv_status tree_ssd_snapshot_commit(const tsv_shape* s, const float* states, flo
 
 typedef struct {
     int32_t n_seqs;   /* sequences >= 0 (0: nothing to do) */
-    int32_t n_tokens; /* rows of the packed arrays >= 0 */
+    int32_t n_tokens; /* rows of the packed arrays >= 0, at most 2^31 - 2^16 (TSV_E_UNSUPPORTED past it) */
     int32_t n_heads;  /* H in [1, 65535] */
     int32_t head_dim; /* P in [1, 256] */
     int32_t d_state;  /* N in [1, 256] */

@@ -17,6 +17,10 @@ constexpr long long kMaxBlocks = 0xffffffffLL / 256;
 
 bool dtype_ok(int d) { return d == TSV_F32 || d == TSV_BF16; }
 
+// Rows, sequences and positions end 2^16 below the largest int, so that the kernels'
+// sums of one of them and a tile or a step do not pass it
+constexpr int kMaxRows = 0x7fff0000;
+
 tsv_status check_seq(const tsv_seq_shape* s) {
     if (!s) return TSV_E_NULL;
     if (!dtype_ok(s->in_dtype)) return TSV_E_DTYPE;
@@ -24,6 +28,7 @@ tsv_status check_seq(const tsv_seq_shape* s) {
     if (s->n_heads < 1 || s->head_dim < 1 || s->d_state < 1 || s->n_groups < 1) return TSV_E_SHAPE;
     if (s->n_heads % s->n_groups != 0) return TSV_E_SHAPE;
     if (s->head_dim > kMaxDim || s->d_state > kMaxDim || s->n_heads > 0xffff) return TSV_E_UNSUPPORTED;
+    if (s->n_seqs > kMaxRows || s->n_tokens > kMaxRows) return TSV_E_UNSUPPORTED;
     if (tsv::prefill_blocks(s, s->head_dim * s->d_state % 4 == 0) > kMaxBlocks) return TSV_E_UNSUPPORTED;
     return TSV_OK;
 }
@@ -36,7 +41,7 @@ tsv_status check_attn(const tsv_attn_shape* s, bool tree) {
     if (s->n_heads < 1 || s->n_kv_heads < 1 || s->n_heads % s->n_kv_heads != 0) return TSV_E_SHAPE;
     if (s->head_dim < 1 || s->n_pages < 0 || s->max_pages < 0) return TSV_E_SHAPE;
     if (s->page_size < 1 || s->page_size > 65536) return TSV_E_SHAPE;
-    if ((long long)s->max_pages * s->page_size > 0x7fff0000LL) return TSV_E_SHAPE;
+    if ((long long)s->max_pages * s->page_size > kMaxRows) return TSV_E_SHAPE;
     if (!isfinite(s->scale)) return TSV_E_SHAPE;
     if (s->cache_dtype != s->in_dtype && s->cache_dtype != TSV_E4M3) return TSV_E_UNSUPPORTED;
     if (s->head_dim > kMaxDim || s->n_heads > 0xffff) return TSV_E_UNSUPPORTED;

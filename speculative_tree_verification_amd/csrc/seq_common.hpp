@@ -29,7 +29,7 @@ constexpr int kStBadSeq = 32;
 // are cut.
 struct SeqPlan {
     int seg;        // tokens per segment
-    int slots;      // upper bound of segments over all sequences
+    long long slots;  // upper bound of segments over all sequences
     bool split;     // whether a sequence may have more than one
     bool sorted;    // slots follow the sequences by falling length, dealt to the XCDs in turn
 };
@@ -65,7 +65,7 @@ inline SeqPlan seq_plan(int n_seqs, int n_tokens, int n_heads, bool matrix) {
     if (seg > 0x7fffffc0LL) seg = 0x7fffffc0LL;
     SeqPlan p;
     p.seg = (int)seg;
-    p.slots = n_tokens / p.seg + (n_seqs < n_tokens ? n_seqs : n_tokens);
+    p.slots = (long long)(n_tokens / p.seg) + (n_seqs < n_tokens ? n_seqs : n_tokens);
     p.split = n_tokens > p.seg;
     p.sorted = n_seqs >= kSortMin && n_seqs <= kSortMax;
     if (p.sorted) p.slots = (p.slots + 7) / 8 * 8;
@@ -163,7 +163,7 @@ __device__ __forceinline__ Segment find_segment(const int32_t* __restrict__ seq_
             s_out->n = cnt;
             s_out->base = base;
             s_out->t0 = a + k * seg;
-            s_out->t1 = min(b, s_out->t0 + seg);
+            s_out->t1 = b - s_out->t0 > seg ? s_out->t0 + seg : b;
             s_out->ok = 1;
         }
         run += total;

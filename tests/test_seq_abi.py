@@ -213,3 +213,19 @@ def test_sizes_below_the_largest_grid_are_not_refused():
         assert L.tree_ssd_prefill_workspace(ctypes.byref(s), ctypes.byref(n)) == OK
     assert commit(attn(batch=MOST // 4), lmax=8, ptrs=[None] * 11) == NULL  # past the size checks
     assert append(attn(batch=2, n_nodes=16 * (MOST - 2)), ptrs=[None] * 9) == NULL
+
+
+def test_rows_near_the_largest_int_are_refused():
+    """Tokens up to 2^31 - 2^16, below which no sum of a row and a step passes an int; and many sequences of one
+    token, whose segments are more than an int holds."""
+    one = dict(n_seqs=1, n_heads=1, head_dim=1, d_state=1)
+    n = ctypes.c_uint64()
+    for tokens, code in ((2 ** 31 - 2 ** 16, OK), (2 ** 31 - 2 ** 16 + 1, UNSUPPORTED), (2 ** 31 - 1, UNSUPPORTED)):
+        assert L.tree_ssd_prefill_workspace(ctypes.byref(seq(n_tokens=tokens, **one)), ctypes.byref(n)) == code
+    assert prefill(seq(n_tokens=2 ** 31 - 1, **one)) == UNSUPPORTED
+    many = dict(one, n_seqs=2 ** 31 - 2 ** 16)
+    assert prefill(seq(n_tokens=2 ** 31 - 2 ** 16, **many)) == UNSUPPORTED
+    # the bound of the segments is not negative: as many states as 16 million sequences and 500 more segments have
+    need = B.prefill_workspace_bytes(16_000_000, 2 ** 31 - 2 ** 16, 1, 1, 1)
+    assert need >= 16_000_000 * 20
+    assert append(attn(n_nodes=2 ** 31 - 1)) == UNSUPPORTED
