@@ -925,6 +925,8 @@ def _launch(at, stream, body):
             return body(_raw_stream(at))
         with torch.cuda.device(at):
             return body(_raw_stream(at))
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != at:
+        raise ValueError(f"stream of {stream.device}, tensors on cuda:{at}")
     with torch.cuda.device(at), _on_stream(stream):
         return body(stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream))
 

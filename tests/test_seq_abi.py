@@ -229,3 +229,18 @@ def test_rows_near_the_largest_int_are_refused():
     need = B.prefill_workspace_bytes(16_000_000, 2 ** 31 - 2 ** 16, 1, 1, 1)
     assert need >= 16_000_000 * 20
     assert append(attn(n_nodes=2 ** 31 - 1)) == UNSUPPORTED
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """Launching there would hand it this device's addresses."""
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 0
+
+    def body(s):
+        raise AssertionError("launched")
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    with pytest.raises(ValueError, match="stream"):
+        B._launch(0, Stream(), body)
