@@ -579,7 +579,7 @@ typedef struct {
     int32_t in_dtype;    /* tsv_dtype of q, k, v, o */
     int32_t cache_dtype; /* in_dtype or TSV_E4M3 (TSV_E_UNSUPPORTED for other pairs) */
     int32_t flags;       /* TSV_FLAG_FORCE_GENERIC or 0 */
-    float scale;         /* factor of the scores, usually head_dim^-1/2 (finite) */
+    float scale;         /* factor of the scores, usually head_dim^-1/2 (finite, also times log2(e)) */
 } tsv_attn_shape;
 
 /*

@@ -11,6 +11,7 @@ namespace {
 
 constexpr int kMaxTree = 1024;
 constexpr int kMaxDim = 256;
+constexpr float kLog2e = 1.44269504088896340736f;  // the scores' exponentials have base 2
 // A launch counts its threads in 32 bits, and all of these have work-groups of
 // 256: one more work-group than this would run as a grid of what is left over
 constexpr long long kMaxBlocks = 0xffffffffLL / 256;
@@ -42,7 +43,7 @@ tsv_status check_attn(const tsv_attn_shape* s, bool tree) {
     if (s->head_dim < 1 || s->n_pages < 0 || s->max_pages < 0) return TSV_E_SHAPE;
     if (s->page_size < 1 || s->page_size > 65536) return TSV_E_SHAPE;
     if ((long long)s->max_pages * s->page_size > kMaxRows) return TSV_E_SHAPE;
-    if (!isfinite(s->scale)) return TSV_E_SHAPE;
+    if (!isfinite(s->scale * kLog2e)) return TSV_E_SHAPE;
     if (s->cache_dtype != s->in_dtype && s->cache_dtype != TSV_E4M3) return TSV_E_UNSUPPORTED;
     if (s->head_dim > kMaxDim || s->n_heads > 0xffff) return TSV_E_UNSUPPORTED;
     return TSV_OK;
@@ -136,7 +137,7 @@ tsv_status tree_attn_verify(const tsv_attn_shape* s, const void* q, const void* 
     const bool e4m3 = s->cache_dtype == TSV_E4M3;
     tsv::AttnArgs a{q, k, v, parent, k_cache, v_cache, e4m3 ? k_scale : nullptr, e4m3 ? v_scale : nullptr, page_table,
                     cache_len, o, tree_status, s->batch, s->n_nodes, s->n_heads, s->n_kv_heads, s->head_dim, s->n_pages,
-                    s->page_size, s->max_pages, s->max_pages * s->page_size, s->scale * 1.44269504088896340736f,
+                    s->page_size, s->max_pages, s->max_pages * s->page_size, s->scale * kLog2e,
                     tsv::page_div(s->page_size)};
     return result(tsv::launch_attn_verify(a, s, need > 0 ? workspace : nullptr, (hipStream_t)stream));
 }

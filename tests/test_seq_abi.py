@@ -244,3 +244,10 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
     monkeypatch.setattr(torch.cuda, "Stream", Stream)
     with pytest.raises(ValueError, match="stream"):
         B._launch(0, Stream(), body)
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38])
+def test_a_factor_that_passes_the_floats_range_is_refused(scale):
+    """The scores' factor is taken times log2(e)."""
+    assert verify(attn(scale=scale)) == SHAPE
+    assert commit(attn(scale=scale)) == SHAPE
