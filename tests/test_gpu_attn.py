@@ -411,6 +411,52 @@ def test_infinite_values_of_the_cache(bnd, dtype, D, T, L, generic):
         assert torch.equal(o[..., rest], clean[..., rest])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_largest_tree_of_one_head_each(bnd, dtype):
+    """1024 nodes, a query head a key head: the largest tables of ancestors, beside the largest tiles."""
+    c = U.cache(48, 1, [70], 2, 128, 16, dtype, dtype)
+    check(bnd, *nodes(48, 1, 1024, 2, 2, 128, dtype), U.trees(48, 1, 1024), c, dtype, f"1024 nodes, one head each, {dtype}")
+
+
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+@pytest.mark.parametrize("H,T", [(64, 1), (300, 1), (200, 3)])
+def test_many_heads_of_one_key_head(bnd, dtype, cdtype, H, T):
+    """More query heads than a block of rows holds."""
+    c = U.cache(49, 2, [77, 600], 1, 64, 16, dtype, cdtype)
+    check(bnd, *nodes(49, 2, T, H, 1, 64, dtype), U.trees(49, 2, T), c, dtype, f"{H} heads T={T} {dtype} {cdtype}")
+
+
+@pytest.mark.parametrize("T", [1, 21])
+def test_shared_pages(bnd, T):
+    """Items that share the pages of a prefix read the same keys."""
+    c = U.cache(50, 3, [500, 9, 40], 2, 64, 16, BF, BF)
+    c["page_table"][1, :31], c["cache_len"][1] = c["page_table"][0, :31], 491
+    c["page_table"][2, :2], c["cache_len"][2] = c["page_table"][0, :2], 32
+    check(bnd, *nodes(50, 3, T, 4, 2, 64, BF), U.trees(50, 3, T), c, BF, f"shared pages T={T}")
+
+
+def test_two_graphs_of_one_pool_replayed_in_turn(bnd):
+    """The workspaces of two captured calls may lie in the same memory of the graphs' pool."""
+    calls, pool = [], None
+    for seed, T in ((51, 1), (52, 30)):
+        c = U.cache(seed, 2, [3000, 40], 2, 64, 16, BF, BF)
+        q, k, v = nodes(seed, 2, T, 4, 2, 64, BF)
+        par, (args, _) = U.trees(seed, 2, T).cuda(), U.cache_args(c)
+        want, o = bnd.attn_verify(q, k, v, par, *args), torch.zeros_like(q)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=pool):
+            bnd.attn_verify(q, k, v, par, *args, o=o)
+        pool = g.pool()
+        calls.append((g, o, want, (q, k, v, par, args)))
+    for _ in range(3):
+        for g, o, want, (q, k, v, par, args) in calls:
+            o.zero_()
+            g.replay()
+            assert torch.equal(o, want)
+            assert torch.equal(bnd.attn_verify(q, k, v, par, *args), want)
+
+
 # ---------------------------------------------------------------- writes
 def expect(c, rows, at, what):
     """The cache with rows ([m,Hk,D] k, v) written at (item, position)s, as header and torch's types define it."""

@@ -106,6 +106,44 @@ def test_prefill_longest_first(bnd, dtype, n, longest):
     check_prefill(bnd, d, lens, dtype)
 
 
+@pytest.mark.parametrize("H,N,G", [(64, 64, 8), (80, 128, 1), (75, 128, 5)])
+def test_prefill_longest_first_in_segments(bnd, H, N, G):
+    """Dealt by falling length, cut, two heads a work-group (one where a group has an odd number)."""
+    lens = [(29 * i + 3) % 40 for i in range(18)]
+    lens[4], lens[11] = 2900, 900
+    d = U.ssd(67 + N, sum(lens) + 2, len(lens), H, 64, N, G, BF, dt_bias=-4.0)
+    assert bnd.prefill_workspace_bytes(len(lens), sum(lens) + 2, H, 64, N, G, BF) > 0
+    check_prefill(bnd, d, lens, BF, start0=1)
+
+
+@pytest.mark.parametrize("dtype,H,P,N,G", SHAPES[4:])
+def test_prefill_segments_of_other_shapes(bnd, dtype, H, P, N, G):
+    d = U.ssd(69 + P, 707, 2, H, P, N, G, dtype, dt_bias=-4.0)
+    assert bnd.prefill_workspace_bytes(2, 707, H, P, N, G, dtype) > 0
+    check_prefill(bnd, d, [690, 17], dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("which", [["dt"], ["h"], ["x"], ["B", "C"], ["x", "dt", "B", "C", "h"]])
+def test_prefill_unaligned_in_segments(bnd, dtype, which):
+    """Each tensor alone at an odd element: steps by words, the combining pass and the choice of the kernel."""
+    d = U.ssd(70, 900, 2, 16, 64, 128, 2, dtype, dt_bias=-4.0)
+    for k in which:
+        buf = torch.empty(d[k].numel() + 1, dtype=d[k].dtype, device="cuda")
+        buf[1:] = d[k].reshape(-1)
+        d[k] = buf[1:].view(d[k].shape)
+    st = torch.zeros(2, dtype=torch.int32, device="cuda")
+    lens, seq = [630, 270], torch.tensor([0, 630, 900], dtype=torch.int32, device="cuda")
+    e, h0 = {k: U.f64(v) for k, v in d.items()}, U.f64(d["h"])
+    y = bnd.prefill(*(d[k] for k in ("x", "dt", "A", "B", "C", "D")), d["h"], seq, seq_status=st)  # h in place, where it is
+    torch.cuda.synchronize()
+    assert st.tolist() == [0, 0]
+    for q, r in enumerate((slice(0, 630), slice(630, 900))):
+        yr, hr, ya, ha = S.scan(e["x"][r], e["dt"][r], e["A"], e["B"][r], e["C"][r], e["D"], h0[q])
+        by, bh = bounds(d, lens[q], yr, ya, ha, dtype)
+        U.within(U.f64(y)[r], yr, by, f"y of sequence {q}, {which}"), U.within(U.f64(d["h"])[q], hr, bh, f"state {q}, {which}")
+
+
 def test_prefill_many_sequences(bnd):
     """More sequences than threads of the search for a segment."""
     lens = [(7 * i) % 4 for i in range(700)]
