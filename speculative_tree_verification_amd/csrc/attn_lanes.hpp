@@ -45,8 +45,9 @@ __device__ __forceinline__ float row_sum(float v) {
     return q.a + q.b;
 }
 
-// Row index of position `pos` of an item in the cache's arrays, or -1 for a page
-// out of range. `page` is what the table holds for it.
+// Whether `page`, what the table holds, is a page of the pool; and the row index of
+// position `pos`, which lies on it, in the cache's arrays (of another page, or of
+// none: take page 0, whose rows exist, and the item's status bit).
 __device__ __forceinline__ bool page_ok(const AttnArgs& a, int page) { return (uint32_t)page < (uint32_t)a.n_pages; }
 __device__ __forceinline__ uint32_t cache_row(const AttnArgs& a, int page, int hk, int pos) {
     const int off = pos - page_of(pos, a.div) * a.page_size;

@@ -5,10 +5,11 @@
 // Plain kernel: the recurrence token by token. A lane holds one row p of the
 // state and a wave a quarter of the columns n, so the decay, the update and the
 // read-out of a token are 3 NS operations per lane without a reduction across
-// lanes; the four waves' parts of y meet in LDS once per 16 tokens. Bound by
-// the vector ALU: 3 P N operations per token and head, four cycles for each 64
-// of them: 45 us for the scan of 1360 tokens, 24 heads, N = 128 (0.8 GFLOP and as
-// much again in 30 us for the local pass).
+// lanes; the four waves' parts of y meet in LDS once per 16 tokens. The scan of
+// 1360 tokens, 24 heads, N = 128 takes 45 us and the local pass 30. Their vector
+// work, 3 P N and 2 P N operations per token and head at four cycles for each 64,
+// is 20 and 13 us of that; what the rest waits for (few waves a SIMD, each of
+// which steps from token to token) was not taken apart.
 #include "seq_common.hpp"
 
 namespace tsv {

@@ -21,7 +21,8 @@
 // weights) of the two waves of a SIMD, which hardly overlap on this GPU (a wave
 // of products and a wave of multiply-adds side by side take three quarters of
 // the sum of their times): 14,000 cycles a chunk, 58 us for the scan of 4096
-// tokens, 80 heads. Tried and not kept: four waves a SIMD with half the rows
+// tokens, 80 heads. With two heads and N = 128 all 256 registers are taken and 13
+// values go to scratch, five words out and seven back a chunk. Tried and not kept: four waves a SIMD with half the rows
 // (spills at 128 registers, 79 us); vector work laid between the products by
 // hand (62 us); residuals by dot products instead of subtractions (60 us); one
 // head (104 us, LDS bound).
@@ -35,7 +36,9 @@
 //    taken from alternating pieces of 4 rows they leave as 16-byte pieces.
 //  - S is read out as two bf16 parts (what is left is at most 2^-18 of an
 //    element, below the rounding of y), w x enters the update as three, so that
-//    the state keeps its 24 bits. W o C B^T is rounded once, as y is.
+//    the state keeps its 24 bits. W o C B^T is rounded once, as y is (y is off by
+//    0.0020 to 0.0021 of its size on average, by 0.0017 from its own rounding): a
+//    second part would be as many products again as the masked one has.
 //  - The next chunk's rows are requested between the products of this one, a
 //    third at a time: a compute unit takes about 32 bytes a cycle from its L2,
 //    and a wave waits where it asks for more at once.
