@@ -12,8 +12,9 @@
 // 64 keys at a time are shared in LDS by four waves; WK 1: of 16 rows each, WK 4: of
 // the same 16 rows, a quarter of the keys each, which meet at the end. Bound by the
 // fp32 matrix rate and, for single tokens, the cache's bytes: 32 tokens over 2200
-// positions each, 8 key heads of 128 (577 MB), 116 us (5.0 TB/s; 359 us in the
-// plain kernel), 4 trees of 63 nodes over them 119 us (78 of 153 TFLOP/s; 721 us).
+// positions each, 8 key heads of 128 (577 MB), 111 us (5.2 TB/s; 359 us in the
+// plain kernel), 4 trees of 63 nodes over them 106 us (85 of 153 TFLOP/s, the matrix
+// unit busy 72% of the cycles; 721 us).
 #include <cfloat>
 
 #include "attn_lanes.hpp"

@@ -16,7 +16,7 @@
 //          are shared in LDS by four waves. 32 rows halve the LDS reads of a row
 //          (and keep two waves a SIMD). Bound by matrix and vector work, which
 //          hardly overlap: 32 trees of 63 nodes over 300 to 4099 positions, 32
-//          query heads, 123 us (0.6 PFLOP/s; matrix unit busy 32% of the time, vector
+//          query heads, 124 us (0.6 PFLOP/s; matrix unit busy 32% of the time, vector
 //          issue 37%). Tried and not kept there: two LDS buffers and one barrier a
 //          tile (127 to 145 us), requests while the scores' product runs (124 us).
 // In both, the loads of the next keys are under way while these are worked on,
