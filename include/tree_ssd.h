@@ -511,7 +511,12 @@ typedef struct {
  *              that is 0), in use until the stream passes this call: calls
  *              that may overlap need one each
  * An empty sequence keeps its state. A long sequence is cut into segments that
- * run side by side, each from the state that the ones before it leave.
+ * run side by side, each from the state that the ones before it leave. Every
+ * work-group reads all of seq_start to find its own: thousands of sequences a
+ * call are meant, not millions.
+ * A token that is not finite reaches its own and the later outputs of its
+ * sequence and its state, and nothing else, as infinities or NaNs (which of the
+ * two may differ from kernel to kernel).
  *
  * Arithmetic: bf16 inputs with P == 64 and N in {64, 128} take an MFMA kernel
  * over chunks of 64 tokens: scores and decays in fp32, their masked product

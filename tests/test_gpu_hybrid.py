@@ -95,3 +95,58 @@ def test_two_calls_at_once_on_two_streams(bnd):
     torch.cuda.synchronize()
     for y, o, h in got:
         assert torch.equal(y, want[0]) and torch.equal(o, want[1]) and torch.equal(h, want_h)
+
+
+def test_step_and_writes_on_a_side_stream_and_in_a_graph(bnd):
+    """The calls without a workspace: ordered on the given stream, and replayed with other lengths and inputs."""
+    n, H, Hk, D, page, T = 3, 4, 2, 64, 16, 9
+    d = U.ssd(91, n, n, H, 64, 128, 1, BF)
+    names = ("x", "dt", "A", "B", "C", "D")
+    c = U.cache(92, n, [20, 0, 33], Hk, D, page, BF, torch.float8_e4m3fn, room=64)
+    cache = [c[m] for m in ("k_cache", "v_cache", "k_scale", "v_scale")]
+    args, scales = U.cache_args(c)
+    g = torch.Generator().manual_seed(93)
+    k, v, kp, vp = (torch.randn(*s, Hk, D, generator=g).to(BF).cuda() for s in ((n, T), (n, T), (40,), (40,)))
+    par = U.trees(94, n, T, "chain").cuda()
+    acc = torch.arange(T, dtype=torch.int32).repeat(n, 1).cuda()
+    count = torch.tensor([3, 9, 0], dtype=torch.int32, device="cuda")
+    seq = torch.tensor([0, 7, 30, 40], dtype=torch.int32, device="cuda")
+    h0, cache0, len0 = d["h"].clone(), [t.clone() for t in cache], c["cache_len"].clone()
+    h, y = h0.clone(), torch.zeros_like(d["x"])
+
+    def once(stream=None):
+        bnd.step(*(d[m] for m in names), h, y=y, stream=stream)
+        bnd.attn_commit(k, v, par, acc, count, *args, **scales, stream=stream)
+        bnd.attn_append(kp, vp, seq, *args, **scales, stream=stream)
+
+    def fresh(lens):
+        h.copy_(h0)
+        y.zero_()
+        c["cache_len"].copy_(len0 + lens)
+        for t, t0 in zip(cache, cache0):
+            t.view(torch.uint8).copy_(t0.view(torch.uint8))
+
+    def result():
+        torch.cuda.synchronize()
+        return [t.clone().view(torch.uint8) for t in (h, y, *cache)]
+
+    want = {}
+    for lens in (0, 5):
+        fresh(lens)
+        once()
+        want[lens] = result()
+    fresh(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda._sleep(20_000_000)  # the current stream is busy
+    once(side)
+    assert all(torch.equal(a, b) for a, b in zip(result(), want[0]))
+    fresh(0)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        once()
+    for lens in (0, 5, 0):
+        fresh(lens)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(result(), want[lens])), lens
