@@ -574,7 +574,7 @@ tsv_status tree_ssd_step(const tsv_shape* s, const void* x, const void* dt, cons
 
 typedef struct {
     int32_t batch;       /* Bt >= 0 (0: nothing to do) */
-    int32_t n_nodes;     /* T in [0, 1024]; tree_attn_append: rows of k and v */
+    int32_t n_nodes;     /* T in [0, 1024]; packed rows: their number (tree_attn_append and those below) */
     int32_t n_heads;     /* query heads H >= 1 */
     int32_t n_kv_heads;  /* Hk >= 1, H % Hk == 0; head h reads key head h / (H / Hk) */
     int32_t head_dim;    /* D in [1, 256] */
@@ -653,6 +653,153 @@ tsv_status tree_attn_append(const tsv_attn_shape* s, const void* k, const void* 
                             const int32_t* page_table, const int32_t* cache_len, void* k_cache,
                             void* v_cache, float* k_scale, float* v_scale, int32_t* seq_status,
                             void* stream);
+
+/* ------------------------------------------------------------------------
+ * The short causal convolution in front of an SSM layer: depthwise over the
+ * C = H P + 2 G N channels of x, B and C (in this order, as the layer's input
+ * projection gives them), with its bias and activation,
+ *   y_t = act(bias + sum_{k < W} weight[W-1-k] u_{t-k}),
+ * split into the x, B and C that the SSM calls take. The state holds the last
+ * W - 1 inputs of an item, oldest first; an item without a past has zeros.
+ *
+ *   xbc    rows of C channels, row_stride elements apart   in_dtype
+ *   weight [C][W]           float      the tap of the newest input last
+ *   bias   [C]              float      may be NULL (0)
+ *   state  [n][W-1][C]      in_dtype
+ *   x [rows][H][P], B, C [rows][G][N]  in_dtype, contiguous; they may not
+ *          overlap xbc or the state
+ * Sums are fp32, rounded once; states are the inputs as they are. SiLU is y /
+ * (1 + exp(-y)). An input that is not finite reaches the outputs of its channel
+ * whose W taps hold it, and nothing else.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int32_t width;      /* W in [2, 4] (TSV_E_UNSUPPORTED above) */
+    int32_t row_stride; /* elements between rows of xbc, at least C */
+    int32_t silu;       /* 1: SiLU, 0: no activation */
+} tsv_conv;
+
+/*
+ * tree_ssd_conv_prefill -- over packed prompts of any lengths: xbc has
+ * s->n_tokens rows, seq_start [n_seqs + 1] and seq_status [n_seqs] (optional;
+ * TSV_ST_BAD_SEQ or 0) as for tree_ssd_prefill; state_inout [n_seqs][W-1][C]
+ * is the state before, then after, each sequence. Rows of no sequence are left
+ * as they were.
+ */
+tsv_status tree_ssd_conv_prefill(const tsv_seq_shape* s, const tsv_conv* c, const void* xbc, const float* weight,
+                                 const float* bias, void* state_inout, const int32_t* seq_start, void* x, void* B,
+                                 void* C, int32_t* seq_status, void* stream);
+
+/*
+ * tree_ssd_conv_step -- one token of each item: xbc has batch rows; s->n_nodes
+ * must be 1 (0: nothing to do). Not idempotent.
+ */
+tsv_status tree_ssd_conv_step(const tsv_shape* s, const tsv_conv* c, const void* xbc, const float* weight,
+                              const float* bias, void* state_inout, void* x, void* B, void* C, void* stream);
+
+/*
+ * tree_ssd_conv_verify -- every node of a packed tree: u_{t-k} is the input of
+ * its k-th ancestor, past the root the state's rows from the last one on. xbc
+ * has batch * n_nodes rows (node i of item b is row b n_nodes + i); parent and
+ * tree_status as for tree_ssd_verify. The state is not written.
+ */
+tsv_status tree_ssd_conv_verify(const tsv_shape* s, const tsv_conv* c, const void* xbc, const float* weight,
+                                const float* bias, const void* state, const int32_t* parent, void* x, void* B, void* C,
+                                int32_t* tree_status, void* stream);
+
+/*
+ * tree_ssd_conv_commit -- the state after the accepted path: its last W - 1
+ * inputs, or those behind what is left of the old state. xbc and parent as for
+ * tree_ssd_conv_verify; accepted, accepted_len, max_path_len and tree_status as
+ * for tree_ssd_commit. c->silu is not used. Not idempotent.
+ */
+tsv_status tree_ssd_conv_commit(const tsv_shape* s, const tsv_conv* c, const void* xbc, void* state_inout,
+                                const int32_t* parent, const int32_t* accepted, const int32_t* accepted_len,
+                                int32_t max_path_len, int32_t* tree_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Queries and keys between a projection and the attention: the heads' norms
+ * with the position rotation, in one pass,
+ *   z = weight x / sqrt(mean(x^2) + eps)         over a head's D elements
+ *   (z_a, z_b) <- (z_a cos t - z_b sin t, z_b cos t + z_a sin t),
+ *   t = position * inv_freq[i],  i < rot_dim / 2,
+ * for the pairs (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) where
+ * `interleaved`; the elements from rot_dim on are z. A NULL weight leaves the
+ * norm out (z = x). fp32 arithmetic, the angle's whole turns taken off in 64
+ * bits (so that far positions lose nothing), one rounding at the end. A head
+ * with an element that is not finite is not finite where it would be in this
+ * arithmetic, other heads are as they would be without it.
+ *
+ *   q [rows][H][D], k [rows][Hk][D], v [rows][Hk][D]   in_dtype, rows
+ *     q_stride, k_stride, v_stride elements apart (slices of one projection's
+ *     output do), at least a row's and below 2^28
+ *   inv_freq [rot_dim / 2], q_weight [D], k_weight [D]   float
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int32_t rot_dim;     /* even, in [0, head_dim] */
+    int32_t interleaved; /* 0 or 1 */
+    float eps;           /* >= 0 */
+    int64_t q_stride, k_stride, v_stride; /* those of a NULL tensor are not used */
+} tsv_rope;
+
+/*
+ * tree_attn_rope -- q and k of s->batch * s->n_nodes rows (a tree's nodes in
+ * the order of tree_attn_verify; any rows with batch 1) at position [rows]
+ * int32: a node's is cache_len[b] + its depth (tree_ssd_tree_info). Rows with
+ * a negative position are left as they were. q_out [rows][H][D], k_out
+ * [rows][Hk][D] contiguous in in_dtype, or q and k themselves where those are
+ * contiguous; q or k may be NULL (left out). Of s the batch, n_nodes, heads,
+ * head_dim and in_dtype are used.
+ */
+tsv_status tree_attn_rope(const tsv_attn_shape* s, const tsv_rope* r, const void* q, const void* k,
+                          const int32_t* position, const float* inv_freq, const float* q_weight, const float* k_weight,
+                          void* q_out, void* k_out, void* stream);
+
+/*
+ * tree_attn_append_rope -- tree_attn_append with the norm and the rotation of
+ * the keys on the way, at their positions in the cache: k and v of s->n_nodes
+ * packed rows enter the cache, and where q is given q_out [n_nodes][H][D] gets
+ * the queries of the same rows. An e4m3 row and its scale are formed from the
+ * row in fp32, without a rounding in between. seq_start and seq_status as for
+ * tree_attn_append; rows of no sequence, and of sequences with a status bit,
+ * are left as they were in q_out too.
+ */
+tsv_status tree_attn_append_rope(const tsv_attn_shape* s, const tsv_rope* r, const void* q, const void* k, const void* v,
+                                 const int32_t* seq_start, const float* inv_freq, const float* q_weight,
+                                 const float* k_weight, const int32_t* page_table, const int32_t* cache_len, void* q_out,
+                                 void* k_cache, void* v_cache, float* k_scale, float* v_scale, int32_t* seq_status,
+                                 void* stream);
+
+/*
+ * tree_attn_prefill -- attention of packed rows of new tokens over the cache
+ * that already holds them (tree_attn_append or tree_attn_append_rope wrote
+ * them, behind cache_len, which is still the number of positions before them):
+ * row seq_start[b] + i of q and o [n_nodes][H][D] is at position p =
+ * cache_len[b] + i of item b and sees the positions j <= p, and with a window
+ * (window > 0) of those only the ones with j > p - window or j < sinks:
+ *   o = sum_j softmax_j(scale q . k_j) v_j.
+ * One row of each item is the single-token step of such a layer. seq_start and
+ * seq_status (TSV_ST_BAD_SEQ and TSV_ST_BAD_CACHE) as for tree_attn_append.
+ * Rows of no sequence, and of sequences with a status bit, are left as they
+ * were. Pages wholly outside the windows of a call's rows and the sinks are not
+ * looked at: their entries of the table may hold anything.
+ *
+ * The work is split over the keys by the lengths found on the device, so that
+ * long prompts, chunks over long caches and single tokens may share a call; a
+ * second launch joins the parts. workspace as for tree_attn_verify, with
+ * tree_attn_prefill_workspace. Every work-group reads all of seq_start and
+ * cache_len: thousands of sequences a call are meant, not millions.
+ *
+ * Arithmetic: fp32 scores, maxima, sums and accumulators. A key or value that
+ * is not finite reaches the rows that see its position and no others.
+ * TSV_E_SHAPE for a negative window or sinks, and for sinks without a window.
+ */
+tsv_status tree_attn_prefill(const tsv_attn_shape* s, int32_t window, int32_t sinks, const void* q,
+                             const int32_t* seq_start, const void* k_cache, const void* v_cache, const float* k_scale,
+                             const float* v_scale, const int32_t* page_table, const int32_t* cache_len, void* o,
+                             int32_t* seq_status, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that tree_attn_prefill needs for this shape (host only). */
+tsv_status tree_attn_prefill_workspace(const tsv_attn_shape* s, uint64_t* bytes);
 
 /* Static, human-readable name of a tsv_status value. */
 const char* tree_ssd_status_string(int32_t status);

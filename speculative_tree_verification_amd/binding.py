@@ -9,8 +9,10 @@ missing, importing this module raises.
 Entry points mirror include/tree_ssd.h: ``verify``, ``commit``,
 ``commit_layers``, ``accept_greedy``, ``tree_info``, for the gated delta rule
 ``gdn_verify`` and ``gdn_commit``, for sequences around the tree ``prefill``
-and ``step``, and for a hybrid model's attention layers ``attn_verify``,
-``attn_commit`` and ``attn_append``.
+and ``step``, for the convolution in front of an SSM layer ``conv_prefill``,
+``conv_step``, ``conv_verify`` and ``conv_commit``, and for a hybrid model's
+attention layers ``attn_rope``, ``attn_verify``, ``attn_prefill``,
+``attn_commit``, ``attn_append`` and ``attn_append_rope``.
 """
 from __future__ import annotations
 
@@ -39,7 +41,9 @@ EXPORTS = ("tree_ssd_verify", "tree_ssd_commit", "tree_ssd_commit_layers", "tree
            "tree_gdn_commit", "tree_ssd_unroll_plan", "tree_ssd_unroll_gather", "tree_ssd_seq_scan",
            "tree_ssd_snapshot_verify", "tree_ssd_snapshot_commit", "tree_ssd_accept_stochastic",
            "tree_ssd_commit_layers_static", "tree_ssd_prefill", "tree_ssd_prefill_workspace", "tree_ssd_step",
-           "tree_attn_verify", "tree_attn_verify_workspace", "tree_attn_commit", "tree_attn_append")
+           "tree_attn_verify", "tree_attn_verify_workspace", "tree_attn_commit", "tree_attn_append",
+           "tree_ssd_conv_prefill", "tree_ssd_conv_step", "tree_ssd_conv_verify", "tree_ssd_conv_commit",
+           "tree_attn_rope", "tree_attn_append_rope", "tree_attn_prefill", "tree_attn_prefill_workspace")
 STATIC_MAX_LAYERS = 1024  # TSV_STATIC_MAX_LAYERS
 ST_OVER_CAPACITY = 8
 ST_BAD_TOKEN = 16
@@ -67,6 +71,17 @@ class AttnShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("batch", "n_nodes", "n_heads", "n_kv_heads", "head_dim", "n_pages",
                                               "page_size", "max_pages", "in_dtype", "cache_dtype", "flags")] + \
         [("scale", ctypes.c_float)]
+
+
+class Conv(ctypes.Structure):
+    """tsv_conv"""
+    _fields_ = [(n, ctypes.c_int32) for n in ("width", "row_stride", "silu")]
+
+
+class Rope(ctypes.Structure):
+    """tsv_rope"""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float)] + \
+        [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")]
 
 
 class CommitLayer(ctypes.Structure):
@@ -134,8 +149,20 @@ def _load():
     L.tree_attn_verify_workspace.argtypes = [ctypes.POINTER(AttnShape), ctypes.POINTER(u64)]
     L.tree_attn_commit.argtypes = [ctypes.POINTER(AttnShape)] + [_VP] * 5 + [ctypes.c_int32] + [_VP] * 8
     L.tree_attn_append.argtypes = [ctypes.POINTER(AttnShape)] + [_VP] * 11
+    seq_conv, tree_conv = ([ctypes.POINTER(t), ctypes.POINTER(Conv)] for t in (SeqShape, Shape))
+    L.tree_ssd_conv_prefill.argtypes = seq_conv + [_VP] * 10
+    L.tree_ssd_conv_step.argtypes = tree_conv + [_VP] * 8
+    L.tree_ssd_conv_verify.argtypes = tree_conv + [_VP] * 10
+    L.tree_ssd_conv_commit.argtypes = tree_conv + [_VP] * 5 + [ctypes.c_int32, _VP, _VP]
+    attn_rope = [ctypes.POINTER(AttnShape), ctypes.POINTER(Rope)]
+    L.tree_attn_rope.argtypes = attn_rope + [_VP] * 9
+    L.tree_attn_append_rope.argtypes = attn_rope + [_VP] * 16
+    L.tree_attn_prefill.argtypes = [ctypes.POINTER(AttnShape), ctypes.c_int32, ctypes.c_int32] + [_VP] * 11 + [u64, _VP]
+    L.tree_attn_prefill_workspace.argtypes = [ctypes.POINTER(AttnShape), ctypes.POINTER(u64)]
     for f in (L.tree_ssd_prefill, L.tree_ssd_prefill_workspace, L.tree_ssd_step, L.tree_attn_verify,
-              L.tree_attn_verify_workspace, L.tree_attn_commit, L.tree_attn_append):
+              L.tree_attn_verify_workspace, L.tree_attn_commit, L.tree_attn_append, L.tree_ssd_conv_prefill,
+              L.tree_ssd_conv_step, L.tree_ssd_conv_verify, L.tree_ssd_conv_commit, L.tree_attn_rope,
+              L.tree_attn_append_rope, L.tree_attn_prefill, L.tree_attn_prefill_workspace):
         f.restype = ctypes.c_int
     return L
 
@@ -1039,11 +1066,15 @@ def step(x, dt, A, B, C, D, h, y=None, stream=None):
 
 
 def _attn_fields(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, batch, rows, n_heads, scale,
-                 force_generic):
-    """Checks what every attention call has of the cache: the fields of tsv_attn_shape."""
+                 force_generic, query: bool = False):
+    """Checks what every attention call has of the cache: the fields of tsv_attn_shape. k: the call's keys, or
+    (query) its queries."""
     at, ct = k.get_device(), k_cache.dtype
     n_pages, Hk, page_size, D = k_cache.shape
-    if k.shape[-2:] != (Hk, D):
+    if query:
+        if k.shape[-1] != D:
+            raise ValueError(f"q: head_dim {k.shape[-1]} != the cache's {D}")
+    elif k.shape[-2:] != (Hk, D):
         raise ValueError(f"k: heads and head_dim {tuple(k.shape[-2:])} != the cache's {(Hk, D)}")
     e4m3 = ct is torch.float8_e4m3fn
     if not e4m3 and ct is not k.dtype:
@@ -1156,5 +1187,263 @@ def attn_append(k, v, seq_start, k_cache, v_cache, page_table, cache_len, k_scal
                                   v_cache.data_ptr(), _opt(k_scale), _opt(v_scale), _opt(seq_status), s)
         if rc != 0:
             raise TreeSSDError(rc, "tree_attn_append")
+
+    _launch(at, stream, body)
+
+
+@functools.lru_cache(maxsize=4096)
+def _attn_prefill_workspace(*fields) -> int:
+    need = ctypes.c_uint64()
+    rc = lib.tree_attn_prefill_workspace(ctypes.byref(AttnShape(*fields)), ctypes.byref(need))
+    if rc != 0:
+        raise TreeSSDError(rc, "tree_attn_prefill_workspace")
+    return need.value
+
+
+def attn_prefill(q, seq_start, k_cache, v_cache, page_table, cache_len, k_scale=None, v_scale=None, window: int = 0,
+                 sinks: int = 0, scale: Optional[float] = None, o=None, seq_status=None, workspace=None, stream=None,
+                 force_generic: bool = False):
+    """o [L,H,D]: attention of packed rows of new tokens, q [L,H,D] (seq_start
+    [Bt+1] int32), over the cache that already holds them behind its cache_len
+    positions (tree_attn_prefill): ``attn_append`` or ``attn_append_rope`` first,
+    cache_len grows afterwards. ``window`` > 0: a row sees its last ``window``
+    positions, itself included, and the first ``sinks``. Caches, scales, ``scale``
+    and ``workspace`` as for ``attn_verify``. Rows of no sequence are left as they
+    were in a given ``o``, and undefined in one made here."""
+    L, H, D = q.shape
+    at, io, Bt = q.get_device(), q.dtype, cache_len.shape[0]
+    _need(q, "q", (L, H, D), io, at)
+    _need(seq_start, "seq_start", (Bt + 1,), torch.int32, at)
+    if seq_status is not None:
+        _need(seq_status, "seq_status", (Bt,), torch.int32, at)
+    if o is not None:
+        _need(o, "o", (L, H, D), io, at)
+    fields = _attn_fields(q, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, L, H,
+                          D ** -0.5 if scale is None else float(scale), force_generic, query=True)
+
+    def body(s):
+        out = torch.empty_like(q) if o is None else o
+        ws, size = _workspace(_attn_prefill_workspace(*fields), workspace, at)
+        rc = lib.tree_attn_prefill(AttnShape(*fields), window, sinks, q.data_ptr(), seq_start.data_ptr(),
+                                   k_cache.data_ptr(), v_cache.data_ptr(), _opt(k_scale), _opt(v_scale),
+                                   page_table.data_ptr(), cache_len.data_ptr(), out.data_ptr(), _opt(seq_status),
+                                   _opt(ws), size, s)
+        if rc != 0:
+            raise TreeSSDError(rc, "tree_attn_prefill")
+        return out
+
+    return _launch(at, stream, body)
+
+
+def attn_prefill_workspace_bytes(batch, n_rows, n_heads, n_kv_heads, head_dim, page_size, max_pages,
+                                 dtype=torch.bfloat16, cache_dtype=None, n_pages: int = 1) -> int:
+    """Bytes of workspace an ``attn_prefill`` of these sizes needs."""
+    io = TSV_BF16 if dtype == torch.bfloat16 else TSV_F32
+    return _attn_prefill_workspace(batch, n_rows, n_heads, n_kv_heads, head_dim, n_pages, page_size, max_pages, io,
+                                   TSV_E4M3 if cache_dtype == torch.float8_e4m3fn else io, 0, 1.0)
+
+
+def _need_rows(t, name: str, rows, row, dtype, at: int) -> int:
+    """Checks rows [*rows][*row], each contiguous, that lie one after another at one distance, and returns that
+    distance in elements."""
+    if t.shape != (*rows, *row) or t.dtype is not dtype or t.get_device() != at:
+        _check(t, name, (*rows, *row), dtype, torch.device("cuda", at) if at >= 0 else torch.device("cpu"))
+    width, steps = 1, t.stride()
+    for size, step in zip(reversed(row), reversed(steps)):
+        if size > 1 and step != width:
+            raise ValueError(f"{name}: a row must be contiguous")
+        width *= size
+    apart, count = None, 1  # the distance, where there is more than one row; rows so far
+    for size, step in zip(reversed(rows), reversed(steps[:len(rows)])):
+        if size > 1:
+            if apart is None:
+                apart = step
+            elif step != count * apart:
+                raise ValueError(f"{name}: rows must lie at one distance from each other")
+            count *= size
+    return width if apart is None else apart
+
+
+def _rope_fields(q, k, v, inv_freq, q_weight, k_weight, eps, interleaved, rows, heads, at, io):
+    """Checks what the rotation takes; rows: the tensors' leading sizes, heads: H, Hk, D."""
+    H, Hk, D = heads
+    strides = [0 if t is None else _need_rows(t, name, rows, (n, D), io, at)
+               for t, name, n in ((q, "q", H), (k, "k", Hk), (v, "v", Hk))]
+    _need(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float32, at)
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _need(t, name, (D,), torch.float32, at)
+    return Rope(2 * inv_freq.numel(), int(interleaved), eps, *strides)
+
+
+def attn_rope(q, k, position, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+              q_out=None, k_out=None, stream=None):
+    """(q_out, k_out): the heads' norms (where a weight [D] is given) and the
+    position rotation of q [...,H,D] and k [...,Hk,D] (tree_attn_rope); either
+    may be None. position [...] int32 (negative: the row is left as it was),
+    inv_freq [rot_dim/2] float32; ``interleaved`` rotates neighbouring elements,
+    otherwise (i, i + rot_dim/2). Rows may be slices of a projection's output; a
+    contiguous q or k may be its own output."""
+    given = q if q is not None else k
+    if given is None:
+        raise ValueError("q or k is needed")
+    rows, D = tuple(given.shape[:-2]), given.shape[-1]
+    at, io = given.get_device(), given.dtype
+    H, Hk = (1 if t is None else t.shape[-2] for t in (q, k))
+    rope = _rope_fields(q, k, None, inv_freq, q_weight, k_weight, eps, interleaved, rows, (H, Hk, D), at, io)
+    _need(position, "position", rows, torch.int32, at)
+    for t, o, name, n in ((q, q_out, "q_out", H), (k, k_out, "k_out", Hk)):
+        if o is not None:
+            if t is None:
+                raise ValueError(f"{name} is given without {name[0]}")
+            _need(o, name, (*rows, n, D), io, at)
+    n_rows = position.numel()
+    # (one key head for the shape's H % Hk where there are none)
+    shape = AttnShape(1, n_rows, H if q is not None else Hk, Hk if k is not None else 1, D, 0, 1, 0, _dtype_code(given),
+                      _dtype_code(given), 0, 1.0)
+
+    def body(s):
+        qo, ko = (None if t is None else torch.empty(t.shape, dtype=io, device=t.device) if o is None else o
+                  for t, o in ((q, q_out), (k, k_out)))
+        rc = lib.tree_attn_rope(shape, rope, _opt(q), _opt(k), position.data_ptr(), inv_freq.data_ptr(), _opt(q_weight),
+                                _opt(k_weight), _opt(qo), _opt(ko), s)
+        if rc != 0:
+            raise TreeSSDError(rc, "tree_attn_rope")
+        return qo, ko
+
+    return _launch(at, stream, body)
+
+
+def attn_append_rope(q, k, v, seq_start, inv_freq, k_cache, v_cache, page_table, cache_len, k_scale=None, v_scale=None,
+                     q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False, q_out=None,
+                     seq_status=None, stream=None):
+    """``attn_append`` of packed rows k, v [L,Hk,D] with the norm and the rotation
+    of the keys on the way, at their positions in the cache
+    (tree_attn_append_rope). Returns q_out [L,H,D], the queries of the same rows,
+    or None where q is None. Rows may be slices of a projection's output; the
+    other arguments as for ``attn_rope``. Rows of no sequence are left as they
+    were in a given ``q_out``, and undefined in one made here."""
+    L, Hk, D = k.shape
+    at, io, Bt = k.get_device(), k.dtype, cache_len.shape[0]
+    H = Hk if q is None else q.shape[-2]
+    rope = _rope_fields(q, k, v, inv_freq, q_weight, k_weight, eps, interleaved, (L,), (H, Hk, D), at, io)
+    _need(seq_start, "seq_start", (Bt + 1,), torch.int32, at)
+    if seq_status is not None:
+        _need(seq_status, "seq_status", (Bt,), torch.int32, at)
+    if q_out is not None:
+        if q is None:
+            raise ValueError("q_out is given without q")
+        _need(q_out, "q_out", (L, H, D), io, at)
+    fields = _attn_fields(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, L, H, 1.0, False)
+
+    def body(s):
+        qo = None if q is None else torch.empty((L, H, D), dtype=io, device=q.device) if q_out is None else q_out
+        rc = lib.tree_attn_append_rope(AttnShape(*fields), rope, _opt(q), k.data_ptr(), v.data_ptr(),
+                                       seq_start.data_ptr(), inv_freq.data_ptr(), _opt(q_weight), _opt(k_weight),
+                                       page_table.data_ptr(), cache_len.data_ptr(), _opt(qo), k_cache.data_ptr(),
+                                       v_cache.data_ptr(), _opt(k_scale), _opt(v_scale), _opt(seq_status), s)
+        if rc != 0:
+            raise TreeSSDError(rc, "tree_attn_append_rope")
+        return qo
+
+    return _launch(at, stream, body)
+
+
+def _conv_fields(xbc, weight, bias, state, x, B, C, rows, n, at, io):
+    """Checks what the convolutions take: (H, P, N, G), tsv_conv's width and row stride."""
+    (H, P), (G, N) = x.shape[-2:], B.shape[-2:]
+    channels = H * P + 2 * G * N
+    back = state.shape[1]
+    _need(state, "state", (n, back, channels), io, at)
+    _need(weight, "weight", (channels, back + 1), torch.float32, at)
+    if bias is not None:
+        _need(bias, "bias", (channels,), torch.float32, at)
+    for t, name, tail in ((x, "x", (H, P)), (B, "B", (G, N)), (C, "C", (G, N))):
+        _need(t, name, (*rows, *tail), io, at)
+    return (H, P, N, G), (back + 1, _need_rows(xbc, "xbc", rows, (channels,), io, at))
+
+
+def conv_prefill(xbc, weight, bias, state, seq_start, x, B, C, silu: bool = True, seq_status=None, stream=None):
+    """The short causal convolution over packed prompts (tree_ssd_conv_prefill):
+    x [L,H,P], B, C [L,G,N] are written from xbc [L,HP+2GN] (rows may be slices
+    of a projection's output), weight [HP+2GN,W] and bias (or None) float32;
+    state [n,W-1,HP+2GN], the inputs before each sequence, becomes those at its
+    end. seq_start [n+1] int32."""
+    L, n, at, io = xbc.shape[0], state.shape[0], xbc.get_device(), xbc.dtype
+    (H, P, N, G), conv = _conv_fields(xbc, weight, bias, state, x, B, C, (L,), n, at, io)
+    _need(seq_start, "seq_start", (n + 1,), torch.int32, at)
+    if seq_status is not None:
+        _need(seq_status, "seq_status", (n,), torch.int32, at)
+    shape = SeqShape(n, L, H, P, N, G, _dtype_code(xbc), 0)
+
+    def body(s):
+        rc = lib.tree_ssd_conv_prefill(shape, Conv(*conv, int(silu)), xbc.data_ptr(), weight.data_ptr(), _opt(bias),
+                                       state.data_ptr(), seq_start.data_ptr(), x.data_ptr(), B.data_ptr(), C.data_ptr(),
+                                       _opt(seq_status), s)
+        if rc != 0:
+            raise TreeSSDError(rc, "tree_ssd_conv_prefill")
+
+    _launch(at, stream, body)
+
+
+def conv_step(xbc, weight, bias, state, x, B, C, silu: bool = True, stream=None):
+    """``conv_prefill`` for one token of each item (tree_ssd_conv_step): xbc
+    [Bt,HP+2GN], x [Bt,H,P], B, C [Bt,G,N]; state advanced in place."""
+    Bt, at, io = xbc.shape[0], xbc.get_device(), xbc.dtype
+    (H, P, N, G), conv = _conv_fields(xbc, weight, bias, state, x, B, C, (Bt,), Bt, at, io)
+    shape = Shape(Bt, 1, H, P, N, G, _dtype_code(xbc), 0, 0)
+
+    def body(s):
+        rc = lib.tree_ssd_conv_step(shape, Conv(*conv, int(silu)), xbc.data_ptr(), weight.data_ptr(), _opt(bias),
+                                    state.data_ptr(), x.data_ptr(), B.data_ptr(), C.data_ptr(), s)
+        if rc != 0:
+            raise TreeSSDError(rc, "tree_ssd_conv_step")
+
+    _launch(at, stream, body)
+
+
+def conv_verify(xbc, weight, bias, state, parent, x, B, C, silu: bool = True, tree_status=None, stream=None):
+    """The convolution over the nodes of packed trees (tree_ssd_conv_verify): a
+    node's earlier inputs are its ancestors', then the state's. xbc
+    [Bt,T,HP+2GN], x [Bt,T,H,P], B, C [Bt,T,G,N]; the state is not changed."""
+    Bt, T = xbc.shape[:2]
+    at, io = xbc.get_device(), xbc.dtype
+    (H, P, N, G), conv = _conv_fields(xbc, weight, bias, state, x, B, C, (Bt, T), Bt, at, io)
+    _need(parent, "parent", (Bt, T), torch.int32, at)
+    if tree_status is not None:
+        _need(tree_status, "tree_status", (Bt,), torch.int32, at)
+    shape = Shape(Bt, T, H, P, N, G, _dtype_code(xbc), 0, 0)
+
+    def body(s):
+        rc = lib.tree_ssd_conv_verify(shape, Conv(*conv, int(silu)), xbc.data_ptr(), weight.data_ptr(), _opt(bias),
+                                      state.data_ptr(), parent.data_ptr(), x.data_ptr(), B.data_ptr(), C.data_ptr(),
+                                      _opt(tree_status), s)
+        if rc != 0:
+            raise TreeSSDError(rc, "tree_ssd_conv_verify")
+
+    _launch(at, stream, body)
+
+
+def conv_commit(xbc, state, parent, accepted, accepted_len, n_heads: int, head_dim: int, n_groups: int, d_state: int,
+                tree_status=None, stream=None):
+    """The convolution's state [Bt,W-1,HP+2GN] after the accepted paths, in place
+    (tree_ssd_conv_commit): xbc [Bt,T,HP+2GN] as for ``conv_verify``."""
+    Bt, T = xbc.shape[:2]
+    at, io = xbc.get_device(), xbc.dtype
+    channels, back, Lmax = n_heads * head_dim + 2 * n_groups * d_state, state.shape[1], accepted.shape[1]
+    _need(state, "state", (Bt, back, channels), io, at)
+    _need(parent, "parent", (Bt, T), torch.int32, at)
+    _need(accepted, "accepted", (Bt, Lmax), torch.int32, at)
+    _need(accepted_len, "accepted_len", (Bt,), torch.int32, at)
+    if tree_status is not None:
+        _need(tree_status, "tree_status", (Bt,), torch.int32, at)
+    conv = Conv(back + 1, _need_rows(xbc, "xbc", (Bt, T), (channels,), io, at), 0)
+    shape = Shape(Bt, T, n_heads, head_dim, d_state, n_groups, _dtype_code(xbc), 0, 0)
+
+    def body(s):
+        rc = lib.tree_ssd_conv_commit(shape, conv, xbc.data_ptr(), state.data_ptr(), parent.data_ptr(),
+                                      accepted.data_ptr(), accepted_len.data_ptr(), Lmax, _opt(tree_status), s)
+        if rc != 0:
+            raise TreeSSDError(rc, "tree_ssd_conv_commit")
 
     _launch(at, stream, body)

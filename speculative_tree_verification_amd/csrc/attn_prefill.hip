@@ -1,0 +1,297 @@
+// attn_prefill.hip -- attention of packed rows over the paged cache: the plain fp32
+// kernel (any head_dim up to 256, any types), the join of the parts, and the choice of
+// the kernel.
+//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(scale log2(e) q_i . k_j - m_i)
+// over the positions j <= cache_len + i that row i sees, in one pass with a running maximum
+// m_i and sum; parts of the keys (attn_chunk.hpp) are joined by
+//   o = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k,  m = max_k m_k.
+//
+// Plain kernel: a work-group takes kRows rows (token, query head) of one key head; its
+// waves take 64 keys each in turn. Scores: a lane per key, the rows' q from LDS (the same
+// for all lanes). Values: lanes over the head_dim, weights from LDS. Bound by the vector
+// ALU and the LDS broadcasts (4 D operations per row and key).
+#include "attn_chunk.hpp"
+
+namespace tsv {
+namespace {
+
+constexpr int kRows = 8;
+
+template <typename TC>
+__device__ __forceinline__ float elem(const TC* p, size_t i) {
+    if constexpr (sizeof(TC) == 1)
+        return e4m3_ld((const uint8_t*)p + i);
+    else
+        return Elem<TC>::ld(p, i);
+}
+
+template <typename TIO, typename TC, int DV>
+__global__ __launch_bounds__(256) void chunk_plain_kernel(ChunkArgs a, ChunkPlan plan, ChunkWorkspace ws) {
+    __shared__ float s_q[kRows][256], s_p[4][kRows][kWave], s_o[kRows][256], s_ml[4][kRows][2];
+    __shared__ long long s_off[4][kWave];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int hk = blockIdx.x % a.Hk;
+    const ChunkUnit u = find_unit<false>(a, plan, blockIdx.x / a.Hk);
+    if (blockIdx.x == 0 && w == 0) chunk_status(a, plan, u.bad);
+    if (!u.ok) return;
+    const int bad = __syncthreads_or(chunk_pages_bad<256>(a, u));
+    if (u.lead && hk == 0 && tid == 0 && a.status) a.status[u.seq] = bad ? kStBadCache : 0;
+    if (bad) return;
+    const ChunkKeys kk = chunk_keys(a, plan, u);
+    const int D = a.D, g = a.H / a.Hk, R = u.n * g, row0 = u.block * kRows;
+    for (int i = tid; i < kRows * D; i += 256) {
+        const int r = row0 + i / D;
+        s_q[i / D][i % D] = r < R ? Elem<TIO>::ld((const TIO*)a.q, (((size_t)u.start + r / g) * a.H + hk * g + r % g) * D + i % D) : 0.f;
+    }
+    __syncthreads();
+    float m[kRows], l[kRows], o[kRows][DV];
+    int own[kRows];  // the rows' positions
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        own[r] = u.old + min(row0 + r, R - 1) / g;
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < DV; ++i) o[r][i] = 0.f;
+    }
+    const TC* kp = (const TC*)a.k_cache;
+    const TC* vp = (const TC*)a.v_cache;
+    for (int t0 = kk.k0 + w * kWave; t0 < kk.k1; t0 += 4 * kWave) {
+        const int v = t0 + lane, n = min(kWave, kk.k1 - t0);
+        long long key = -1;
+        int pos = 0;
+        float ks = 1.f, vs = 1.f;
+        if (v < kk.k1) {
+            pos = chunk_pos(kk, v);
+            const int page = page_of(pos, a.div);
+            key = ((long long)a.page_table[(size_t)u.seq * a.max_pages + page] * a.Hk + hk) * a.page_size + (pos - page * a.page_size);
+            if (a.k_scale) {
+                ks = a.k_scale[key];
+                vs = a.v_scale[key];
+            }
+        }
+        float s[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) s[r] = 0.f;
+        if (key >= 0) {
+            for (int d = 0; d < D; ++d) {
+                const float kv = elem<TC>(kp, (size_t)key * D + d);
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) s[r] = fmaf(s_q[r][d], kv, s[r]);
+            }
+        }
+        s_off[w][lane] = key;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const bool seen = key >= 0 && pos <= own[r] && (own[r] - pos < a.window || pos < a.sinks);
+            const float sc = seen ? s[r] * ks * a.scale_log2 : -INFINITY;
+            float top = sc;
+#pragma unroll
+            for (int x = 1; x < kWave; x <<= 1) top = fmaxf(top, __shfl_xor(top, x, kWave));
+            // fmaxf passes over a NaN, which the weights then carry
+            const float mn = fmaxf(m[r], top), base = mn == -INFINITY ? 0.f : mn;
+            const float p = seen ? exp2f(sc - base) : 0.f, al = exp2f(m[r] - base);
+            float sum = p;
+#pragma unroll
+            for (int x = 1; x < kWave; x <<= 1) sum += __shfl_xor(sum, x, kWave);
+            l[r] = l[r] * al + sum;
+            m[r] = mn;
+#pragma unroll
+            for (int i = 0; i < DV; ++i) o[r][i] *= al;
+            s_p[w][r][lane] = p * vs;
+            if (!seen) s_p[w][r][lane] = 0.f;  // (a scale that is not finite)
+        }
+        wave_sync();
+        for (int j = 0; j < n; ++j) {
+            const long long at = s_off[w][j];
+#pragma unroll
+            for (int i = 0; i < DV; ++i) {
+                const int d = lane + i * kWave;
+                if (d >= D) continue;
+                const float x = elem<TC>(vp, (size_t)at * D + d);
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    // a key that row r does not see has weight 0, also where its value is not finite
+                    const float p = s_p[w][r][j];
+                    o[r][i] = p == 0.f ? o[r][i] : fmaf(p, x, o[r][i]);
+                }
+            }
+        }
+        wave_sync();
+    }
+    // the four waves' parts
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+        if (lane == 0) {
+            s_ml[w][r][0] = m[r];
+            s_ml[w][r][1] = l[r];
+        }
+    __syncthreads();
+    float mt[kRows], lt[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        mt[r] = fmaxf(fmaxf(s_ml[0][r][0], s_ml[1][r][0]), fmaxf(s_ml[2][r][0], s_ml[3][r][0]));
+        const float base = mt[r] == -INFINITY ? 0.f : mt[r];
+        lt[r] = 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) lt[r] += s_ml[x][r][1] * exp2f(s_ml[x][r][0] - base);
+        const float al = exp2f(m[r] - base);
+#pragma unroll
+        for (int i = 0; i < DV; ++i) o[r][i] *= al;
+    }
+    for (int x = 0; x < 4; ++x) {
+        if (w == x) {
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                for (int i = 0; i < DV; ++i) {
+                    const int d = lane + i * kWave;
+                    s_o[r][d] = x == 0 ? o[r][i] : s_o[r][d] + o[r][i];
+                }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        if (row0 + r >= R) break;
+        if (u.parts > 1) {
+            const size_t at = ((size_t)u.slot * a.Hk + hk) * kRows + r;
+            if (tid < D) ws.o[at * D + tid] = s_o[r][tid];
+            if (tid < 2) ws.ml[at * 2 + tid] = tid ? lt[r] : mt[r];
+        } else if (tid < D) {
+            const int row = row0 + r;
+            Elem<TIO>::st((TIO*)a.o, (((size_t)u.start + row / g) * a.H + hk * g + row % g) * D + tid, s_o[r][tid] / lt[r]);
+        }
+    }
+}
+
+// Lanes take 4 elements of a row each, LPR lanes a row, which reads its block's parts four
+// at once.
+template <typename TIO, int LPR>
+__global__ __launch_bounds__(256) void chunk_join_kernel(ChunkArgs a, ChunkPlan plan, ChunkWorkspace ws, int groups) {
+    constexpr int kAt = 256 / LPR;
+    const int tid = threadIdx.x, group = blockIdx.x % groups, unit = blockIdx.x / groups, hk = unit % a.Hk;
+    const ChunkUnit u = find_unit<true>(a, plan, unit / a.Hk);
+    if (!u.ok) return;
+    const int D = a.D, g = a.H / a.Hk, R = u.n * g, r = group * kAt + tid / LPR, row = u.block * plan.rows + r;
+    if (__syncthreads_or(chunk_pages_bad<256>(a, u)) || r >= plan.rows || row >= R) return;
+    const int d = tid % LPR * 4;
+    const bool whole = D % 4 == 0 && (uintptr_t)a.o % (4 * sizeof(TIO)) == 0;  // pieces of four, aligned
+    auto piece = [&](const float* p) { return d >= D ? make_float4(0.f, 0.f, 0.f, 0.f) : whole ? ld4<true>(p, 4) : ld4<false>(p, D - d); };
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < u.parts; k0 += 4) {
+        float mk[4], lk[4];
+        float4 v[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            mk[x] = -INFINITY;
+            lk[x] = 0.f;
+            v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 + x >= u.parts) continue;
+            const size_t at = ((size_t)(u.slot + k0 + x) * a.Hk + hk) * plan.rows + r;
+            mk[x] = ws.ml[at * 2];
+            lk[x] = ws.ml[at * 2 + 1];
+            v[x] = piece(ws.o + at * D + d);
+        }
+        const float mn = fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), m);
+        const float base = mn == -INFINITY ? 0.f : mn, old = exp2f(m - base);
+        l *= old;
+        o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float f = exp2f(mk[x] - base);
+            l = fmaf(f, lk[x], l);
+            o.x = fmaf(f, v[x].x, o.x);
+            o.y = fmaf(f, v[x].y, o.y);
+            o.z = fmaf(f, v[x].z, o.z);
+            o.w = fmaf(f, v[x].w, o.w);
+        }
+        m = mn;
+    }
+    if (d >= D) return;
+    TIO* to = (TIO*)a.o + (((size_t)u.start + row / g) * a.H + hk * g + row % g) * D + d;
+    const float f[4] = {o.x / l, o.y / l, o.z / l, o.w / l};
+    if (whole) {
+        if constexpr (sizeof(TIO) == 4)
+            *(float4*)to = make_float4(f[0], f[1], f[2], f[3]);
+        else
+            *(uint2*)to = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (d + e < D) Elem<TIO>::st(to, e, f[e]);
+    }
+}
+
+template <typename TIO, typename TC>
+void launch_plain(const ChunkArgs& a, const ChunkPlan& p, const ChunkWorkspace& ws, dim3 grid, hipStream_t stream) {
+    if (a.D <= 64)
+        hipLaunchKernelGGL((chunk_plain_kernel<TIO, TC, 1>), grid, dim3(256), 0, stream, a, p, ws);
+    else if (a.D <= 128)
+        hipLaunchKernelGGL((chunk_plain_kernel<TIO, TC, 2>), grid, dim3(256), 0, stream, a, p, ws);
+    else
+        hipLaunchKernelGGL((chunk_plain_kernel<TIO, TC, 4>), grid, dim3(256), 0, stream, a, p, ws);
+}
+
+constexpr int lanes_of(int D) { return D <= 64 ? 16 : D <= 128 ? 32 : 64; }
+int groups_of(int rows, int D) { return (rows + 256 / lanes_of(D) - 1) / (256 / lanes_of(D)); }
+
+template <typename TIO>
+void launch_join(const ChunkArgs& a, const ChunkPlan& p, const ChunkWorkspace& ws, hipStream_t stream) {
+    const int groups = groups_of(p.rows, a.D);
+    const dim3 grid((unsigned)((long long)(p.want / a.Hk) * a.Hk * groups));
+    if (grid.x == 0) return;
+    if (a.D <= 64)
+        hipLaunchKernelGGL((chunk_join_kernel<TIO, 16>), grid, dim3(256), 0, stream, a, p, ws, groups);
+    else if (a.D <= 128)
+        hipLaunchKernelGGL((chunk_join_kernel<TIO, 32>), grid, dim3(256), 0, stream, a, p, ws, groups);
+    else
+        hipLaunchKernelGGL((chunk_join_kernel<TIO, 64>), grid, dim3(256), 0, stream, a, p, ws, groups);
+}
+
+ChunkPlan plan_of(const tsv_attn_shape* s) {
+    ChunkPlan p;
+    p.rows = kRows;
+    p.want = 1024;
+    p.min_keys = 256;
+    p.split = (long long)s->max_pages * s->page_size > 2 * p.min_keys && s->n_kv_heads <= p.want;
+    return p;
+}
+
+}  // namespace
+
+uint64_t attn_prefill_workspace_bytes(const tsv_attn_shape* s) { return chunk_workspace_bytes(plan_of(s), s->n_kv_heads, s->head_dim); }
+
+long long attn_prefill_blocks(const tsv_attn_shape* s) {
+    const ChunkPlan p = plan_of(s);
+    const long long units = chunk_units(p, s->n_nodes, s->n_heads / s->n_kv_heads, s->batch, s->n_kv_heads) * s->n_kv_heads;
+    const long long join = (long long)p.want * groups_of(p.rows, s->head_dim);
+    return units > join ? units : join;
+}
+
+hipError_t launch_attn_prefill(const ChunkArgs& a, const tsv_attn_shape* s, void* workspace, hipStream_t stream) {
+    const ChunkPlan p = plan_of(s);
+    const ChunkWorkspace ws = chunk_workspace(workspace, p, a.Hk, a.D);
+    const long long units = chunk_units(p, a.T, a.H / a.Hk, a.batch, a.Hk) * a.Hk;
+    const dim3 grid((unsigned)(units > 0 ? units : 1));
+    const bool bf16 = s->in_dtype == TSV_BF16, e4m3 = s->cache_dtype == TSV_E4M3;
+    if (bf16 && e4m3)
+        launch_plain<uint16_t, uint8_t>(a, p, ws, grid, stream);
+    else if (bf16)
+        launch_plain<uint16_t, uint16_t>(a, p, ws, grid, stream);
+    else if (e4m3)
+        launch_plain<float, uint8_t>(a, p, ws, grid, stream);
+    else
+        launch_plain<float, float>(a, p, ws, grid, stream);
+    if (p.split && a.T > 0) {
+        if (bf16)
+            launch_join<uint16_t>(a, p, ws, stream);
+        else
+            launch_join<float>(a, p, ws, stream);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace tsv
