@@ -21,6 +21,7 @@ struct ChunkPlan {
     int want;      // work-groups wanted
     int min_keys;  // smallest part
     bool split;    // whether a block may have more than one part
+    bool sorted;   // the sequences' units by falling length (of at most 64 sequences)
 };
 
 // Upper bounds over all lengths. A cut block has parts of more than half of `keys`, and
@@ -33,17 +34,21 @@ inline long long chunk_slots(const ChunkPlan& p, int Hk) { return p.split ? 2LL 
 
 // Partial results of a part for one key head: the rows' unnormalised outputs, running
 // maxima (base 2) and sums
+// (and whether the sequence is left out)
 struct ChunkWorkspace {
     float* o;   // [slots][Hk][rows][D]
     float* ml;  // [slots][Hk][rows][2]
+    int* bad;   // [slots][Hk]
 };
 inline uint64_t chunk_workspace_bytes(const ChunkPlan& p, int Hk, int D) {
-    return (uint64_t)chunk_slots(p, Hk) * Hk * p.rows * (D + 2) * sizeof(float);
+    return (uint64_t)chunk_slots(p, Hk) * Hk * ((uint64_t)p.rows * (D + 2) + 1) * sizeof(float);
 }
 inline ChunkWorkspace chunk_workspace(void* ws, const ChunkPlan& p, int Hk, int D) {
     ChunkWorkspace w;
+    const size_t n = (size_t)chunk_slots(p, Hk) * Hk;
     w.o = (float*)ws;
-    w.ml = ws ? w.o + (size_t)chunk_slots(p, Hk) * Hk * p.rows * D : nullptr;
+    w.ml = ws ? w.o + n * p.rows * D : nullptr;
+    w.bad = ws ? (int*)(w.ml + n * p.rows * 2) : nullptr;
     return w;
 }
 
@@ -125,10 +130,18 @@ __device__ __forceinline__ ChunkUnit find_unit(const ChunkArgs& a, const ChunkPl
             }
         }
         const int at = want - run;
-        const unsigned long long who = __ballot(at >= upto - cnt && at < upto);
+        int from = upto - cnt;
+        if (!JOIN && plan.sorted) {
+            from = 0;
+            for (int j = 0; j < a.batch; ++j) {
+                const int other = __builtin_amdgcn_readlane(s.longest, j);
+                if (other > s.longest || (other == s.longest && j < lane)) from += __builtin_amdgcn_readlane(cnt, j);
+            }
+        }
+        const unsigned long long who = __ballot(at >= from && at < from + cnt);
         if (who) {
             const int src = __builtin_ctzll(who);
-            const int turn = at - __builtin_amdgcn_readlane(upto - cnt, src);
+            const int turn = at - __builtin_amdgcn_readlane(from, src);
             u.ok = 1;
             u.seq = q0 + src;
             u.start = __builtin_amdgcn_readlane(s.start, src);
@@ -182,6 +195,18 @@ __device__ __forceinline__ bool chunk_pages_bad(const ChunkArgs& a, const ChunkU
     return bad;
 }
 
+// The pages' check of a work-group, its status and its word for the join: whether to leave
+// the sequence out, the same in all threads. A barrier.
+template <int NT>
+__device__ __forceinline__ bool chunk_check(const ChunkArgs& a, const ChunkUnit& u, int hk, const ChunkWorkspace& ws) {
+    const int bad = __syncthreads_or(chunk_pages_bad<NT>(a, u));
+    if (threadIdx.x == 0) {
+        if (u.lead && hk == 0 && a.status) a.status[u.seq] = bad ? kStBadCache : 0;
+        if (u.parts > 1) ws.bad[(size_t)u.slot * a.Hk + hk] = bad;
+    }
+    return bad;
+}
+
 // Status of the sequences that have no unit (empty, or too long for their pages), and of
 // all where the packing is none: one wave of a launch
 __device__ __forceinline__ void chunk_status(const ChunkArgs& a, const ChunkPlan& plan, bool bad) {
@@ -194,5 +219,8 @@ __device__ __forceinline__ void chunk_status(const ChunkArgs& a, const ChunkPlan
             a.status[q] = s.fits ? 0 : kStBadCache;
     }
 }
+
+// bf16 MFMA kernels (attn_chunk_mfma.hip): plan.rows 128 or 256
+void launch_chunk_mfma(const ChunkArgs& a, bool e4m3, const ChunkPlan& p, const ChunkWorkspace& ws, dim3 grid, hipStream_t stream);
 
 }  // namespace tsv

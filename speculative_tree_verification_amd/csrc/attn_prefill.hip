@@ -35,9 +35,7 @@ __global__ __launch_bounds__(256) void chunk_plain_kernel(ChunkArgs a, ChunkPlan
     const ChunkUnit u = find_unit<false>(a, plan, blockIdx.x / a.Hk);
     if (blockIdx.x == 0 && w == 0) chunk_status(a, plan, u.bad);
     if (!u.ok) return;
-    const int bad = __syncthreads_or(chunk_pages_bad<256>(a, u));
-    if (u.lead && hk == 0 && tid == 0 && a.status) a.status[u.seq] = bad ? kStBadCache : 0;
-    if (bad) return;
+    if (chunk_check<256>(a, u, hk, ws)) return;
     const ChunkKeys kk = chunk_keys(a, plan, u);
     const int D = a.D, g = a.H / a.Hk, R = u.n * g, row0 = u.block * kRows;
     for (int i = tid; i < kRows * D; i += 256) {
@@ -166,62 +164,96 @@ __global__ __launch_bounds__(256) void chunk_plain_kernel(ChunkArgs a, ChunkPlan
     }
 }
 
-// Lanes take 4 elements of a row each, LPR lanes a row, which reads its block's parts four
-// at once.
+// Lanes take 4 elements of a row each, LPR lanes a row. A work-group has kJoinRows rows of a
+// block; where the block has fewer rows than the work-group groups of lanes, several groups
+// share a row's parts.
+constexpr int kJoinRows = 32;
+
 template <typename TIO, int LPR>
 __global__ __launch_bounds__(256) void chunk_join_kernel(ChunkArgs a, ChunkPlan plan, ChunkWorkspace ws, int groups) {
-    constexpr int kAt = 256 / LPR;
-    const int tid = threadIdx.x, group = blockIdx.x % groups, unit = blockIdx.x / groups, hk = unit % a.Hk;
+    constexpr int kAt = 256 / LPR, kLoads = 8;
+    __shared__ __attribute__((aligned(16))) float s_o[kAt][LPR * 4];
+    __shared__ float s_ml[kAt][2];
+    const int tid = threadIdx.x, unit = blockIdx.x / groups, hk = unit % a.Hk, grp = tid / LPR, d = tid % LPR * 4;
     const ChunkUnit u = find_unit<true>(a, plan, unit / a.Hk);
-    if (!u.ok) return;
-    const int D = a.D, g = a.H / a.Hk, R = u.n * g, r = group * kAt + tid / LPR, row = u.block * plan.rows + r;
-    if (__syncthreads_or(chunk_pages_bad<256>(a, u)) || r >= plan.rows || row >= R) return;
-    const int d = tid % LPR * 4;
+    if (!u.ok || ws.bad[(size_t)u.slot * a.Hk + hk]) return;
+    const int D = a.D, g = a.H / a.Hk, row0 = u.block * plan.rows, rows = min(u.n * g - row0, plan.rows);
+    int share = 1;  // groups of a row
+    while (2 * share * rows <= kAt) share *= 2;
+    const int first = blockIdx.x % groups * kJoinRows;
     const bool whole = D % 4 == 0 && (uintptr_t)a.o % (4 * sizeof(TIO)) == 0;  // pieces of four, aligned
     auto piece = [&](const float* p) { return d >= D ? make_float4(0.f, 0.f, 0.f, 0.f) : whole ? ld4<true>(p, 4) : ld4<false>(p, D - d); };
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < u.parts; k0 += 4) {
-        float mk[4], lk[4];
-        float4 v[4];
+    for (int r0 = first; r0 < min(rows, first + kJoinRows); r0 += kAt / share) {
+        const int r = min(r0 + grp / share, rows - 1);
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = grp % share; k0 < u.parts; k0 += kLoads * share) {
+            float mk[kLoads], lk[kLoads];
+            float4 v[kLoads];
+            float mn = m;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            mk[x] = -INFINITY;
-            lk[x] = 0.f;
-            v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k0 + x >= u.parts) continue;
-            const size_t at = ((size_t)(u.slot + k0 + x) * a.Hk + hk) * plan.rows + r;
-            mk[x] = ws.ml[at * 2];
-            lk[x] = ws.ml[at * 2 + 1];
-            v[x] = piece(ws.o + at * D + d);
+            for (int x = 0; x < kLoads; ++x) {
+                mk[x] = -INFINITY;
+                lk[x] = 0.f;
+                v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k0 + x * share >= u.parts) continue;
+                const size_t at = ((size_t)(u.slot + k0 + x * share) * a.Hk + hk) * plan.rows + r;
+                mk[x] = ws.ml[at * 2];
+                lk[x] = ws.ml[at * 2 + 1];
+                v[x] = piece(ws.o + at * D + d);
+            }
+#pragma unroll
+            for (int x = 0; x < kLoads; ++x) mn = fmaxf(mn, mk[x]);
+            const float base = mn == -INFINITY ? 0.f : mn, old = exp2f(m - base);
+            l *= old;
+            o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+#pragma unroll
+            for (int x = 0; x < kLoads; ++x) {
+                const float f = exp2f(mk[x] - base);
+                l = fmaf(f, lk[x], l);
+                o.x = fmaf(f, v[x].x, o.x);
+                o.y = fmaf(f, v[x].y, o.y);
+                o.z = fmaf(f, v[x].z, o.z);
+                o.w = fmaf(f, v[x].w, o.w);
+            }
+            m = mn;
         }
-        const float mn = fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), m);
-        const float base = mn == -INFINITY ? 0.f : mn, old = exp2f(m - base);
-        l *= old;
-        o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const float f = exp2f(mk[x] - base);
-            l = fmaf(f, lk[x], l);
-            o.x = fmaf(f, v[x].x, o.x);
-            o.y = fmaf(f, v[x].y, o.y);
-            o.z = fmaf(f, v[x].z, o.z);
-            o.w = fmaf(f, v[x].w, o.w);
+        if (share > 1) {  // (one turn of this loop)
+            *(float4*)&s_o[grp][d] = o;
+            if (d == 0) {
+                s_ml[grp][0] = m;
+                s_ml[grp][1] = l;
+            }
+            __syncthreads();
+            float mt = -INFINITY;
+            for (int x = 0; x < share; ++x) mt = fmaxf(mt, s_ml[grp / share * share + x][0]);
+            l = 0.f;
+            o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int x = 0; x < share; ++x) {
+                const int from = grp / share * share + x;
+                const float f = exp2f(s_ml[from][0] - (mt == -INFINITY ? 0.f : mt));
+                const float4 v = *(const float4*)&s_o[from][d];
+                l = fmaf(f, s_ml[from][1], l);
+                o.x = fmaf(f, v.x, o.x);
+                o.y = fmaf(f, v.y, o.y);
+                o.z = fmaf(f, v.z, o.z);
+                o.w = fmaf(f, v.w, o.w);
+            }
         }
-        m = mn;
-    }
-    if (d >= D) return;
-    TIO* to = (TIO*)a.o + (((size_t)u.start + row / g) * a.H + hk * g + row % g) * D + d;
-    const float f[4] = {o.x / l, o.y / l, o.z / l, o.w / l};
-    if (whole) {
-        if constexpr (sizeof(TIO) == 4)
-            *(float4*)to = make_float4(f[0], f[1], f[2], f[3]);
-        else
-            *(uint2*)to = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-    } else {
+        if (d >= D || grp % share || r0 + grp / share >= rows) continue;
+        const int row = row0 + r;
+        TIO* to = (TIO*)a.o + (((size_t)u.start + row / g) * a.H + hk * g + row % g) * D + d;
+        const float f[4] = {o.x / l, o.y / l, o.z / l, o.w / l};
+        if (whole) {
+            if constexpr (sizeof(TIO) == 4)
+                *(float4*)to = make_float4(f[0], f[1], f[2], f[3]);
+            else
+                *(uint2*)to = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (d + e < D) Elem<TIO>::st(to, e, f[e]);
+            for (int e = 0; e < 4; ++e)
+                if (d + e < D) Elem<TIO>::st(to, e, f[e]);
+        }
     }
 }
 
@@ -235,12 +267,11 @@ void launch_plain(const ChunkArgs& a, const ChunkPlan& p, const ChunkWorkspace& 
         hipLaunchKernelGGL((chunk_plain_kernel<TIO, TC, 4>), grid, dim3(256), 0, stream, a, p, ws);
 }
 
-constexpr int lanes_of(int D) { return D <= 64 ? 16 : D <= 128 ? 32 : 64; }
-int groups_of(int rows, int D) { return (rows + 256 / lanes_of(D) - 1) / (256 / lanes_of(D)); }
+int groups_of(int rows) { return (rows + kJoinRows - 1) / kJoinRows; }
 
 template <typename TIO>
 void launch_join(const ChunkArgs& a, const ChunkPlan& p, const ChunkWorkspace& ws, hipStream_t stream) {
-    const int groups = groups_of(p.rows, a.D);
+    const int groups = groups_of(p.rows);
     const dim3 grid((unsigned)((long long)(p.want / a.Hk) * a.Hk * groups));
     if (grid.x == 0) return;
     if (a.D <= 64)
@@ -251,33 +282,73 @@ void launch_join(const ChunkArgs& a, const ChunkPlan& p, const ChunkWorkspace& w
         hipLaunchKernelGGL((chunk_join_kernel<TIO, 64>), grid, dim3(256), 0, stream, a, p, ws, groups);
 }
 
-ChunkPlan plan_of(const tsv_attn_shape* s) {
+// Whether the matrix kernels take the shape: 32-bit row numbers into the pool, and
+// 16-byte rows of 64 or 128 elements (their alignment is looked at per call)
+bool matrix_shape(const tsv_attn_shape* s) {
+    return s->in_dtype == TSV_BF16 && (s->head_dim == 64 || s->head_dim == 128) && !(s->flags & TSV_FLAG_FORCE_GENERIC) &&
+           (long long)s->n_pages * s->n_kv_heads * s->page_size < (1LL << 32);
+}
+
+// Rows of a block: 16 (chunk_rows_kernel) where the sequences have no more on average, as
+// single tokens do, 128 (chunk_tiles_kernel), or 8 (plain). Work-groups wanted, for x of
+// them that would run without any cut:
+//   tiles  one round of two a compute unit (a chunk of 509 over 33258 positions: 316 us, 388
+//          for half as many, 339 for twice)
+//   rows   few parts while they fill one round, small ones where many items of different
+//          lengths share the GPU
+// Where a window bounds every block and blocks fill the GPU, none is long enough to be cut
+// (64 tokens, windows of 1021: 55 us, 65 with a second launch that finds nothing to join).
+ChunkPlan plan_of(const tsv_attn_shape* s, bool matrix, int window) {
     ChunkPlan p;
-    p.rows = kRows;
-    p.want = 1024;
+    const int g = s->n_heads / s->n_kv_heads;
+    const long long T = s->n_nodes, rows = T * g, items = s->batch < T ? s->batch : T, x = items * s->n_kv_heads;
+    p.rows = !matrix ? kRows : rows <= 16LL * s->batch ? 16 : 128;
+    p.want = !matrix ? 1024 : p.rows == 128 || x <= 128 ? 512 : x >= 512 ? 2048 : (int)(4 * x);
     p.min_keys = 256;
-    p.split = (long long)s->max_pages * s->page_size > 2 * p.min_keys && s->n_kv_heads <= p.want;
+    const long long blocks = rows / p.rows > items ? rows / p.rows : items;
+    p.split = (long long)s->max_pages * s->page_size > 2 * p.min_keys && s->n_kv_heads <= p.want &&
+              !(window > 0 && blocks * s->n_kv_heads >= 512);
+    // long work-groups should not start last (their order costs each a search of a microsecond)
+    p.sorted = p.rows == 128 && s->batch > 1 && s->batch <= kWave;
     return p;
 }
 
 }  // namespace
 
-uint64_t attn_prefill_workspace_bytes(const tsv_attn_shape* s) { return chunk_workspace_bytes(plan_of(s), s->n_kv_heads, s->head_dim); }
+// both kernels' needs, without a window: which of them runs depends on the pointers too, and
+// a window cuts no more
+uint64_t attn_prefill_workspace_bytes(const tsv_attn_shape* s) {
+    uint64_t most = 0;
+    for (int matrix = 0; matrix <= (int)matrix_shape(s); ++matrix) {
+        const uint64_t n = chunk_workspace_bytes(plan_of(s, matrix, 0), s->n_kv_heads, s->head_dim);
+        if (n > most) most = n;
+    }
+    return most;
+}
 
 long long attn_prefill_blocks(const tsv_attn_shape* s) {
-    const ChunkPlan p = plan_of(s);
-    const long long units = chunk_units(p, s->n_nodes, s->n_heads / s->n_kv_heads, s->batch, s->n_kv_heads) * s->n_kv_heads;
-    const long long join = (long long)p.want * groups_of(p.rows, s->head_dim);
-    return units > join ? units : join;
+    long long most = 0;
+    for (int matrix = 0; matrix <= (int)matrix_shape(s); ++matrix) {
+        const ChunkPlan p = plan_of(s, matrix, 0);
+        const long long units = chunk_units(p, s->n_nodes, s->n_heads / s->n_kv_heads, s->batch, s->n_kv_heads) * s->n_kv_heads;
+        const long long join = (long long)p.want * groups_of(p.rows);
+        if (units > most) most = units;
+        if (join > most) most = join;
+    }
+    return most;
 }
 
 hipError_t launch_attn_prefill(const ChunkArgs& a, const tsv_attn_shape* s, void* workspace, hipStream_t stream) {
-    const ChunkPlan p = plan_of(s);
+    const uintptr_t all = (uintptr_t)a.q | (uintptr_t)a.o | (uintptr_t)a.k_cache | (uintptr_t)a.v_cache;
+    const bool matrix = matrix_shape(s) && all % 16 == 0;
+    const ChunkPlan p = plan_of(s, matrix, a.window == 0x7fffffff ? 0 : a.window);
     const ChunkWorkspace ws = chunk_workspace(workspace, p, a.Hk, a.D);
     const long long units = chunk_units(p, a.T, a.H / a.Hk, a.batch, a.Hk) * a.Hk;
     const dim3 grid((unsigned)(units > 0 ? units : 1));
     const bool bf16 = s->in_dtype == TSV_BF16, e4m3 = s->cache_dtype == TSV_E4M3;
-    if (bf16 && e4m3)
+    if (matrix)
+        launch_chunk_mfma(a, e4m3, p, ws, grid, stream);
+    else if (bf16 && e4m3)
         launch_plain<uint16_t, uint8_t>(a, p, ws, grid, stream);
     else if (bf16)
         launch_plain<uint16_t, uint16_t>(a, p, ws, grid, stream);
