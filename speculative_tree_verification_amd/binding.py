@@ -1224,7 +1224,7 @@ def attn_prefill(q, seq_start, k_cache, v_cache, page_table, cache_len, k_scale=
     def body(s):
         out = torch.empty_like(q) if o is None else o
         ws, size = _workspace(_attn_prefill_workspace(*fields), workspace, at)
-        rc = lib.tree_attn_prefill(AttnShape(*fields), window, sinks, q.data_ptr(), seq_start.data_ptr(),
+        rc = lib.tree_attn_prefill(_attn_shape(*fields), window, sinks, q.data_ptr(), seq_start.data_ptr(),
                                    k_cache.data_ptr(), v_cache.data_ptr(), _opt(k_scale), _opt(v_scale),
                                    page_table.data_ptr(), cache_len.data_ptr(), out.data_ptr(), _opt(seq_status),
                                    _opt(ws), size, s)
@@ -1243,18 +1243,16 @@ def attn_prefill_workspace_bytes(batch, n_rows, n_heads, n_kv_heads, head_dim, p
                                    TSV_E4M3 if cache_dtype == torch.float8_e4m3fn else io, 0, 1.0)
 
 
-def _need_rows(t, name: str, rows, row, dtype, at: int) -> int:
-    """Checks rows [*rows][*row], each contiguous, that lie one after another at one distance, and returns that
-    distance in elements."""
-    if t.shape != (*rows, *row) or t.dtype is not dtype or t.get_device() != at:
-        _check(t, name, (*rows, *row), dtype, torch.device("cuda", at) if at >= 0 else torch.device("cpu"))
-    width, steps = 1, t.stride()
-    for size, step in zip(reversed(row), reversed(steps)):
+@functools.lru_cache(maxsize=4096)
+def _distance(shape, steps, lead: int, name: str) -> int:
+    """Elements between rows [*shape[lead:]], each contiguous, that lie one after another at one distance."""
+    width = 1
+    for size, step in zip(reversed(shape[lead:]), reversed(steps)):
         if size > 1 and step != width:
             raise ValueError(f"{name}: a row must be contiguous")
         width *= size
     apart, count = None, 1  # the distance, where there is more than one row; rows so far
-    for size, step in zip(reversed(rows), reversed(steps[:len(rows)])):
+    for size, step in zip(reversed(shape[:lead]), reversed(steps[:lead])):
         if size > 1:
             if apart is None:
                 apart = step
@@ -1264,16 +1262,30 @@ def _need_rows(t, name: str, rows, row, dtype, at: int) -> int:
     return width if apart is None else apart
 
 
-def _rope_fields(q, k, v, inv_freq, q_weight, k_weight, eps, interleaved, rows, heads, at, io):
-    """Checks what the rotation takes; rows: the tensors' leading sizes, heads: H, Hk, D."""
-    H, Hk, D = heads
-    strides = [0 if t is None else _need_rows(t, name, rows, (n, D), io, at)
-               for t, name, n in ((q, "q", H), (k, "k", Hk), (v, "v", Hk))]
-    _need(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float32, at)
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _need(t, name, (D,), torch.float32, at)
-    return Rope(2 * inv_freq.numel(), int(interleaved), eps, *strides)
+def _need_rows(t, name: str, rows, row, dtype, at: int) -> int:
+    """Checks rows [*rows][*row] and returns their distance (_distance)."""
+    if t.shape != rows + row or t.dtype is not dtype or t.get_device() != at:
+        _check(t, name, rows + row, dtype, torch.device("cuda", at) if at >= 0 else torch.device("cpu"))
+    return _distance(t.shape, t.stride(), len(rows), name)
+
+
+# the structures of a call, by their values: forming one costs a microsecond
+_attn_shape = functools.lru_cache(maxsize=4096)(lambda *fields: AttnShape(*fields))
+_rope_struct = functools.lru_cache(maxsize=4096)(lambda *fields: Rope(*fields))
+_conv_struct = functools.lru_cache(maxsize=4096)(lambda *fields: Conv(*fields))
+_seq_shape = functools.lru_cache(maxsize=4096)(lambda *fields: SeqShape(*fields))
+_tree_shape = functools.lru_cache(maxsize=4096)(lambda *fields: Shape(*fields))
+
+
+def _rope_weights(inv_freq, q_weight, k_weight, D, at):
+    """Checks what the rotation takes beside its rows: rot_dim."""
+    half = inv_freq.numel()
+    _need(inv_freq, "inv_freq", (half,), torch.float32, at)
+    if q_weight is not None:
+        _need(q_weight, "q_weight", (D,), torch.float32, at)
+    if k_weight is not None:
+        _need(k_weight, "k_weight", (D,), torch.float32, at)
+    return 2 * half
 
 
 def attn_rope(q, k, position, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
@@ -1288,23 +1300,28 @@ def attn_rope(q, k, position, inv_freq, q_weight=None, k_weight=None, eps: float
     if given is None:
         raise ValueError("q or k is needed")
     rows, D = tuple(given.shape[:-2]), given.shape[-1]
-    at, io = given.get_device(), given.dtype
-    H, Hk = (1 if t is None else t.shape[-2] for t in (q, k))
-    rope = _rope_fields(q, k, None, inv_freq, q_weight, k_weight, eps, interleaved, rows, (H, Hk, D), at, io)
+    at, io, H, Hk, q_step, k_step = given.get_device(), given.dtype, 0, 0, 0, 0
+    if q is not None:
+        H = q.shape[-2]
+        q_step = _need_rows(q, "q", rows, (H, D), io, at)
+    if k is not None:
+        Hk = k.shape[-2]
+        k_step = _need_rows(k, "k", rows, (Hk, D), io, at)
+    R = _rope_weights(inv_freq, q_weight, k_weight, D, at)
     _need(position, "position", rows, torch.int32, at)
-    for t, o, name, n in ((q, q_out, "q_out", H), (k, k_out, "k_out", Hk)):
+    for t, o, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
         if o is not None:
             if t is None:
                 raise ValueError(f"{name} is given without {name[0]}")
-            _need(o, name, (*rows, n, D), io, at)
-    n_rows = position.numel()
+            _need(o, name, t.shape, io, at)
+    code = _dtype_code(given)
+    rope = _rope_struct(R, 1 if interleaved else 0, eps, q_step, k_step, 0)
     # (one key head for the shape's H % Hk where there are none)
-    shape = AttnShape(1, n_rows, H if q is not None else Hk, Hk if k is not None else 1, D, 0, 1, 0, _dtype_code(given),
-                      _dtype_code(given), 0, 1.0)
+    shape = _attn_shape(1, position.numel(), H or Hk, Hk or 1, D, 0, 1, 0, code, code, 0, 1.0)
 
     def body(s):
-        qo, ko = (None if t is None else torch.empty(t.shape, dtype=io, device=t.device) if o is None else o
-                  for t, o in ((q, q_out), (k, k_out)))
+        qo = q_out if q is None or q_out is not None else q.new_empty(q.shape)
+        ko = k_out if k is None or k_out is not None else k.new_empty(k.shape)
         rc = lib.tree_attn_rope(shape, rope, _opt(q), _opt(k), position.data_ptr(), inv_freq.data_ptr(), _opt(q_weight),
                                 _opt(k_weight), _opt(qo), _opt(ko), s)
         if rc != 0:
@@ -1325,8 +1342,12 @@ def attn_append_rope(q, k, v, seq_start, inv_freq, k_cache, v_cache, page_table,
     were in a given ``q_out``, and undefined in one made here."""
     L, Hk, D = k.shape
     at, io, Bt = k.get_device(), k.dtype, cache_len.shape[0]
-    H = Hk if q is None else q.shape[-2]
-    rope = _rope_fields(q, k, v, inv_freq, q_weight, k_weight, eps, interleaved, (L,), (H, Hk, D), at, io)
+    H, q_step = Hk, 0
+    if q is not None:
+        H = q.shape[-2]
+        q_step = _need_rows(q, "q", (L,), (H, D), io, at)
+    rope = _rope_struct(_rope_weights(inv_freq, q_weight, k_weight, D, at), 1 if interleaved else 0, eps, q_step,
+                        _need_rows(k, "k", (L,), (Hk, D), io, at), _need_rows(v, "v", (L,), (Hk, D), io, at))
     _need(seq_start, "seq_start", (Bt + 1,), torch.int32, at)
     if seq_status is not None:
         _need(seq_status, "seq_status", (Bt,), torch.int32, at)
@@ -1337,8 +1358,8 @@ def attn_append_rope(q, k, v, seq_start, inv_freq, k_cache, v_cache, page_table,
     fields = _attn_fields(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, L, H, 1.0, False)
 
     def body(s):
-        qo = None if q is None else torch.empty((L, H, D), dtype=io, device=q.device) if q_out is None else q_out
-        rc = lib.tree_attn_append_rope(AttnShape(*fields), rope, _opt(q), k.data_ptr(), v.data_ptr(),
+        qo = q_out if q is None or q_out is not None else q.new_empty((L, H, D))
+        rc = lib.tree_attn_append_rope(_attn_shape(*fields), rope, _opt(q), k.data_ptr(), v.data_ptr(),
                                        seq_start.data_ptr(), inv_freq.data_ptr(), _opt(q_weight), _opt(k_weight),
                                        page_table.data_ptr(), cache_len.data_ptr(), _opt(qo), k_cache.data_ptr(),
                                        v_cache.data_ptr(), _opt(k_scale), _opt(v_scale), _opt(seq_status), s)
@@ -1350,17 +1371,18 @@ def attn_append_rope(q, k, v, seq_start, inv_freq, k_cache, v_cache, page_table,
 
 
 def _conv_fields(xbc, weight, bias, state, x, B, C, rows, n, at, io):
-    """Checks what the convolutions take: (H, P, N, G), tsv_conv's width and row stride."""
-    (H, P), (G, N) = x.shape[-2:], B.shape[-2:]
-    channels = H * P + 2 * G * N
-    back = state.shape[1]
+    """Checks what the convolutions take: (H, P, N, G, dtype code), and tsv_conv's width and row stride."""
+    H, P = x.shape[-2:]
+    G, N = B.shape[-2:]
+    channels, back = H * P + 2 * G * N, state.shape[1]
     _need(state, "state", (n, back, channels), io, at)
     _need(weight, "weight", (channels, back + 1), torch.float32, at)
     if bias is not None:
         _need(bias, "bias", (channels,), torch.float32, at)
-    for t, name, tail in ((x, "x", (H, P)), (B, "B", (G, N)), (C, "C", (G, N))):
-        _need(t, name, (*rows, *tail), io, at)
-    return (H, P, N, G), (back + 1, _need_rows(xbc, "xbc", rows, (channels,), io, at))
+    _need(x, "x", rows + (H, P), io, at)
+    _need(B, "B", rows + (G, N), io, at)
+    _need(C, "C", rows + (G, N), io, at)
+    return (H, P, N, G, _dtype_code(xbc)), (back + 1, _need_rows(xbc, "xbc", rows, (channels,), io, at))
 
 
 def conv_prefill(xbc, weight, bias, state, seq_start, x, B, C, silu: bool = True, seq_status=None, stream=None):
@@ -1370,14 +1392,14 @@ def conv_prefill(xbc, weight, bias, state, seq_start, x, B, C, silu: bool = True
     state [n,W-1,HP+2GN], the inputs before each sequence, becomes those at its
     end. seq_start [n+1] int32."""
     L, n, at, io = xbc.shape[0], state.shape[0], xbc.get_device(), xbc.dtype
-    (H, P, N, G), conv = _conv_fields(xbc, weight, bias, state, x, B, C, (L,), n, at, io)
+    dims, conv = _conv_fields(xbc, weight, bias, state, x, B, C, (L,), n, at, io)
     _need(seq_start, "seq_start", (n + 1,), torch.int32, at)
     if seq_status is not None:
         _need(seq_status, "seq_status", (n,), torch.int32, at)
-    shape = SeqShape(n, L, H, P, N, G, _dtype_code(xbc), 0)
+    shape, conv = _seq_shape(n, L, *dims, 0), _conv_struct(*conv, 1 if silu else 0)
 
     def body(s):
-        rc = lib.tree_ssd_conv_prefill(shape, Conv(*conv, int(silu)), xbc.data_ptr(), weight.data_ptr(), _opt(bias),
+        rc = lib.tree_ssd_conv_prefill(shape, conv, xbc.data_ptr(), weight.data_ptr(), _opt(bias),
                                        state.data_ptr(), seq_start.data_ptr(), x.data_ptr(), B.data_ptr(), C.data_ptr(),
                                        _opt(seq_status), s)
         if rc != 0:
@@ -1390,11 +1412,11 @@ def conv_step(xbc, weight, bias, state, x, B, C, silu: bool = True, stream=None)
     """``conv_prefill`` for one token of each item (tree_ssd_conv_step): xbc
     [Bt,HP+2GN], x [Bt,H,P], B, C [Bt,G,N]; state advanced in place."""
     Bt, at, io = xbc.shape[0], xbc.get_device(), xbc.dtype
-    (H, P, N, G), conv = _conv_fields(xbc, weight, bias, state, x, B, C, (Bt,), Bt, at, io)
-    shape = Shape(Bt, 1, H, P, N, G, _dtype_code(xbc), 0, 0)
+    dims, conv = _conv_fields(xbc, weight, bias, state, x, B, C, (Bt,), Bt, at, io)
+    shape, conv = _tree_shape(Bt, 1, *dims, 0, 0), _conv_struct(*conv, 1 if silu else 0)
 
     def body(s):
-        rc = lib.tree_ssd_conv_step(shape, Conv(*conv, int(silu)), xbc.data_ptr(), weight.data_ptr(), _opt(bias),
+        rc = lib.tree_ssd_conv_step(shape, conv, xbc.data_ptr(), weight.data_ptr(), _opt(bias),
                                     state.data_ptr(), x.data_ptr(), B.data_ptr(), C.data_ptr(), s)
         if rc != 0:
             raise TreeSSDError(rc, "tree_ssd_conv_step")
@@ -1408,14 +1430,14 @@ def conv_verify(xbc, weight, bias, state, parent, x, B, C, silu: bool = True, tr
     [Bt,T,HP+2GN], x [Bt,T,H,P], B, C [Bt,T,G,N]; the state is not changed."""
     Bt, T = xbc.shape[:2]
     at, io = xbc.get_device(), xbc.dtype
-    (H, P, N, G), conv = _conv_fields(xbc, weight, bias, state, x, B, C, (Bt, T), Bt, at, io)
+    dims, conv = _conv_fields(xbc, weight, bias, state, x, B, C, (Bt, T), Bt, at, io)
     _need(parent, "parent", (Bt, T), torch.int32, at)
     if tree_status is not None:
         _need(tree_status, "tree_status", (Bt,), torch.int32, at)
-    shape = Shape(Bt, T, H, P, N, G, _dtype_code(xbc), 0, 0)
+    shape, conv = _tree_shape(Bt, T, *dims, 0, 0), _conv_struct(*conv, 1 if silu else 0)
 
     def body(s):
-        rc = lib.tree_ssd_conv_verify(shape, Conv(*conv, int(silu)), xbc.data_ptr(), weight.data_ptr(), _opt(bias),
+        rc = lib.tree_ssd_conv_verify(shape, conv, xbc.data_ptr(), weight.data_ptr(), _opt(bias),
                                       state.data_ptr(), parent.data_ptr(), x.data_ptr(), B.data_ptr(), C.data_ptr(),
                                       _opt(tree_status), s)
         if rc != 0:
@@ -1437,8 +1459,8 @@ def conv_commit(xbc, state, parent, accepted, accepted_len, n_heads: int, head_d
     _need(accepted_len, "accepted_len", (Bt,), torch.int32, at)
     if tree_status is not None:
         _need(tree_status, "tree_status", (Bt,), torch.int32, at)
-    conv = Conv(back + 1, _need_rows(xbc, "xbc", (Bt, T), (channels,), io, at), 0)
-    shape = Shape(Bt, T, n_heads, head_dim, d_state, n_groups, _dtype_code(xbc), 0, 0)
+    conv = _conv_struct(back + 1, _need_rows(xbc, "xbc", (Bt, T), (channels,), io, at), 0)
+    shape = _tree_shape(Bt, T, n_heads, head_dim, d_state, n_groups, _dtype_code(xbc), 0, 0)
 
     def body(s):
         rc = lib.tree_ssd_conv_commit(shape, conv, xbc.data_ptr(), state.data_ptr(), parent.data_ptr(),
