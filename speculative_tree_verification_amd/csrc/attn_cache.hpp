@@ -197,7 +197,7 @@ __device__ __forceinline__ uint32_t max_of(uint32_t v) {
 template <int ROWS>
 struct RowPlaces {
     long long dst[ROWS];
-    int item[ROWS], pos[ROWS], place[ROWS], bad[ROWS], is_long[ROWS], first, red[4];
+    int item[ROWS], pos[ROWS], len[ROWS], count[ROWS], place[ROWS], bad[ROWS], is_long[ROWS], red[4];
 };
 
 // False: nothing to write for this work-group. With status_of >= 0 it writes the status of
@@ -206,15 +206,23 @@ struct RowPlaces {
 template <int ROWS>
 __device__ __forceinline__ bool find_places(const CacheWriteArgs& a, int r0, int n, int status_of, RowPlaces<ROWS>& s) {
     const int tid = threadIdx.x;
-    if (tid == 0) s.first = 0;
-    lds_barrier();
-    int bad = 0, before = 0;
-    for (int q = tid; q < a.batch; q += 256) {
-        const int lo = a.seq_start[q], hi = a.seq_start[q + 1];
-        bad |= lo < 0 || hi < lo || hi > a.T;
-        before += hi <= r0;
+    if (tid < ROWS) {
+        s.pos[tid] = -1;
+        s.item[tid] = s.bad[tid] = s.is_long[tid] = 0;
     }
-    if (before) atomicAdd(&s.first, before);
+    lds_barrier();
+    // the thread of a sequence that has rows here writes what the rows need of it
+    int bad = 0;
+    for (int q = tid; q < a.batch; q += 256) {
+        const int lo = a.seq_start[q], hi = a.seq_start[q + 1], len = a.cache_len[q];
+        bad |= lo < 0 || hi < lo || hi > a.T;
+        for (int r = max(lo, r0); r < min(hi, r0 + n); ++r) {
+            s.item[r - r0] = q;
+            s.pos[r - r0] = r - lo;
+            s.len[r - r0] = len;
+            s.count[r - r0] = hi - lo;
+        }
+    }
     bad = lds_sync_or<256>(bad, s.red);
     if (status_of >= 0) {
         const int b = status_of;
@@ -223,16 +231,13 @@ __device__ __forceinline__ bool find_places(const CacheWriteArgs& a, int r0, int
         return false;
     }
     if (bad) return false;
-    if (tid < ROWS) {
-        int b = s.first, pos = -1;
-        const int r = r0 + tid;
-        while (b < a.batch && a.seq_start[b + 1] <= r) ++b;
-        if (tid < n && b < a.batch && r >= a.seq_start[b]) pos = r - a.seq_start[b];  // in its sequence
-        s.item[tid] = b < a.batch ? b : 0;
-        s.pos[tid] = pos;
+    // a row's page, where its sequence fits the table
+    int page = 0, place = -1, pg = 0, first, last;
+    if (tid < n && s.pos[tid] >= 0 && page_range(a, s.len[tid], s.count[tid], &first, &last)) {
+        place = s.len[tid] + s.pos[tid];
+        page = page_of(place, a.div);
+        pg = a.page_table[(size_t)s.item[tid] * a.max_pages + page];
     }
-    if (tid < ROWS) s.bad[tid] = s.is_long[tid] = 0;
-    lds_barrier();
     // the sequences that begin or go on in these rows: 16 threads each, all at once
     // (16 short prompts one after another took 30 us), and then all threads for
     // each of the few that have many pages
@@ -241,10 +246,7 @@ __device__ __forceinline__ bool find_places(const CacheWriteArgs& a, int r0, int
         const int i = tid / (256 / ROWS), b = s.item[i];
         const bool leads = i < n && s.pos[i] >= 0 && (i == 0 || s.pos[i - 1] < 0 || s.item[i - 1] != b);
         if (leads) {
-            const int len = a.cache_len[b];
-            int first, last;
-            const bool fits = page_range(a, len, a.seq_start[b + 1] - a.seq_start[b], &first, &last);
-            if (!fits)
+            if (!page_range(a, s.len[i], s.count[i], &first, &last))
                 s.bad[i] = 1;
             else if (last - first >= kLong)
                 s.is_long[i] = 1;
@@ -254,19 +256,18 @@ __device__ __forceinline__ bool find_places(const CacheWriteArgs& a, int r0, int
         lds_barrier();
         for (int j = 0; j < n; ++j) {
             if (!s.is_long[j]) continue;
-            const int st = check_pages(a, s.item[j], a.seq_start[s.item[j] + 1] - a.seq_start[s.item[j]]);
+            const int st = check_pages(a, s.item[j], s.count[j]);
             if (tid == 0 && st) s.bad[j] = 1;
             __syncthreads();
         }
     }
-    if (tid < n && s.pos[tid] >= 0) {
+    if (tid < n) {
         int j = tid;  // the first of this sequence's rows here
-        while (j > 0 && s.item[j - 1] == s.item[tid] && s.pos[j - 1] >= 0) --j;
-        s.place[tid] = s.bad[j] ? -1 : s.pos[tid] + a.cache_len[s.item[tid]];
-    } else if (tid < n) {
-        s.place[tid] = -1;
+        while (j > 0 && s.pos[j] >= 0 && s.item[j - 1] == s.item[tid] && s.pos[j - 1] >= 0) --j;
+        if (s.bad[j]) place = -1;
+        s.place[tid] = place;
+        s.dst[tid] = place >= 0 ? (long long)pg * a.Hk * a.page_size + (place - page * a.page_size) : -1;
     }
-    if (tid < n) s.dst[tid] = s.place[tid] >= 0 ? cache_place(a, s.item[tid], s.place[tid]) : -1;
     lds_barrier();
     return true;
 }

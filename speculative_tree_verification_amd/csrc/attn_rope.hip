@@ -18,7 +18,7 @@
 namespace tsv {
 namespace {
 
-constexpr int kRopeRows = 4;  // most rows of a work-group
+constexpr int kRopeRows = 16;  // most rows of a work-group
 
 // Element numbers of pair p
 __device__ __forceinline__ int2 pair_of(const RopeArgs& a, int p) {
@@ -36,16 +36,19 @@ struct Piece {
     Raw<TIO, VEC> lo, hi;
 };
 
-__device__ __forceinline__ bool apart(const RopeArgs& a, int j) { return !a.interleaved && 16 * j < a.R; }
+// First elements of the two pieces: the pairs' first and second ones, or (interleaved pairs,
+// and elements that are not rotated) sixteen neighbours
+__device__ __forceinline__ int2 pieces_of(const RopeArgs& a, int j) {
+    return !a.interleaved && 16 * j < a.R ? make_int2(8 * j, a.R / 2 + 8 * j) : make_int2(16 * j, 16 * j + 8);
+}
 
 template <typename TIO, int LPH, bool VEC>
-__device__ __forceinline__ Piece<TIO, LPH, VEC> load_pairs(const RopeArgs& a, const TIO* row, int j) {
+__device__ __forceinline__ Piece<TIO, LPH, VEC> load_pairs(const RopeArgs& a, const TIO* row, int j, int2 at) {
     Piece<TIO, LPH, VEC> p{};
     if constexpr (VEC) {
         if (16 * j >= a.D) return p;
-        const bool ap = apart(a, j);
-        p.lo = load8<TIO, true>(row + (ap ? 8 * j : 16 * j), 8);
-        p.hi = load8<TIO, true>(row + (ap ? a.R / 2 + 8 * j : 16 * j + 8), 8);
+        p.lo = load8<TIO, true>(row + at.x, 8);
+        p.hi = load8<TIO, true>(row + at.y, 8);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -57,40 +60,59 @@ __device__ __forceinline__ Piece<TIO, LPH, VEC> load_pairs(const RopeArgs& a, co
     return p;
 }
 
-// Pieces in the elements' order <-> pairs (both ways the same lanes)
+// Pieces in the elements' order <-> pairs. Only interleaved pairs are not in their places
+// (elements that are not rotated may pair in any way)
 template <bool VEC>
-__device__ __forceinline__ Pairs to_pairs(const RopeArgs& a, const Quad& lo, const Quad& hi, int j) {
+__device__ __forceinline__ Pairs to_pairs(const RopeArgs& a, const Quad& lo, const Quad& hi) {
     Pairs p;
-    const bool as_is = !VEC || apart(a, j);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float x = i < 4 ? lo.v[2 * i] : hi.v[2 * i - 8], y = i < 4 ? lo.v[2 * i + 1] : hi.v[2 * i - 7];
-        p.a[i] = as_is ? lo.v[i] : x;
-        p.b[i] = as_is ? hi.v[i] : y;
+        p.a[i] = lo.v[i];
+        p.b[i] = hi.v[i];
+    }
+    if (VEC && a.interleaved) {
+        asm volatile("");  // (or the compiler selects, for both kinds)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            p.a[i] = i < 4 ? lo.v[2 * i] : hi.v[2 * i - 8];
+            p.b[i] = i < 4 ? lo.v[2 * i + 1] : hi.v[2 * i - 7];
+        }
     }
     return p;
 }
 template <bool VEC>
-__device__ __forceinline__ void to_pieces(const RopeArgs& a, const Pairs& p, int j, Quad& lo, Quad& hi) {
-    const bool as_is = !VEC || apart(a, j);
+__device__ __forceinline__ void to_pieces(const RopeArgs& a, const Pairs& p, Quad& lo, Quad& hi) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float x = i % 2 ? p.b[i / 2] : p.a[i / 2], y = i % 2 ? p.b[4 + i / 2] : p.a[4 + i / 2];
-        lo.v[i] = as_is ? p.a[i] : x;
-        hi.v[i] = as_is ? p.b[i] : y;
+        lo.v[i] = p.a[i];
+        hi.v[i] = p.b[i];
+    }
+    if (VEC && a.interleaved) {
+        asm volatile("");
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            lo.v[i] = i % 2 ? p.b[i / 2] : p.a[i / 2];
+            hi.v[i] = i % 2 ? p.b[4 + i / 2] : p.a[4 + i / 2];
+        }
     }
 }
 
 template <int LPH, bool VEC>
-__device__ __forceinline__ Pairs load_weight(const RopeArgs& a, const float* w, int j) {
-    Pairs p;
+__device__ __forceinline__ Pairs load_weight(const RopeArgs& a, const float* w, int j, int2 at) {
+    if (!w) return Pairs{};
+    if constexpr (VEC) {
+        if (16 * j >= a.D) return Pairs{};
+        return to_pairs<true>(a, floats<float, true>(load8<float, true>(w + at.x, 8)), floats<float, true>(load8<float, true>(w + at.y, 8)));
+    } else {
+        Pairs p;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int2 e = pair_of(a, VEC ? 8 * j + i : j + LPH * i);
-        p.a[i] = w && e.x < a.D ? gload(w + e.x) : 0.f;
-        p.b[i] = w && e.y < a.D ? gload(w + e.y) : 0.f;
+        for (int i = 0; i < 8; ++i) {
+            const int2 e = pair_of(a, j + LPH * i);
+            p.a[i] = e.x < a.D ? gload(w + e.x) : 0.f;
+            p.b[i] = e.y < a.D ? gload(w + e.y) : 0.f;
+        }
+        return p;
     }
-    return p;
 }
 
 // Sum over the LPH <= 16 neighbouring lanes of a head
@@ -105,8 +127,8 @@ __device__ __forceinline__ float head_sum(float v) {
     return v;
 }
 
-// 8 values at their places, rounded to nearest even (VEC: one piece of neighbours)
-template <typename TIO, bool VEC>
+// 8 neighbours, rounded to nearest even
+template <typename TIO>
 __device__ __forceinline__ void store_piece(TIO* to, const Quad& q) {
     if constexpr (sizeof(TIO) == 2) {
         gstore((uint4*)to, make_uint4(pack_bf16x2(q.v[0], q.v[1]), pack_bf16x2(q.v[2], q.v[3]), pack_bf16x2(q.v[4], q.v[5]),
@@ -117,12 +139,11 @@ __device__ __forceinline__ void store_piece(TIO* to, const Quad& q) {
     }
 }
 template <typename TIO, int LPH, bool VEC>
-__device__ __forceinline__ void store_head(const RopeArgs& a, TIO* row, const Quad& lo, const Quad& hi, int j) {
+__device__ __forceinline__ void store_head(const RopeArgs& a, TIO* row, const Quad& lo, const Quad& hi, int j, int2 to) {
     if constexpr (VEC) {
         if (16 * j >= a.D) return;
-        const bool ap = apart(a, j);
-        store_piece<TIO, true>(row + (ap ? 8 * j : 16 * j), lo);
-        store_piece<TIO, true>(row + (ap ? a.R / 2 + 8 * j : 16 * j + 8), hi);
+        store_piece<TIO>(row + to.x, lo);
+        store_piece<TIO>(row + to.y, hi);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -133,14 +154,13 @@ __device__ __forceinline__ void store_head(const RopeArgs& a, TIO* row, const Qu
     }
 }
 template <int LPH, bool VEC>
-__device__ __forceinline__ void store_head_e4m3(const RopeArgs& a, uint8_t* row, const Quad& lo, const Quad& hi, int j, float scale) {
+__device__ __forceinline__ void store_head_e4m3(const RopeArgs& a, uint8_t* row, const Quad& lo, const Quad& hi, int j, int2 to, float scale) {
     const bool finite = scale == scale;
     const uint2 ul = e4m3_bytes(lo, scale, finite), uh = e4m3_bytes(hi, scale, finite);
     if constexpr (VEC) {
         if (16 * j >= a.D) return;
-        const bool ap = apart(a, j);
-        gstore((uint2*)(row + (ap ? 8 * j : 16 * j)), ul);
-        gstore((uint2*)(row + (ap ? a.R / 2 + 8 * j : 16 * j + 8)), uh);
+        gstore((uint2*)(row + to.x), ul);
+        gstore((uint2*)(row + to.y), uh);
     } else {
         const uint32_t wl[2] = {ul.x, ul.y}, wh[2] = {uh.x, uh.y};
 #pragma unroll
@@ -160,6 +180,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, CacheWriteArgs c,
     __shared__ RowPlaces<kRopeRows> places;
     constexpr int kSlots = 256 / LPH;
     const int tid = threadIdx.x, j = tid % LPH;
+    const int2 at = pieces_of(a, j);
     const bool rows = (int)blockIdx.x < row_blocks;
     const int r0 = blockIdx.x * rb, n = rows ? min(rb, a.rows - r0) : 0;
     const int Hq = a.q ? a.H : 0, Hx = a.k ? a.Hk : 0, heads = Hq + (APPEND ? 2 : 1) * Hx, units = n * heads;
@@ -167,17 +188,17 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, CacheWriteArgs c,
     auto fetch = [&](int u) {
         P p{};
         if (u >= units) return p;
-        const int row = u / heads, h = u - row * heads;
+        const int row = page_of(u, a.heads), h = u - row * heads;
         const size_t r = (size_t)(r0 + row);
         const TIO* from = h < Hq ? (const TIO*)a.q + r * a.qs + (size_t)h * a.D
                                  : h < Hq + Hx ? (const TIO*)a.k + r * a.ks + (size_t)(h - Hq) * a.D
                                                : (const TIO*)a.v + r * a.vs + (size_t)(h - Hq - Hx) * a.D;
-        return load_pairs<TIO, LPH, VEC>(a, from, j);
+        return load_pairs<TIO, LPH, VEC>(a, from, j, at);
     };
     // the first rows are on their way while their places and angles are found
     int u = tid / LPH;
     P next = fetch(u);
-    const Pairs wq = load_weight<LPH, VEC>(a, a.qw, j), wk = load_weight<LPH, VEC>(a, a.kw, j);
+    const Pairs wq = load_weight<LPH, VEC>(a, a.qw, j, at), wk = load_weight<LPH, VEC>(a, a.kw, j, at);
     if (APPEND) {
         if (!find_places<kRopeRows>(c, r0, n, rows ? -1 : (int)blockIdx.x - row_blocks, places)) return;
     } else {
@@ -197,13 +218,13 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, CacheWriteArgs c,
     for (; u < units; u += kSlots) {
         const P now = next;
         next = fetch(u + kSlots);
-        const int row = u / heads, h = u - row * heads;
+        const int row = page_of(u, a.heads), h = u - row * heads;
         const int place = places.place[row];
         if (place < 0) continue;  // a row of no sequence, or left out by its position (the same for a head's lanes)
         const bool is_q = h < Hq, is_v = APPEND && h >= Hq + Hx;
         Quad lo = floats<TIO, VEC>(now.lo), hi = floats<TIO, VEC>(now.hi);
         if (!is_v) {
-            Pairs x = to_pairs<VEC>(a, lo, hi, j);
+            Pairs x = to_pairs<VEC>(a, lo, hi);
             if (is_q ? a.qw != nullptr : a.kw != nullptr) {
                 float sum = 0.f;
 #pragma unroll
@@ -225,25 +246,25 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, CacheWriteArgs c,
                     x.b[i] = fmaf(x.b[i], cs, xa * sn);
                 }
             }
-            to_pieces<VEC>(a, x, j, lo, hi);
+            to_pieces<VEC>(a, x, lo, hi);
         }
         if (is_q) {
-            store_head<TIO, LPH, VEC>(a, (TIO*)a.q_out + ((size_t)(r0 + row) * a.H + h) * a.D, lo, hi, j);
+            store_head<TIO, LPH, VEC>(a, (TIO*)a.q_out + ((size_t)(r0 + row) * a.H + h) * a.D, lo, hi, j, at);
         } else if (!APPEND) {
-            store_head<TIO, LPH, VEC>(a, (TIO*)a.k_out + ((size_t)(r0 + row) * a.Hk + (h - Hq)) * a.D, lo, hi, j);
+            store_head<TIO, LPH, VEC>(a, (TIO*)a.k_out + ((size_t)(r0 + row) * a.Hk + (h - Hq)) * a.D, lo, hi, j, at);
         } else {
             const int hk = is_v ? h - Hq - Hx : h - Hq;
-            const size_t at = (size_t)(places.dst[row] + (long long)hk * c.page_size);
+            const size_t dst = (size_t)(places.dst[row] + (long long)hk * c.page_size);
             if (E4M3) {
                 uint32_t top = 0;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     top = max(top, max(__float_as_uint(lo.v[i]) & 0x7fffffffu, __float_as_uint(hi.v[i]) & 0x7fffffffu));
                 const float scale = scale_of(max_of<LPH>(top));
-                store_head_e4m3<LPH, VEC>(a, (uint8_t*)(is_v ? c.v_cache : c.k_cache) + at * a.D, lo, hi, j, scale);
-                if (j == 0) (is_v ? c.v_scale : c.k_scale)[at] = scale;
+                store_head_e4m3<LPH, VEC>(a, (uint8_t*)(is_v ? c.v_cache : c.k_cache) + dst * a.D, lo, hi, j, at, scale);
+                if (j == 0) (is_v ? c.v_scale : c.k_scale)[dst] = scale;
             } else {
-                store_head<TIO, LPH, VEC>(a, (TIO*)(is_v ? c.v_cache : c.k_cache) + at * a.D, lo, hi, j);
+                store_head<TIO, LPH, VEC>(a, (TIO*)(is_v ? c.v_cache : c.k_cache) + dst * a.D, lo, hi, j, at);
             }
         }
     }
@@ -265,7 +286,7 @@ hipError_t launch_type(const RopeArgs& a, const CacheWriteArgs* c, bool e4m3, hi
     if (all == 0) return hipSuccess;
     // eight elements at a time where heads, strides and pointers allow it
     uintptr_t bits = (uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.q_out | (uintptr_t)a.k_out;
-    bits |= (uintptr_t)((a.qs | a.ks | a.vs) * sizeof(TIO));
+    bits |= (uintptr_t)((a.qs | a.ks | a.vs) * sizeof(TIO)) | (uintptr_t)a.qw | (uintptr_t)a.kw;
     if (c) bits |= (uintptr_t)c->k_cache | (uintptr_t)c->v_cache;
     const bool vec = a.D % 16 == 0 && a.R % 16 == 0 && bits % 16 == 0;
     if (!vec)
@@ -281,7 +302,7 @@ hipError_t launch_type(const RopeArgs& a, const CacheWriteArgs* c, bool e4m3, hi
 
 }  // namespace
 
-int rope_rows(int rows) { return rows <= 1024 ? 1 : kRopeRows; }
+int rope_rows(int rows) { return rows <= 1024 ? 1 : rows <= 8192 ? 4 : kRopeRows; }
 long long rope_blocks(int rows, int items) { return ((long long)rows + rope_rows(rows) - 1) / rope_rows(rows) + items; }
 
 hipError_t launch_rope(const RopeArgs& a, const CacheWriteArgs* c, bool bf16, bool e4m3, hipStream_t stream) {

@@ -6,6 +6,11 @@
 
 namespace tsv {
 
+struct PageDiv {  // n / page_size by a product (attn_common.hpp)
+    uint32_t mul;
+    int shift;
+};
+
 // ---- sequences around the tree
 struct StepArgs {
     const void* x;
@@ -41,10 +46,6 @@ long long prefill_blocks(const tsv_seq_shape* s, bool states_vec);
 hipError_t launch_prefill(const PrefillArgs& a, const tsv_seq_shape* s, int32_t* status, void* workspace, hipStream_t stream);
 
 // ---- the paged cache of attention layers
-struct PageDiv {  // n / page_size by a product (attn_common.hpp)
-    uint32_t mul;
-    int shift;
-};
 struct CacheWriteArgs {
     const void* k;
     const void* v;
@@ -81,6 +82,7 @@ struct RopeArgs {
     long long qs, ks, vs;  // elements between rows
     int rows, H, Hk, D, R, interleaved;
     float eps;
+    PageDiv heads;  // by a row's heads, of q, k and (into the cache) v
 };
 int rope_rows(int rows);                        // rows of a work-group
 long long rope_blocks(int rows, int items);     // work-groups, with the items' status
