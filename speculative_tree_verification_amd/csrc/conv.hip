@@ -74,6 +74,24 @@ __device__ __forceinline__ Chan<TIO, false> rounded_one(float v) {
         return {v};
 }
 
+// N floats (VEC: a multiple of 4, 16-byte aligned)
+template <int N, bool VEC>
+__device__ __forceinline__ void load_floats(const float* p, float (&v)[N]) {
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 u = gload((const float4*)(p + i));
+            v[i] = u.x;
+            v[i + 1] = u.y;
+            v[i + 2] = u.z;
+            v[i + 3] = u.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = gload(p + i);
+    }
+}
+
 // A lane's channels: which, their taps and bias, and where their outputs go
 template <typename TIO, int W, bool VEC>
 struct Lane {
@@ -95,12 +113,15 @@ struct Lane {
         width = in_B < 0 ? a.HP : a.GN;
     }
     __device__ __forceinline__ void taps(const ConvArgs& a) {
+        float v[N * W];
+        load_floats<N * W, VEC>(a.weight + (size_t)c * W, v);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
 #pragma unroll
-            for (int k = 0; k < W; ++k) w[k][i] = gload(a.weight + (size_t)(c + i) * W + k);
-            bias[i] = a.bias ? gload(a.bias + c + i) : 0.f;
+            for (int k = 0; k < W; ++k) w[k][i] = v[i * W + k];
+            bias[i] = 0.f;
         }
+        if (a.bias) load_floats<N, VEC>(a.bias + c, bias);
     }
     // u[0], ..., u[W - 1]: the inputs, oldest first
     __device__ __forceinline__ Ch output(const ConvArgs& a, const Ch* const (&u)[W]) const {
@@ -183,7 +204,7 @@ __global__ __launch_bounds__(256) void conv_prefill_kernel(ConvArgs a, int strip
     const int C = a.HP + 2 * a.GN, t1 = min(len, t0 + strip);
     const size_t state = (size_t)seq * (W - 1) * C + l.c;
     auto row = [&](int t) { return get<TIO, VEC>(a.xbc, (size_t)(first + t) * a.stride + l.c); };
-    constexpr int S = 8;  // rows on their way at once
+    constexpr int S = 4;  // rows on their way at once
     Ch u[W - 1 + S];
 #pragma unroll
     for (int m = 0; m < W - 1; ++m) {
@@ -258,11 +279,13 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int chunks) 
     for (int m = 0; m < W - 1; ++m) put<TIO, VEC>(a.state, state + (size_t)m * C, u[m + 1]);
 }
 
-// Status bits of a tree: the same in all lanes of the wave
-__device__ __forceinline__ int check_parents(const int32_t* parent, int T) {
+// Status bits of a tree: the same in all lanes of the wave. *mine: the parent of node `lane`
+__device__ __forceinline__ int check_parents(const int32_t* parent, int T, int* mine) {
     int bits = 0;
+    *mine = 0;
     for (int i = threadIdx.x & (kWave - 1); i < T; i += kWave) {
         const int p = parent[i];
+        if (i < kWave) *mine = p;
         bits |= i == 0 ? (p != -1 ? kStBadRoot : 0) : (p < 0 || p >= i ? kStBadParent : 0);
     }
     return (__ballot(bits & kStBadRoot) ? kStBadRoot : 0) | (__ballot(bits & kStBadParent) ? kStBadParent : 0);
@@ -279,18 +302,21 @@ __global__ __launch_bounds__(256) void conv_verify_kernel(ConvArgs a, int nodes,
     const int chunk = (int)(unit % chunks), strip = (int)(unit / chunks % strips), b = (int)(unit / chunks / strips);
     if (b >= a.n) return;
     const int32_t* parent = a.parent + (size_t)b * T;
-    const int st = check_parents(parent, T);
-    if (chunk == 0 && strip == 0 && lane == 0 && a.status) a.status[b] = st;
-    if (st) return;
     L l;
     l.init(a, chunk);
     l.taps(a);
+    int par;
+    const int st = check_parents(parent, T, &par);
+    if (chunk == 0 && strip == 0 && lane == 0 && a.status) a.status[b] = st;
+    if (st) return;
     // lane i: the ancestors of node first + i: a node, or -m for the m-th state row from the last one on
     const int first = strip * nodes, n = min(nodes, T - first);
     int up[W - 1], j = first + min(lane, n - 1);
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
-        j = j > 0 ? parent[j] : j - 1;  // (the root's parent is -1: past it the count goes on)
+        // (the root's parent is -1: past it the count goes on)
+        const int p = T <= kWave ? __shfl(par, max(j, 0), kWave) : j > 0 ? parent[j] : -1;
+        j = j > 0 ? p : j - 1;
         up[k] = j;
     }
     const int C = a.HP + 2 * a.GN;
@@ -331,7 +357,7 @@ __global__ __launch_bounds__(256) void conv_commit_kernel(ConvArgs a, int chunks
     if (b >= a.n) return;
     const int32_t* parent = a.parent + (size_t)b * T;
     const int32_t* acc = a.accepted + (size_t)b * a.Lmax;
-    int st = check_parents(parent, T);
+    int par, st = check_parents(parent, T, &par);
     const int len = a.accepted_len[b];
     int bad = len < 0 || len > a.Lmax || len > T;
     for (int i = lane; !bad && i < len; i += kWave) {
@@ -392,7 +418,8 @@ template <typename TIO, int W>
 hipError_t launch_width(ConvKind kind, const ConvArgs& a, hipStream_t stream) {
     // 16 bytes of channels a lane where the outputs' borders, strides and pointers allow it
     constexpr int N = 16 / sizeof(TIO);
-    const uintptr_t all = (uintptr_t)a.xbc | (uintptr_t)a.state | (uintptr_t)a.x | (uintptr_t)a.B | (uintptr_t)a.C;
+    const uintptr_t all = (uintptr_t)a.xbc | (uintptr_t)a.state | (uintptr_t)a.x | (uintptr_t)a.B | (uintptr_t)a.C |
+                          (uintptr_t)a.weight | (uintptr_t)a.bias;
     if (all % 16 == 0 && a.HP % N == 0 && a.GN % N == 0 && a.stride % N == 0)
         launch_one<TIO, W, true>(kind, a, stream);
     else
