@@ -220,7 +220,10 @@ __device__ __forceinline__ void chunk_status(const ChunkArgs& a, const ChunkPlan
     }
 }
 
-// bf16 MFMA kernels (attn_chunk_mfma.hip): plan.rows 128 or 256
+// bf16 MFMA kernels (attn_chunk_mfma.hip): plan.rows 16 or 128
 void launch_chunk_mfma(const ChunkArgs& a, bool e4m3, const ChunkPlan& p, const ChunkWorkspace& ws, dim3 grid, hipStream_t stream);
+
+// fp32 MFMA kernels (attn_chunk_f32.hip): plan.rows 16 or 64
+void launch_chunk_f32(const ChunkArgs& a, bool e4m3, const ChunkPlan& p, const ChunkWorkspace& ws, dim3 grid, hipStream_t stream);
 
 }  // namespace tsv

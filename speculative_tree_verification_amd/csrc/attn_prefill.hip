@@ -285,7 +285,7 @@ void launch_join(const ChunkArgs& a, const ChunkPlan& p, const ChunkWorkspace& w
 // Whether the matrix kernels take the shape: 32-bit row numbers into the pool, and
 // 16-byte rows of 64 or 128 elements (their alignment is looked at per call)
 bool matrix_shape(const tsv_attn_shape* s) {
-    return s->in_dtype == TSV_BF16 && (s->head_dim == 64 || s->head_dim == 128) && !(s->flags & TSV_FLAG_FORCE_GENERIC) &&
+    return (s->head_dim == 64 || s->head_dim == 128) && !(s->flags & TSV_FLAG_FORCE_GENERIC) &&
            (long long)s->n_pages * s->n_kv_heads * s->page_size < (1LL << 32);
 }
 
@@ -296,20 +296,22 @@ bool matrix_shape(const tsv_attn_shape* s) {
 //          for half as many, 339 for twice)
 //   rows   few parts while they fill one round, small ones where many items of different
 //          lengths share the GPU
-// Where a window bounds every block and blocks fill the GPU, none is long enough to be cut
-// (64 tokens, windows of 1021: 55 us, 65 with a second launch that finds nothing to join).
-ChunkPlan plan_of(const tsv_attn_shape* s, bool matrix, int window) {
+// No block is cut that has no more than 512 keys, nor where a window bounds every block and
+// blocks fill the GPU (64 tokens, windows of 1021: 55 us, 65 with a second launch that finds
+// nothing to join).
+ChunkPlan plan_of(const tsv_attn_shape* s, bool matrix, int window, int sinks) {
     ChunkPlan p;
     const int g = s->n_heads / s->n_kv_heads;
     const long long T = s->n_nodes, rows = T * g, items = s->batch < T ? s->batch : T, x = items * s->n_kv_heads;
-    p.rows = !matrix ? kRows : rows <= 16LL * s->batch ? 16 : 128;
-    p.want = !matrix ? 1024 : p.rows == 128 || x <= 128 ? 512 : x >= 512 ? 2048 : (int)(4 * x);
+    p.rows = !matrix ? kRows : rows <= 16LL * s->batch ? 16 : s->in_dtype == TSV_F32 ? 64 : 128;
+    p.want = !matrix ? 1024 : p.rows > 16 || x <= 128 ? 512 : x >= 512 ? 2048 : (int)(4 * x);
     p.min_keys = 256;
     const long long blocks = rows / p.rows > items ? rows / p.rows : items;
-    p.split = (long long)s->max_pages * s->page_size > 2 * p.min_keys && s->n_kv_heads <= p.want &&
-              !(window > 0 && blocks * s->n_kv_heads >= 512);
+    long long longest = (long long)s->max_pages * s->page_size;
+    if (window > 0 && longest > (long long)window + sinks + p.rows) longest = (long long)window + sinks + p.rows;
+    p.split = longest > 2 * p.min_keys && s->n_kv_heads <= p.want && !(window > 0 && blocks * s->n_kv_heads >= 512);
     // long work-groups should not start last (their order costs each a search of a microsecond)
-    p.sorted = p.rows == 128 && s->batch > 1 && s->batch <= kWave;
+    p.sorted = p.rows > 16 && s->batch > 1 && s->batch <= kWave;
     return p;
 }
 
@@ -320,7 +322,7 @@ ChunkPlan plan_of(const tsv_attn_shape* s, bool matrix, int window) {
 uint64_t attn_prefill_workspace_bytes(const tsv_attn_shape* s) {
     uint64_t most = 0;
     for (int matrix = 0; matrix <= (int)matrix_shape(s); ++matrix) {
-        const uint64_t n = chunk_workspace_bytes(plan_of(s, matrix, 0), s->n_kv_heads, s->head_dim);
+        const uint64_t n = chunk_workspace_bytes(plan_of(s, matrix, 0, 0), s->n_kv_heads, s->head_dim);
         if (n > most) most = n;
     }
     return most;
@@ -329,7 +331,7 @@ uint64_t attn_prefill_workspace_bytes(const tsv_attn_shape* s) {
 long long attn_prefill_blocks(const tsv_attn_shape* s) {
     long long most = 0;
     for (int matrix = 0; matrix <= (int)matrix_shape(s); ++matrix) {
-        const ChunkPlan p = plan_of(s, matrix, 0);
+        const ChunkPlan p = plan_of(s, matrix, 0, 0);
         const long long units = chunk_units(p, s->n_nodes, s->n_heads / s->n_kv_heads, s->batch, s->n_kv_heads) * s->n_kv_heads;
         const long long join = (long long)p.want * groups_of(p.rows);
         if (units > most) most = units;
@@ -341,12 +343,14 @@ long long attn_prefill_blocks(const tsv_attn_shape* s) {
 hipError_t launch_attn_prefill(const ChunkArgs& a, const tsv_attn_shape* s, void* workspace, hipStream_t stream) {
     const uintptr_t all = (uintptr_t)a.q | (uintptr_t)a.o | (uintptr_t)a.k_cache | (uintptr_t)a.v_cache;
     const bool matrix = matrix_shape(s) && all % 16 == 0;
-    const ChunkPlan p = plan_of(s, matrix, a.window == 0x7fffffff ? 0 : a.window);
+    const ChunkPlan p = plan_of(s, matrix, a.window == 0x7fffffff ? 0 : a.window, a.sinks);
     const ChunkWorkspace ws = chunk_workspace(workspace, p, a.Hk, a.D);
     const long long units = chunk_units(p, a.T, a.H / a.Hk, a.batch, a.Hk) * a.Hk;
     const dim3 grid((unsigned)(units > 0 ? units : 1));
     const bool bf16 = s->in_dtype == TSV_BF16, e4m3 = s->cache_dtype == TSV_E4M3;
-    if (matrix)
+    if (matrix && !bf16)
+        launch_chunk_f32(a, e4m3, p, ws, grid, stream);
+    else if (matrix)
         launch_chunk_mfma(a, e4m3, p, ws, grid, stream);
     else if (bf16 && e4m3)
         launch_plain<uint16_t, uint8_t>(a, p, ws, grid, stream);
