@@ -24,6 +24,8 @@ constexpr int kSub = 32;  // keys of a step
 // left of its steps, and the step that makes their number even
 constexpr int kOddSteps = 12;
 
+__device__ __forceinline__ bool nonfinite(float v) { return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u; }
+
 __device__ __forceinline__ bf16x8 as_operand(uint4 u) { return __builtin_bit_cast(bf16x8, u); }
 
 __device__ __forceinline__ uint4 only_finite(uint4 u) {
@@ -400,8 +402,14 @@ __global__ __launch_bounds__(256, 2) void chunk_tiles_kernel(ChunkArgs a, ChunkP
             }
         }
         if (E4M3 && w == 0) {
-            s_ks[(2 * m - 1 + lane / kSub) & 7][lane % kSub] = rks;
-            s_vs[(2 * m - 1 + lane / kSub) & 7][lane % kSub] = rvs;
+            // a value row's scale that is not finite: as its elements (below)
+            const int s = 2 * m - 1 + lane / kSub;
+            if (nonfinite(rvs) && !full(s)) {
+                if (s >= 0 && s < n) atomicOr(&s_odd[odd_of(s)], 1u << (lane % kSub));
+                rvs = 0.f;
+            }
+            s_ks[s & 7][lane % kSub] = rks;
+            s_vs[s & 7][lane % kSub] = rvs;
         }
     };
     auto store_V = [&](int m, int first) TSV_INLINE {
@@ -533,8 +541,8 @@ __global__ __launch_bounds__(256, 2) void chunk_tiles_kernel(ChunkArgs a, ChunkP
                 l += x1;
                 if (E4M3) {
                     const float2 vs = *(const float2*)&s_vs[s & 7][e / 4 * 8 + 4 * lg + e % 4];
-                    x0 = x0 == 0.f ? 0.f : x0 * vs.x;  // (a scale that is not finite is no masked row's)
-                    x1 = x1 == 0.f ? 0.f : x1 * vs.y;
+                    x0 *= vs.x;
+                    x1 *= vs.y;
                 }
                 b[e / 2] = pack_bf16x2(x0, x1);
                 asm volatile("" : "+v"(b[e / 2]), "+v"(l));  // (the compiler would move the weights behind all products)
@@ -549,11 +557,11 @@ __global__ __launch_bounds__(256, 2) void chunk_tiles_kernel(ChunkArgs a, ChunkP
     auto add_odd = [&](int i) TSV_INLINE {
         const int pos = chunk_pos(kk, kk.k0 + i);
         const uint32_t at = chunk_row(a, table[page_of(pos, a.div)], hk, pos);
-        const bool seen = pos <= own && (own - pos < a.window || pos < a.sinks);
+        const bool seen = pos <= own && (own - pos < a.window || pos < a.sinks), scaled = !E4M3 || !nonfinite(gload(a.v_scale + at));
 #pragma unroll
         for (int e = 0; e < NO * 16; ++e) {
             const size_t d = (size_t)at * D + e / 16 * 32 + e % 16 / 4 * 8 + 4 * lg + e % 4;
-            const uint16_t b = !E4M3 ? gload((const uint16_t*)a.v_cache + d) : (gload((const uint8_t*)a.v_cache + d) & 0x7f) == 0x7f ? 0x7fc0 : 0;
+            const uint16_t b = !E4M3 ? gload((const uint16_t*)a.v_cache + d) : !scaled || (gload((const uint8_t*)a.v_cache + d) & 0x7f) == 0x7f ? 0x7fc0 : 0;
             if (seen && (b & 0x7f80) == 0x7f80) o[e / 16][e % 16] += bf16_bits_to_f32(b);
             if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
         }

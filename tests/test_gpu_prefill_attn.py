@@ -192,6 +192,39 @@ def test_values_that_are_not_finite(bnd, dtype, value, n, window, sinks):
         c[m].copy_(keep)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("n,window,sinks", [(150, 0, 0), (150, 50, 3), (3, 0, 0), (700, 100, 1)])
+def test_scales_that_are_not_finite(bnd, dtype, value, n, window, sinks):
+    """A row of an 8-bit cache whose scale, or one of whose bytes, is a NaN: as a value that is not finite."""
+    old, at = 40, 41
+    c = case(35, [n], [old], 2, 64, 16, dtype, E4)
+    q = queries(36, n, 8, 64, dtype)
+    args, scales = U.cache_args(c)
+    clean = bnd.attn_prefill(q, V.starts([n]), *args, **scales, window=window, sinks=sinks)
+    see = [i for i in range(n) if Y.sees(old + i, at, window, sinks)]
+    others = [i for i in range(n) if i not in set(see)]
+    assert see and others
+    page, slot = int(c["page_table"][0, at // 16]), at % 16
+    for m in ("k_scale", "v_scale", "v_cache"):
+        t = c[m] if m != "v_cache" else c[m].view(torch.uint8)
+        keep = t.clone()
+        if m == "v_cache":
+            t[page, 1, slot, 7] = 0x7f
+        else:
+            t[page, 1, slot] = value
+        o = bnd.attn_prefill(q, V.starts([n]), *args, **scales, window=window, sinks=sinks)
+        assert torch.equal(o[others], clean[others]), m
+        assert torch.equal(o[:, :4], clean[:, :4]), "the other key head"
+        if m == "v_cache":
+            assert torch.isnan(o[see][:, 4:, 7].float()).all()
+        elif m == "v_scale":
+            assert not torch.isfinite(o[see][:, 4:].float()).any()
+        elif value != value:
+            assert torch.isnan(o[see][:, 4:].float()).all()
+        t.copy_(keep)
+
+
 def test_pages_outside_the_window_are_not_looked_at(bnd):
     """Entries of the table behind the window's start may hold anything."""
     lens, old, window, sinks = [20, 1], [500, 300], 60, 5
