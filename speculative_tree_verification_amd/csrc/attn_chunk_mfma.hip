@@ -315,7 +315,7 @@ __global__ __launch_bounds__(256, 3) void chunk_rows_kernel(ChunkArgs a, ChunkPl
 // in LDS, filled two steps at a time (one barrier), from registers that were requested
 // two steps before; the values follow the keys by two steps.
 template <int ND, bool E4M3>
-__global__ __launch_bounds__(256, 2) void chunk_tiles_kernel(ChunkArgs a, ChunkPlan plan, ChunkWorkspace ws) {
+__global__ __launch_bounds__(256, ND == 2 ? 3 : 2) void chunk_tiles_kernel(ChunkArgs a, ChunkPlan plan, ChunkWorkspace ws) {
     constexpr int D = ND * 32, M = 128, NK = D / 16, NO = D / 32;
     constexpr int kKs = D + 8, kVs = D + 32;
     __shared__ __attribute__((aligned(16))) uint16_t s_K[4][kSub * kKs], s_V[4][kSub * kVs];
@@ -492,13 +492,13 @@ __global__ __launch_bounds__(256, 2) void chunk_tiles_kernel(ChunkArgs a, ChunkP
                 t[e] = v < kk.k1 && pos <= own && (own - pos < a.window || pos < a.sinks) ? t[e] : -INFINITY;
             }
         }
-        float x = max3(t[0], t[1], t[2]), y = max3(t[3], t[4], t[5]);
+        float mx = max3(t[0], t[1], t[2]), my = max3(t[3], t[4], t[5]);
 #pragma unroll
         for (int e = 6; e < 14; e += 4) {
-            x = max3(x, t[e], t[e + 1]);
-            y = max3(y, t[e + 2], t[e + 3]);
+            mx = max3(mx, t[e], t[e + 1]);
+            my = max3(my, t[e + 2], t[e + 3]);
         }
-        const float mx = max3(max3(x, y, y), t[14], t[15]);
+        mx = max3(max3(mx, my, my), t[14], t[15]);
         rescale();  // of the step before: the sums have its predecessor's product now
         moved = __ballot(fmaf(mx, c, -base) > kSlack) != 0;
         if (moved) {
@@ -513,14 +513,31 @@ __global__ __launch_bounds__(256, 2) void chunk_tiles_kernel(ChunkArgs a, ChunkP
         // read all of K and V into registers first). The wave goes first meanwhile (4096 tokens:
         // 183 us without)
         __builtin_amdgcn_s_setprio(1);
-        constexpr int SLOTS = NK + 2 * NO, PAIRS = 8;
-        static_assert(NK == 2 * NO, "as many slots of each");
+        constexpr int SLOTS = NK + 2 * NO, EVERY = SLOTS / 8;
+        static_assert(NK == 2 * NO && SLOTS % 8 == 0, "as many slots of each, whole slots of a pair of weights");
         auto operand = [&](int j) TSV_INLINE {
             const int i = j / 2;
             return j % 2 == 0 ? *(const bf16x8*)&s_K[(slot + 1) & 3][lr * kKs + 16 * i + 8 * lg]
                           : read_columns32(&s_V[(slot + 3) & 3][16 * (i / NO) * kVs + 32 * (i % NO)], kVs, lane);
         };
         uint32_t b[8];
+        float x[3][2];
+        auto exponentials = [&](int y) TSV_INLINE {
+            x[y % 3][0] = __builtin_amdgcn_exp2f(x[y % 3][0]);
+            x[y % 3][1] = __builtin_amdgcn_exp2f(x[y % 3][1]);
+        };
+        auto weights = [&](int y) TSV_INLINE {
+            float x0 = x[y % 3][0], x1 = x[y % 3][1];
+            l += x0;  // of this lane's keys; the lanes of a row meet at the end
+            l += x1;
+            if (E4M3) {
+                const float2 vs = *(const float2*)&s_vs[s & 7][y / 2 * 8 + 4 * lg + 2 * y % 4];
+                x0 *= vs.x;
+                x1 *= vs.y;
+            }
+            b[y] = pack_bf16x2(x0, x1);
+            asm volatile("" : "+v"(b[y]), "+v"(l));  // (the compiler would move the weights behind all products)
+        };
         constexpr int AHEAD = 2;
         bf16x8 f[AHEAD + 1];
 #pragma unroll
@@ -533,22 +550,20 @@ __global__ __launch_bounds__(256, 2) void chunk_tiles_kernel(ChunkArgs a, ChunkP
                 sn = mma(f[j % (AHEAD + 1)], q[j / 2], sn);
             else
                 o[j / 2 % NO] = mma(f[j % (AHEAD + 1)], p[j / 2 / NO], o[j / 2 % NO]);
-#pragma unroll
-            for (int y = j * PAIRS / SLOTS; y < (j + 1) * PAIRS / SLOTS; ++y) {
-                const int e = 2 * y;
-                float x0 = __builtin_amdgcn_exp2f(fmaf(t[e], c, -base)), x1 = __builtin_amdgcn_exp2f(fmaf(t[e + 1], c, -base));
-                l += x0;  // of this lane's keys; the lanes of a row meet at the end
-                l += x1;
-                if (E4M3) {
-                    const float2 vs = *(const float2*)&s_vs[s & 7][e / 4 * 8 + 4 * lg + e % 4];
-                    x0 *= vs.x;
-                    x1 *= vs.y;
-                }
-                b[e / 2] = pack_bf16x2(x0, x1);
-                asm volatile("" : "+v"(b[e / 2]), "+v"(l));  // (the compiler would move the weights behind all products)
+            // pair y of weights: its arguments, a slot later its exponentials, and another one later
+            // the rest, so that no instruction waits for the one before it
+            if (j % EVERY == 0) {
+                const int y = j / EVERY;
+                x[y % 3][0] = fmaf(t[2 * y], c, -base);
+                x[y % 3][1] = fmaf(t[2 * y + 1], c, -base);
             }
+            if (j >= 1 && (j - 1) % EVERY == 0) exponentials((j - 1) / EVERY);
+            if (j >= 2 && (j - 2) % EVERY == 0) weights((j - 2) / EVERY);
             __builtin_amdgcn_sched_barrier(0);
         }
+        if (EVERY == 1) exponentials(7);
+        if (EVERY == 1) weights(6);
+        weights(7);
         __builtin_amdgcn_s_setprio(0);
         pn[0] = as_operand(make_uint4(b[0], b[1], b[2], b[3]));
         pn[1] = as_operand(make_uint4(b[4], b[5], b[6], b[7]));

@@ -164,13 +164,13 @@ __global__ __launch_bounds__(256) void chunk_plain_kernel(ChunkArgs a, ChunkPlan
     }
 }
 
-// Lanes take 4 elements of a row each, LPR lanes a row. A work-group has kJoinRows rows of a
-// block; where the block has fewer rows than the work-group groups of lanes, several groups
-// share a row's parts.
-constexpr int kJoinRows = 32;
-
+// Lanes take 4 elements of a row each, LPR lanes a row. A work-group has `per` rows of a
+// block; where it has more groups of lanes than rows, several share a row's parts. Few blocks
+// have many parts, and their rows work-groups of their own (64 tokens over 30000 positions,
+// 2048 rows of 32 parts each: 53 us with 32 rows a work-group, 15 with 2); but a work-group's
+// search for its block costs as much as some rows, so there are some 2000 of them.
 template <typename TIO, int LPR>
-__global__ __launch_bounds__(256) void chunk_join_kernel(ChunkArgs a, ChunkPlan plan, ChunkWorkspace ws, int groups) {
+__global__ __launch_bounds__(256) void chunk_join_kernel(ChunkArgs a, ChunkPlan plan, ChunkWorkspace ws, int per, int groups) {
     constexpr int kAt = 256 / LPR, kLoads = 8;
     __shared__ __attribute__((aligned(16))) float s_o[kAt][LPR * 4];
     __shared__ float s_ml[kAt][2];
@@ -179,11 +179,11 @@ __global__ __launch_bounds__(256) void chunk_join_kernel(ChunkArgs a, ChunkPlan 
     if (!u.ok || ws.bad[(size_t)u.slot * a.Hk + hk]) return;
     const int D = a.D, g = a.H / a.Hk, row0 = u.block * plan.rows, rows = min(u.n * g - row0, plan.rows);
     int share = 1;  // groups of a row
-    while (2 * share * rows <= kAt) share *= 2;
-    const int first = blockIdx.x % groups * kJoinRows;
+    while (2 * share * min(per, rows) <= kAt) share *= 2;
+    const int first = blockIdx.x % groups * per;
     const bool whole = D % 4 == 0 && (uintptr_t)a.o % (4 * sizeof(TIO)) == 0;  // pieces of four, aligned
     auto piece = [&](const float* p) { return d >= D ? make_float4(0.f, 0.f, 0.f, 0.f) : whole ? ld4<true>(p, 4) : ld4<false>(p, D - d); };
-    for (int r0 = first; r0 < min(rows, first + kJoinRows); r0 += kAt / share) {
+    for (int r0 = first; r0 < min(rows, first + per); r0 += kAt / share) {
         const int r = min(r0 + grp / share, rows - 1);
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(256) void chunk_join_kernel(ChunkArgs a, ChunkPlan 
                 o.w = fmaf(f, v.w, o.w);
             }
         }
-        if (d >= D || grp % share || r0 + grp / share >= rows) continue;
+        if (d >= D || grp % share || r0 + grp / share >= min(rows, first + per)) continue;
         const int row = row0 + r;
         TIO* to = (TIO*)a.o + (((size_t)u.start + row / g) * a.H + hk * g + row % g) * D + d;
         const float f[4] = {o.x / l, o.y / l, o.z / l, o.w / l};
@@ -267,19 +267,30 @@ void launch_plain(const ChunkArgs& a, const ChunkPlan& p, const ChunkWorkspace& 
         hipLaunchKernelGGL((chunk_plain_kernel<TIO, TC, 4>), grid, dim3(256), 0, stream, a, p, ws);
 }
 
-int groups_of(int rows) { return (rows + kJoinRows - 1) / kJoinRows; }
+// The blocks that may be cut, times the key heads; rows and work-groups of the join
+struct Join {
+    int per, groups;  // rows of a work-group, work-groups of a block
+    long long blocks;  // work-groups
+};
+Join join_of(const ChunkPlan& p, long long T, int H, int Hk, int batch) {
+    const long long blocks = chunk_blocks(p, T, H / Hk, batch), units = (blocks < p.want / Hk ? blocks : p.want / Hk) * Hk;
+    Join j;
+    for (j.per = 1; j.per < 32 && units * ((p.rows + j.per - 1) / j.per) > 2048;) j.per *= 2;
+    j.groups = (p.rows + j.per - 1) / j.per;
+    j.blocks = units * j.groups;
+    return j;
+}
 
 template <typename TIO>
 void launch_join(const ChunkArgs& a, const ChunkPlan& p, const ChunkWorkspace& ws, hipStream_t stream) {
-    const int groups = groups_of(p.rows);
-    const dim3 grid((unsigned)((long long)(p.want / a.Hk) * a.Hk * groups));
-    if (grid.x == 0) return;
+    const Join j = join_of(p, a.T, a.H, a.Hk, a.batch);
+    const dim3 grid((unsigned)j.blocks);
     if (a.D <= 64)
-        hipLaunchKernelGGL((chunk_join_kernel<TIO, 16>), grid, dim3(256), 0, stream, a, p, ws, groups);
+        hipLaunchKernelGGL((chunk_join_kernel<TIO, 16>), grid, dim3(256), 0, stream, a, p, ws, j.per, j.groups);
     else if (a.D <= 128)
-        hipLaunchKernelGGL((chunk_join_kernel<TIO, 32>), grid, dim3(256), 0, stream, a, p, ws, groups);
+        hipLaunchKernelGGL((chunk_join_kernel<TIO, 32>), grid, dim3(256), 0, stream, a, p, ws, j.per, j.groups);
     else
-        hipLaunchKernelGGL((chunk_join_kernel<TIO, 64>), grid, dim3(256), 0, stream, a, p, ws, groups);
+        hipLaunchKernelGGL((chunk_join_kernel<TIO, 64>), grid, dim3(256), 0, stream, a, p, ws, j.per, j.groups);
 }
 
 // Whether the matrix kernels take the shape: 32-bit row numbers into the pool, and
@@ -333,7 +344,7 @@ long long attn_prefill_blocks(const tsv_attn_shape* s) {
     for (int matrix = 0; matrix <= (int)matrix_shape(s); ++matrix) {
         const ChunkPlan p = plan_of(s, matrix, 0, 0);
         const long long units = chunk_units(p, s->n_nodes, s->n_heads / s->n_kv_heads, s->batch, s->n_kv_heads) * s->n_kv_heads;
-        const long long join = (long long)p.want * groups_of(p.rows);
+        const long long join = join_of(p, s->n_nodes, s->n_heads, s->n_kv_heads, s->batch).blocks;
         if (units > most) most = units;
         if (join > most) most = join;
     }
