@@ -20,32 +20,32 @@ namespace {
 
 constexpr int kRopeRows = 16;  // most rows of a work-group
 
+// How a lane has its eight pairs:
+//   kHalves       pairs 8 j + i of (i, i + R / 2), as two pieces of eight neighbours; past the
+//                 rotated elements sixteen neighbours, as two pieces
+//   kInterleaved  pairs 8 j + i of (2 i, 2 i + 1), sixteen neighbours
+//   kAny          pairs j + LPH i of either kind, element by element
+enum Pairing { kHalves, kInterleaved, kAny };
+
 // Element numbers of pair p
 __device__ __forceinline__ int2 pair_of(const RopeArgs& a, int p) {
     const int half = a.R / 2;
     return p < half && !a.interleaved ? make_int2(p, p + half) : make_int2(2 * p, 2 * p + 1);
 }
 
-struct Pairs {
-    float a[8], b[8];
-};
-
-// A lane's eight pairs: VEC: 8 j + i, as two pieces of eight elements; otherwise j + LPH i
-template <typename TIO, int LPH, bool VEC>
+// A lane's sixteen elements: its two pieces, or (kAny) its pairs' first and second ones
+template <typename TIO, bool VEC>
 struct Piece {
     Raw<TIO, VEC> lo, hi;
 };
+struct Lane16 {
+    float lo[8], hi[8];
+};
 
-// First elements of the two pieces: the pairs' first and second ones, or (interleaved pairs,
-// and elements that are not rotated) sixteen neighbours
-__device__ __forceinline__ int2 pieces_of(const RopeArgs& a, int j) {
-    return !a.interleaved && 16 * j < a.R ? make_int2(8 * j, a.R / 2 + 8 * j) : make_int2(16 * j, 16 * j + 8);
-}
-
-template <typename TIO, int LPH, bool VEC>
-__device__ __forceinline__ Piece<TIO, LPH, VEC> load_pairs(const RopeArgs& a, const TIO* row, int j, int2 at) {
-    Piece<TIO, LPH, VEC> p{};
-    if constexpr (VEC) {
+template <typename TIO, int LPH, Pairing P>
+__device__ __forceinline__ Piece<TIO, P != kAny> load_head(const RopeArgs& a, const TIO* row, int j, int2 at) {
+    Piece<TIO, P != kAny> p{};
+    if constexpr (P != kAny) {
         if (16 * j >= a.D) return p;
         p.lo = load8<TIO, true>(row + at.x, 8);
         p.hi = load8<TIO, true>(row + at.y, 8);
@@ -58,61 +58,6 @@ __device__ __forceinline__ Piece<TIO, LPH, VEC> load_pairs(const RopeArgs& a, co
         }
     }
     return p;
-}
-
-// Pieces in the elements' order <-> pairs. Only interleaved pairs are not in their places
-// (elements that are not rotated may pair in any way)
-template <bool VEC>
-__device__ __forceinline__ Pairs to_pairs(const RopeArgs& a, const Quad& lo, const Quad& hi) {
-    Pairs p;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        p.a[i] = lo.v[i];
-        p.b[i] = hi.v[i];
-    }
-    if (VEC && a.interleaved) {
-        asm volatile("");  // (or the compiler selects, for both kinds)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            p.a[i] = i < 4 ? lo.v[2 * i] : hi.v[2 * i - 8];
-            p.b[i] = i < 4 ? lo.v[2 * i + 1] : hi.v[2 * i - 7];
-        }
-    }
-    return p;
-}
-template <bool VEC>
-__device__ __forceinline__ void to_pieces(const RopeArgs& a, const Pairs& p, Quad& lo, Quad& hi) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo.v[i] = p.a[i];
-        hi.v[i] = p.b[i];
-    }
-    if (VEC && a.interleaved) {
-        asm volatile("");
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            lo.v[i] = i % 2 ? p.b[i / 2] : p.a[i / 2];
-            hi.v[i] = i % 2 ? p.b[4 + i / 2] : p.a[4 + i / 2];
-        }
-    }
-}
-
-template <int LPH, bool VEC>
-__device__ __forceinline__ Pairs load_weight(const RopeArgs& a, const float* w, int j, int2 at) {
-    if (!w) return Pairs{};
-    if constexpr (VEC) {
-        if (16 * j >= a.D) return Pairs{};
-        return to_pairs<true>(a, floats<float, true>(load8<float, true>(w + at.x, 8)), floats<float, true>(load8<float, true>(w + at.y, 8)));
-    } else {
-        Pairs p;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int2 e = pair_of(a, j + LPH * i);
-            p.a[i] = e.x < a.D ? gload(w + e.x) : 0.f;
-            p.b[i] = e.y < a.D ? gload(w + e.y) : 0.f;
-        }
-        return p;
-    }
 }
 
 // Sum over the LPH <= 16 neighbouring lanes of a head
@@ -129,35 +74,45 @@ __device__ __forceinline__ float head_sum(float v) {
 
 // 8 neighbours, rounded to nearest even
 template <typename TIO>
-__device__ __forceinline__ void store_piece(TIO* to, const Quad& q) {
+__device__ __forceinline__ void store_piece(TIO* to, const float (&v)[8]) {
     if constexpr (sizeof(TIO) == 2) {
-        gstore((uint4*)to, make_uint4(pack_bf16x2(q.v[0], q.v[1]), pack_bf16x2(q.v[2], q.v[3]), pack_bf16x2(q.v[4], q.v[5]),
-                                      pack_bf16x2(q.v[6], q.v[7])));
+        gstore((uint4*)to, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
     } else {
-        gstore((float4*)to, make_float4(q.v[0], q.v[1], q.v[2], q.v[3]));
-        gstore((float4*)to + 1, make_float4(q.v[4], q.v[5], q.v[6], q.v[7]));
+        gstore((float4*)to, make_float4(v[0], v[1], v[2], v[3]));
+        gstore((float4*)to + 1, make_float4(v[4], v[5], v[6], v[7]));
     }
 }
-template <typename TIO, int LPH, bool VEC>
-__device__ __forceinline__ void store_head(const RopeArgs& a, TIO* row, const Quad& lo, const Quad& hi, int j, int2 to) {
-    if constexpr (VEC) {
+template <typename TIO, int LPH, Pairing P>
+__device__ __forceinline__ void store_head(const RopeArgs& a, TIO* row, const Lane16& x, int j, int2 to) {
+    if constexpr (P != kAny) {
         if (16 * j >= a.D) return;
-        store_piece<TIO>(row + to.x, lo);
-        store_piece<TIO>(row + to.y, hi);
+        store_piece<TIO>(row + to.x, x.lo);
+        store_piece<TIO>(row + to.y, x.hi);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int2 e = pair_of(a, j + LPH * i);
-            if (e.x < a.D) Elem<TIO>::st(row, e.x, lo.v[i]);
-            if (e.y < a.D) Elem<TIO>::st(row, e.y, hi.v[i]);
+            if (e.x < a.D) Elem<TIO>::st(row, e.x, x.lo[i]);
+            if (e.y < a.D) Elem<TIO>::st(row, e.y, x.hi[i]);
         }
     }
 }
-template <int LPH, bool VEC>
-__device__ __forceinline__ void store_head_e4m3(const RopeArgs& a, uint8_t* row, const Quad& lo, const Quad& hi, int j, int2 to, float scale) {
+// The row of a head in 8 bits, and its scale
+template <int LPH, Pairing P>
+__device__ __forceinline__ void store_head_e4m3(const RopeArgs& a, uint8_t* row, float* scale_to, const Lane16& x, int j, int2 to) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, max(__float_as_uint(x.lo[i]) & 0x7fffffffu, __float_as_uint(x.hi[i]) & 0x7fffffffu));
+    const float scale = scale_of(max_of<LPH>(top));
     const bool finite = scale == scale;
-    const uint2 ul = e4m3_bytes(lo, scale, finite), uh = e4m3_bytes(hi, scale, finite);
-    if constexpr (VEC) {
+    Quad q;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q.v[i] = x.lo[i];
+    const uint2 ul = e4m3_bytes(q, scale, finite);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q.v[i] = x.hi[i];
+    const uint2 uh = e4m3_bytes(q, scale, finite);
+    if constexpr (P != kAny) {
         if (16 * j >= a.D) return;
         gstore((uint2*)(row + to.x), ul);
         gstore((uint2*)(row + to.y), uh);
@@ -170,35 +125,60 @@ __device__ __forceinline__ void store_head_e4m3(const RopeArgs& a, uint8_t* row,
             if (e.y < a.D) row[e.y] = (uint8_t)(wh[i / 4] >> (8 * (i % 4)));
         }
     }
+    if (j == 0) *scale_to = scale;
 }
 
-// Heads of a row: H of q, Hk of k, and where they go into the cache Hk of v.
-// `rb` rows a work-group.
-template <typename TIO, int LPH, bool VEC, bool APPEND, bool E4M3>
+template <typename TIO, bool VEC>
+__device__ __forceinline__ Lane16 to_floats(const Piece<TIO, VEC>& p) {
+    Lane16 x;
+    const Quad lo = floats<TIO, VEC>(p.lo), hi = floats<TIO, VEC>(p.hi);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x.lo[i] = lo.v[i];
+        x.hi[i] = hi.v[i];
+    }
+    return x;
+}
+
+// (z_a, z_b) turned
+__device__ __forceinline__ void turn(float& za, float& zb, float cs, float sn) {
+    const float x = za;
+    za = fmaf(x, cs, -zb * sn);
+    zb = fmaf(zb, cs, x * sn);
+}
+
+// Heads of a row: H of q and Hk of k, which are normed and turned, and where they go into the
+// cache Hk of v. `rb` rows a work-group.
+template <typename TIO, int LPH, Pairing P, bool APPEND, bool E4M3>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, CacheWriteArgs c, int rb, int row_blocks) {
-    __shared__ __attribute__((aligned(16))) float s_cos[kRopeRows][128], s_sin[kRopeRows][128];
+    __shared__ __attribute__((aligned(16))) float s_cos[kRopeRows][128], s_sin[kRopeRows][128], s_w[2][256];
     __shared__ RowPlaces<kRopeRows> places;
+    constexpr bool VEC = P != kAny;
     constexpr int kSlots = 256 / LPH;
     const int tid = threadIdx.x, j = tid % LPH;
-    const int2 at = pieces_of(a, j);
+    // first elements of the lane's two pieces
+    const bool turned = 16 * j < a.R;
+    const int2 at = P == kHalves && turned ? make_int2(8 * j, a.R / 2 + 8 * j) : make_int2(16 * j, 16 * j + 8);
     const bool rows = (int)blockIdx.x < row_blocks;
     const int r0 = blockIdx.x * rb, n = rows ? min(rb, a.rows - r0) : 0;
-    const int Hq = a.q ? a.H : 0, Hx = a.k ? a.Hk : 0, heads = Hq + (APPEND ? 2 : 1) * Hx, units = n * heads;
-    typedef Piece<TIO, LPH, VEC> P;
+    const int Hq = a.q ? a.H : 0, Hx = a.k ? a.Hk : 0, heads = Hq + Hx, units = n * heads;
+    typedef Piece<TIO, VEC> Raw16;
     auto fetch = [&](int u) {
-        P p{};
-        if (u >= units) return p;
+        if (u >= units) return Raw16{};
         const int row = page_of(u, a.heads), h = u - row * heads;
         const size_t r = (size_t)(r0 + row);
-        const TIO* from = h < Hq ? (const TIO*)a.q + r * a.qs + (size_t)h * a.D
-                                 : h < Hq + Hx ? (const TIO*)a.k + r * a.ks + (size_t)(h - Hq) * a.D
-                                               : (const TIO*)a.v + r * a.vs + (size_t)(h - Hq - Hx) * a.D;
-        return load_pairs<TIO, LPH, VEC>(a, from, j, at);
+        return load_head<TIO, LPH, P>(a, h < Hq ? (const TIO*)a.q + r * a.qs + (size_t)h * a.D : (const TIO*)a.k + r * a.ks + (size_t)(h - Hq) * a.D, j, at);
+    };
+    auto fetch_v = [&](int u) {
+        if (u >= n * Hx) return Raw16{};
+        const int row = page_of(u, a.key_heads), h = u - row * Hx;
+        return load_head<TIO, LPH, P>(a, (const TIO*)a.v + (size_t)(r0 + row) * a.vs + (size_t)h * a.D, j, at);
     };
     // the first rows are on their way while their places and angles are found
     int u = tid / LPH;
-    P next = fetch(u);
-    const Pairs wq = load_weight<LPH, VEC>(a, a.qw, j, at), wk = load_weight<LPH, VEC>(a, a.kw, j, at);
+    Raw16 next = fetch(u);
+    s_w[0][tid] = a.qw && tid < a.D ? a.qw[tid] : 1.f;
+    s_w[1][tid] = a.kw && tid < a.D ? a.kw[tid] : 1.f;
     if (APPEND) {
         if (!find_places<kRopeRows>(c, r0, n, rows ? -1 : (int)blockIdx.x - row_blocks, places)) return;
     } else {
@@ -216,68 +196,92 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, CacheWriteArgs c,
     }
     lds_barrier();
     for (; u < units; u += kSlots) {
-        const P now = next;
+        const Raw16 now = next;
         next = fetch(u + kSlots);
         const int row = page_of(u, a.heads), h = u - row * heads;
-        const int place = places.place[row];
-        if (place < 0) continue;  // a row of no sequence, or left out by its position (the same for a head's lanes)
-        const bool is_q = h < Hq, is_v = APPEND && h >= Hq + Hx;
-        Quad lo = floats<TIO, VEC>(now.lo), hi = floats<TIO, VEC>(now.hi);
-        if (!is_v) {
-            Pairs x = to_pairs<VEC>(a, lo, hi);
-            if (is_q ? a.qw != nullptr : a.kw != nullptr) {
-                float sum = 0.f;
+        if (places.place[row] < 0) continue;  // a row of no sequence, or left out by its position (the same for a head's lanes)
+        const bool is_q = h < Hq;
+        const float* wt = s_w[!is_q];
+        Lane16 x = to_floats<TIO, VEC>(now);
+        float by = 1.f;
+        if (is_q ? a.qw != nullptr : a.kw != nullptr) {
+            float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum = fmaf(x.a[i], x.a[i], fmaf(x.b[i], x.b[i], sum));
-                sum = head_sum<LPH>(sum);
-                const float r = 1.f / sqrtf(sum / (float)a.D + a.eps);
+            for (int i = 0; i < 8; ++i) sum = fmaf(x.lo[i], x.lo[i], fmaf(x.hi[i], x.hi[i], sum));
+            by = 1.f / sqrtf(head_sum<LPH>(sum) / (float)a.D + a.eps);
+        }
+        // (the weights are 1 where there is no norm; a lane past the head's end has zeros)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x.a[i] *= r * (is_q ? wq.a[i] : wk.a[i]);
-                    x.b[i] *= r * (is_q ? wq.b[i] : wk.b[i]);
-                }
-            }
+        for (int i = 0; i < 8; ++i) {
+            const int2 e = VEC ? make_int2(at.x + i, at.y + i) : pair_of(a, j + LPH * i);
+            x.lo[i] *= by * wt[e.x];
+            x.hi[i] *= by * wt[e.y];
+        }
+        if (!VEC) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int p = VEC ? 8 * j + i : j + LPH * i;
-                if (2 * p < a.R) {
-                    const float cs = s_cos[row][p], sn = s_sin[row][p], xa = x.a[i];
-                    x.a[i] = fmaf(xa, cs, -x.b[i] * sn);
-                    x.b[i] = fmaf(x.b[i], cs, xa * sn);
-                }
+                const int p = j + LPH * i;
+                if (2 * p < a.R) turn(x.lo[i], x.hi[i], s_cos[row][p], s_sin[row][p]);
             }
-            to_pieces<VEC>(a, x, lo, hi);
+        } else if (turned) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float cs = s_cos[row][8 * j + i], sn = s_sin[row][8 * j + i];
+                if (P == kHalves)
+                    turn(x.lo[i], x.hi[i], cs, sn);
+                else if (i < 4)
+                    turn(x.lo[2 * i], x.lo[2 * i + 1], cs, sn);
+                else
+                    turn(x.hi[2 * i - 8], x.hi[2 * i - 7], cs, sn);
+            }
         }
         if (is_q) {
-            store_head<TIO, LPH, VEC>(a, (TIO*)a.q_out + ((size_t)(r0 + row) * a.H + h) * a.D, lo, hi, j, at);
+            store_head<TIO, LPH, P>(a, (TIO*)a.q_out + ((size_t)(r0 + row) * a.H + h) * a.D, x, j, at);
         } else if (!APPEND) {
-            store_head<TIO, LPH, VEC>(a, (TIO*)a.k_out + ((size_t)(r0 + row) * a.Hk + (h - Hq)) * a.D, lo, hi, j, at);
+            store_head<TIO, LPH, P>(a, (TIO*)a.k_out + ((size_t)(r0 + row) * a.Hk + (h - Hq)) * a.D, x, j, at);
         } else {
-            const int hk = is_v ? h - Hq - Hx : h - Hq;
-            const size_t dst = (size_t)(places.dst[row] + (long long)hk * c.page_size);
-            if (E4M3) {
-                uint32_t top = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    top = max(top, max(__float_as_uint(lo.v[i]) & 0x7fffffffu, __float_as_uint(hi.v[i]) & 0x7fffffffu));
-                const float scale = scale_of(max_of<LPH>(top));
-                store_head_e4m3<LPH, VEC>(a, (uint8_t*)(is_v ? c.v_cache : c.k_cache) + dst * a.D, lo, hi, j, at, scale);
-                if (j == 0) (is_v ? c.v_scale : c.k_scale)[dst] = scale;
-            } else {
-                store_head<TIO, LPH, VEC>(a, (TIO*)(is_v ? c.v_cache : c.k_cache) + dst * a.D, lo, hi, j, at);
-            }
+            const size_t dst = (size_t)(places.dst[row] + (long long)(h - Hq) * c.page_size);
+            if constexpr (E4M3)
+                store_head_e4m3<LPH, P>(a, (uint8_t*)c.k_cache + dst * a.D, c.k_scale + dst, x, j, at);
+            else
+                store_head<TIO, LPH, P>(a, (TIO*)c.k_cache + dst * a.D, x, j, at);
         }
+    }
+    if (!APPEND) return;
+    u = tid / LPH;
+    next = fetch_v(u);
+    for (; u < n * Hx; u += kSlots) {
+        const Raw16 now = next;
+        next = fetch_v(u + kSlots);
+        const int row = page_of(u, a.key_heads), h = u - row * Hx;
+        if (places.place[row] < 0) continue;
+        const size_t dst = (size_t)(places.dst[row] + (long long)h * c.page_size);
+        const Lane16 x = to_floats<TIO, VEC>(now);
+        if constexpr (E4M3)
+            store_head_e4m3<LPH, P>(a, (uint8_t*)c.v_cache + dst * a.D, c.v_scale + dst, x, j, at);
+        else
+            store_head<TIO, LPH, P>(a, (TIO*)c.v_cache + dst * a.D, x, j, at);
     }
 }
 
-template <typename TIO, int LPH, bool VEC>
+template <typename TIO, int LPH, Pairing P>
 void launch_one(const RopeArgs& a, const CacheWriteArgs* c, bool e4m3, int rb, int blocks, int all, hipStream_t stream) {
     if (!c)
-        hipLaunchKernelGGL((rope_kernel<TIO, LPH, VEC, false, false>), dim3(all), dim3(256), 0, stream, a, CacheWriteArgs{}, rb, blocks);
+        hipLaunchKernelGGL((rope_kernel<TIO, LPH, P, false, false>), dim3(all), dim3(256), 0, stream, a, CacheWriteArgs{}, rb, blocks);
     else if (e4m3)
-        hipLaunchKernelGGL((rope_kernel<TIO, LPH, VEC, true, true>), dim3(all), dim3(256), 0, stream, a, *c, rb, blocks);
+        hipLaunchKernelGGL((rope_kernel<TIO, LPH, P, true, true>), dim3(all), dim3(256), 0, stream, a, *c, rb, blocks);
     else
-        hipLaunchKernelGGL((rope_kernel<TIO, LPH, VEC, true, false>), dim3(all), dim3(256), 0, stream, a, *c, rb, blocks);
+        hipLaunchKernelGGL((rope_kernel<TIO, LPH, P, true, false>), dim3(all), dim3(256), 0, stream, a, *c, rb, blocks);
+}
+
+template <typename TIO, Pairing P>
+void launch_pairing(const RopeArgs& a, const CacheWriteArgs* c, bool e4m3, int rb, int blocks, int all, hipStream_t stream) {
+    if (a.D <= 64)
+        launch_one<TIO, 4, P>(a, c, e4m3, rb, blocks, all, stream);
+    else if (a.D <= 128)
+        launch_one<TIO, 8, P>(a, c, e4m3, rb, blocks, all, stream);
+    else
+        launch_one<TIO, 16, P>(a, c, e4m3, rb, blocks, all, stream);
 }
 
 template <typename TIO>
@@ -286,17 +290,15 @@ hipError_t launch_type(const RopeArgs& a, const CacheWriteArgs* c, bool e4m3, hi
     if (all == 0) return hipSuccess;
     // eight elements at a time where heads, strides and pointers allow it
     uintptr_t bits = (uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.q_out | (uintptr_t)a.k_out;
-    bits |= (uintptr_t)((a.qs | a.ks | a.vs) * sizeof(TIO)) | (uintptr_t)a.qw | (uintptr_t)a.kw;
+    bits |= (uintptr_t)((a.qs | a.ks | a.vs) * sizeof(TIO));
     if (c) bits |= (uintptr_t)c->k_cache | (uintptr_t)c->v_cache;
     const bool vec = a.D % 16 == 0 && a.R % 16 == 0 && bits % 16 == 0;
     if (!vec)
-        launch_one<TIO, 16, false>(a, c, e4m3, rb, blocks, all, stream);
-    else if (a.D <= 64)
-        launch_one<TIO, 4, true>(a, c, e4m3, rb, blocks, all, stream);
-    else if (a.D <= 128)
-        launch_one<TIO, 8, true>(a, c, e4m3, rb, blocks, all, stream);
+        launch_one<TIO, 16, kAny>(a, c, e4m3, rb, blocks, all, stream);
+    else if (a.interleaved)
+        launch_pairing<TIO, kInterleaved>(a, c, e4m3, rb, blocks, all, stream);
     else
-        launch_one<TIO, 16, true>(a, c, e4m3, rb, blocks, all, stream);
+        launch_pairing<TIO, kHalves>(a, c, e4m3, rb, blocks, all, stream);
     return hipGetLastError();
 }
 

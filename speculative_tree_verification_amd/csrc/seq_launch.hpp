@@ -82,7 +82,7 @@ struct RopeArgs {
     long long qs, ks, vs;  // elements between rows
     int rows, H, Hk, D, R, interleaved;
     float eps;
-    PageDiv heads;  // by a row's heads, of q, k and (into the cache) v
+    PageDiv heads, key_heads;  // by a row's heads of q and k, and by those of k
 };
 int rope_rows(int rows);                        // rows of a work-group
 long long rope_blocks(int rows, int items);     // work-groups, with the items' status
