@@ -428,3 +428,90 @@ def test_calls_on_two_streams(bnd):
     torch.cuda.synchronize()
     for r in got:
         assert all(torch.equal(a, b) for a, b in zip(r, want))
+
+
+def test_cache_past_32_bits(bnd):
+    """Pages whose bytes lie past 2^32: written by the rotated append, read by each kernel."""
+    Hk, D, page, pages = 8, 128, 64, 35000  # 4.6 GB a cache
+    free, _ = torch.cuda.mem_get_info()
+    if free < 12 << 30:
+        pytest.skip("needs 12 GB")
+    kc, vc = (torch.empty(pages, Hk, page, D, dtype=BF, device="cuda") for _ in range(2))
+    table = torch.tensor([[pages - 1, 5, pages - 3, pages - 2], [pages - 7, 0, 0, 0]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([0, 0], dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(37)
+    q, k, v = (torch.randn(203, h, D, generator=g).to(BF).cuda() for h in (16, Hk, Hk))
+    f = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).float().cuda()
+    qo = bnd.attn_append_rope(q, k, v, V.starts([200, 3]), f, kc, vc, table, lens)
+    c = {"k_cache": kc[[pages - 1, 5, pages - 3, pages - 2, pages - 7]], "v_cache": vc[[pages - 1, 5, pages - 3, pages - 2, pages - 7]],
+         "page_table": torch.tensor([[0, 1, 2, 3], [4, 0, 0, 0]], dtype=torch.int32), "cache_len": lens, "k_scale": None, "v_scale": None}
+    pos = torch.tensor([*range(200), *range(3)], dtype=torch.int32, device="cuda")
+    want = bnd.attn_rope(None, k, pos, f)[1]
+    rows = torch.arange(200)
+    assert torch.equal(c["k_cache"][(rows // page).cuda(), :, (rows % page).cuda()], want[:200])
+    for generic in (False, True):
+        o = bnd.attn_prefill(qo, V.starts([200, 3]), kc, vc, table, lens, force_generic=generic)
+        for b, i, at in ((0, 0, 0), (0, 199, 199), (0, 77, 77), (1, 2, 202)):
+            kk, vv = V.cached(c, b, i + 1)
+            r, oa, top = Y.attend(U.f64(qo[at:at + 1]), i, kk, vv, D ** -0.5)
+            U.within(U.f64(o[at:at + 1]), r, V.attend_bound(r, oa, top, D, i + 1, BF), f"row {i} of {b}")
+    lens.copy_(torch.tensor([199, 2]))
+    one = bnd.attn_prefill(qo[[199, 202]], V.starts([1, 1]), kc, vc, table, lens)  # the few rows' kernel
+    for x, (b, i, at) in zip(one, ((0, 199, 199), (1, 2, 202))):
+        kk, vv = V.cached(c, b, i + 1)
+        r, oa, top = Y.attend(U.f64(qo[at:at + 1]), i, kk, vv, D ** -0.5)
+        U.within(U.f64(x[None]), r, V.attend_bound(r, oa, top, D, i + 1, BF), f"token {i} of {b}")
+
+
+def test_layer_calls_in_a_graph(bnd):
+    """Rotation, append, attention, convolution and their tree forms, captured once and replayed with other lengths and
+    inputs, with eager work between the replays."""
+    H, Hk, D, n, T = 4, 2, 64, 3, 5
+    c = U.cache(38, n, [0] * n, Hk, D, 16, BF, E4, room=120)
+    args, scales = U.cache_args(c)
+    g = torch.Generator().manual_seed(39)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(BF).cuda()
+    wide, f = rnd(40, H + 2 * Hk, D), torch.rand(D // 2, generator=g).cuda()
+    q, k, v = wide.split([H, Hk, Hk], -2)
+    start, pos, par = V.starts([20, 0, 13]), torch.zeros(n, T, dtype=torch.int32, device="cuda"), U.trees(40, n, T, "chain").cuda()
+    tq, tk = rnd(n, T, H, D), rnd(n, T, Hk, D)
+    xbc, w, state0 = rnd(40, 192), torch.rand(192, 4, generator=g).cuda(), rnd(n, 3, 192)
+    txbc, acc, count = rnd(n, T, 192), torch.arange(T, dtype=torch.int32).repeat(n, 1).cuda(), torch.tensor([2, 0, 5], dtype=torch.int32, device="cuda")
+    out = [torch.zeros(*s, 1, 64, dtype=BF, device="cuda") for s in ((40,), (n, T), (n,)) for _ in range(3)]
+    qo, o, state = torch.zeros(40, H, D, dtype=BF, device="cuda"), torch.zeros(40, H, D, dtype=BF, device="cuda"), state0.clone()
+    tqo, tko = torch.zeros_like(tq), torch.zeros_like(tk)
+
+    def once():
+        bnd.attn_append_rope(q, k, v, start, f, *args, **scales, q_out=qo)
+        bnd.attn_prefill(qo, start, *args, **scales, o=o)
+        bnd.attn_rope(tq, tk, pos, f, q_out=tqo, k_out=tko)
+        bnd.conv_prefill(xbc, w, None, state, start, *out[:3])
+        bnd.conv_verify(txbc, w, None, state, par, *out[3:6])
+        bnd.conv_commit(txbc, state, par, acc, count, 1, 64, 1, 64)
+        bnd.conv_step(txbc[:, 0], w, None, state, *out[6:])
+
+    everything = [qo, o, tqo, tko, state, *out, c["k_scale"], c["v_scale"]]
+    caches = [c["k_cache"].view(torch.uint8), c["v_cache"].view(torch.uint8)]
+    first = [t.clone() for t in everything + caches]
+
+    def fresh(lens, old):
+        for t, t0 in zip(everything + caches, first):
+            t.copy_(t0)
+        start.copy_(V.starts(lens))
+        c["cache_len"].copy_(torch.tensor(old))
+        pos.copy_(torch.tensor(old)[:, None] + torch.arange(T))
+
+    once()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        once()
+    for lens, old in (([20, 0, 13], [0, 5, 90]), ([1, 1, 1], [100, 0, 17]), ([0, 30, 10], [3, 70, 0]), ([20, 0, 13], [0, 5, 90])):
+        fresh(lens, old)
+        once()
+        want = [t.clone() for t in everything + caches]
+        fresh(lens, old)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(everything + caches, want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), lens
