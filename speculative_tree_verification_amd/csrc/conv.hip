@@ -131,12 +131,8 @@ struct Lane {
             y[i] = bias[i];
 #pragma unroll
             for (int k = 0; k < W; ++k) y[i] = fmaf(w[k][i], u[k]->f(i), y[i]);
-            if (a.silu) {
-                if constexpr (sizeof(TIO) == 2)
-                    y[i] *= __builtin_amdgcn_rcpf(1.f + __expf(-y[i]));  // (off by some 2^-22, the result is rounded to 2^-9)
-                else
-                    y[i] = y[i] / (1.f + expf(-y[i]));
-            }
+            // (its quotient off by 2^-22 and |y| 2^-24: below -88 the exponential is infinite, and the result 0)
+            if (a.silu) y[i] *= __builtin_amdgcn_rcpf(1.f + __expf(-y[i]));
         }
         if constexpr (VEC)
             return rounded(y);
@@ -385,8 +381,16 @@ __global__ __launch_bounds__(256) void conv_commit_kernel(ConvArgs a, int chunks
 
 int chunks_of(int HP, int GN, int lane_channels) { return (HP + 2 * GN + kWave * lane_channels - 1) / (kWave * lane_channels); }
 
-int strip_of(int rows, int chunks) { return (long long)rows * chunks >= 65536 ? 32 : 8; }
+// Rows of a strip: some 4000 waves, whose first rows are read twice and whose taps are loaded
+// once each, or as many as there can be (32 packed prompts of an 8B hybrid: 118 us, 144 in
+// strips of 64, 117 of 16; three fp32 prompts of 1360 tokens in all: 7.4 us in strips of 4, 8.0
+// of 8, 9.7 of 16)
+int strip_of(int rows, int chunks) {
+    const long long all = (long long)rows * chunks;
+    return all >= 65536 ? 32 : all >= 32768 ? 16 : all >= 16384 ? 8 : 4;
+}
 
+// Nodes of a wave (16 trees of 31 nodes: 8.6 us with 4, 9.2 with 2, 9.0 with 8)
 int nodes_of(int n, int T, int chunks) { return min(T, (long long)n * T * chunks >= 65536 ? 32 : 4); }
 
 // Waves of a launch
