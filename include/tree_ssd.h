@@ -748,7 +748,8 @@ typedef struct {
  * a negative position are left as they were. q_out [rows][H][D], k_out
  * [rows][Hk][D] contiguous in in_dtype, or q and k themselves where those are
  * contiguous; q or k may be NULL (left out). Of s the batch, n_nodes, heads,
- * head_dim and in_dtype are used.
+ * head_dim and in_dtype are used; the rest is only checked (without a cache
+ * n_pages and max_pages 0, page_size 1, cache_dtype as in_dtype).
  */
 tsv_status tree_attn_rope(const tsv_attn_shape* s, const tsv_rope* r, const void* q, const void* k,
                           const int32_t* position, const float* inv_freq, const float* q_weight, const float* k_weight,
@@ -789,8 +790,16 @@ tsv_status tree_attn_append_rope(const tsv_attn_shape* s, const tsv_rope* r, con
  * tree_attn_prefill_workspace. Every work-group reads all of seq_start and
  * cache_len: thousands of sequences a call are meant, not millions.
  *
- * Arithmetic: fp32 scores, maxima, sums and accumulators. A key or value that
- * is not finite reaches the rows that see its position and no others.
+ * Arithmetic: fp32 scores, maxima, sums and accumulators, one rounding of the
+ * output. head_dim 64 or 128 with 16-byte aligned q, o and caches of fewer than
+ * 2^32 rows of a head runs on matrix instructions: bf16 inputs on bf16 ones,
+ * where the weights, relative to a running maximum, are rounded to bf16 once
+ * (2^-9 of a weight at most), or, where the sequences have no more than 16
+ * (token, query head) rows of a key head on average, taken as two bf16 parts;
+ * fp32 inputs on fp32 ones. All other shapes run in plain fp32. A key or value
+ * that is not finite reaches the rows that see its position and no others; an
+ * infinite value gives an infinity there, unless its weight is 0 in fp32.
+ * o may not overlap the other arguments.
  * TSV_E_SHAPE for a negative window or sinks, and for sinks without a window.
  */
 tsv_status tree_attn_prefill(const tsv_attn_shape* s, int32_t window, int32_t sinks, const void* q,

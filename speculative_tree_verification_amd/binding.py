@@ -1315,7 +1315,7 @@ def attn_rope(q, k, position, inv_freq, q_weight=None, k_weight=None, eps: float
                 raise ValueError(f"{name} is given without {name[0]}")
             _need(o, name, t.shape, io, at)
     code = _dtype_code(given)
-    rope = _rope_struct(R, 1 if interleaved else 0, eps, q_step, k_step, 0)
+    rope = _rope_struct(R, 1 if interleaved else 0, float(eps), q_step, k_step, 0)
     # (one key head for the shape's H % Hk where there are none)
     shape = _attn_shape(1, position.numel(), H or Hk, Hk or 1, D, 0, 1, 0, code, code, 0, 1.0)
 
@@ -1346,7 +1346,7 @@ def attn_append_rope(q, k, v, seq_start, inv_freq, k_cache, v_cache, page_table,
     if q is not None:
         H = q.shape[-2]
         q_step = _need_rows(q, "q", (L,), (H, D), io, at)
-    rope = _rope_struct(_rope_weights(inv_freq, q_weight, k_weight, D, at), 1 if interleaved else 0, eps, q_step,
+    rope = _rope_struct(_rope_weights(inv_freq, q_weight, k_weight, D, at), 1 if interleaved else 0, float(eps), q_step,
                         _need_rows(k, "k", (L,), (Hk, D), io, at), _need_rows(v, "v", (L,), (Hk, D), io, at))
     _need(seq_start, "seq_start", (Bt + 1,), torch.int32, at)
     if seq_status is not None:

@@ -1,7 +1,7 @@
 // api_seq.hip -- extern "C" entry points of the operators around the tree: the
 // prompt scan, the single-token step, the short convolution, the heads' norms and
-// rotation, and the paged cache's attention and writes (declared in include/tree_ssd.h). Host-side validation happens here,
-// before anything is enqueued.
+// rotation, and the paged cache's attention and writes (declared in
+// include/tree_ssd.h). Host-side validation happens here, before anything is enqueued.
 #include <math.h>
 
 #include "attn_common.hpp"
