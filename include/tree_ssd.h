@@ -794,7 +794,7 @@ tsv_status tree_attn_append_rope(const tsv_attn_shape* s, const tsv_rope* r, con
  * output. head_dim 64 or 128 with 16-byte aligned q, o and caches of fewer than
  * 2^32 rows of a head runs on matrix instructions: bf16 inputs on bf16 ones,
  * where the weights, relative to a running maximum, are rounded to bf16 once
- * (2^-9 of a weight at most), or, where the sequences have no more than 16
+ * (2^-8 of a weight at most), or, where the sequences have no more than 16
  * (token, query head) rows of a key head on average, taken as two bf16 parts;
  * fp32 inputs on fp32 ones. All other shapes run in plain fp32. A key or value
  * that is not finite reaches the rows that see its position and no others; an

@@ -197,7 +197,11 @@ __device__ __forceinline__ uint32_t max_of(uint32_t v) {
 template <int ROWS>
 struct RowPlaces {
     long long dst[ROWS];
-    int item[ROWS], pos[ROWS], len[ROWS], count[ROWS], place[ROWS], bad[ROWS], is_long[ROWS], red[4];
+    int place[ROWS];
+    // of the rows with which a sequence begins or goes on here: bits of `leads`
+    int item[ROWS], pos[ROWS], len[ROWS], count[ROWS], bad[ROWS], is_long[ROWS];
+    uint32_t leads;
+    int red[4];
 };
 
 // False: nothing to write for this work-group. With status_of >= 0 it writes the status of
@@ -205,22 +209,22 @@ struct RowPlaces {
 // that loads from before it stay in flight).
 template <int ROWS>
 __device__ __forceinline__ bool find_places(const CacheWriteArgs& a, int r0, int n, int status_of, RowPlaces<ROWS>& s) {
+    static_assert(ROWS <= 32, "a bit for each row");
     const int tid = threadIdx.x;
-    if (tid < ROWS) {
-        s.pos[tid] = -1;
-        s.item[tid] = s.bad[tid] = s.is_long[tid] = 0;
-    }
+    if (tid < ROWS) s.bad[tid] = s.is_long[tid] = 0;
+    if (tid == 0) s.leads = 0;
     lds_barrier();
-    // the thread of a sequence that has rows here writes what the rows need of it
+    // the thread of a sequence that has rows here writes what they need of it
     int bad = 0;
     for (int q = tid; q < a.batch; q += 256) {
-        const int lo = a.seq_start[q], hi = a.seq_start[q + 1], len = a.cache_len[q];
+        const int lo = a.seq_start[q], hi = a.seq_start[q + 1], len = a.cache_len[q], r = max(lo, r0);
         bad |= lo < 0 || hi < lo || hi > a.T;
-        for (int r = max(lo, r0); r < min(hi, r0 + n); ++r) {
+        if (r < min(hi, r0 + n)) {
             s.item[r - r0] = q;
             s.pos[r - r0] = r - lo;
             s.len[r - r0] = len;
             s.count[r - r0] = hi - lo;
+            atomicOr(&s.leads, 1u << (r - r0));
         }
     }
     bad = lds_sync_or<256>(bad, s.red);
@@ -232,25 +236,28 @@ __device__ __forceinline__ bool find_places(const CacheWriteArgs& a, int r0, int
     }
     if (bad) return false;
     // a row's page, where its sequence fits the table
-    int page = 0, place = -1, pg = 0, first, last;
-    if (tid < n && s.pos[tid] >= 0 && page_range(a, s.len[tid], s.count[tid], &first, &last)) {
-        place = s.len[tid] + s.pos[tid];
-        page = page_of(place, a.div);
-        pg = a.page_table[(size_t)s.item[tid] * a.max_pages + page];
+    int lead = 0, page = 0, place = -1, pg = 0, first, last;
+    if (const uint32_t before = tid < n ? s.leads & ((2u << tid) - 1) : 0) {
+        lead = 31 - __builtin_clz(before);
+        const int at = s.pos[lead] + tid - lead;
+        if (at < s.count[lead] && page_range(a, s.len[lead], s.count[lead], &first, &last)) {
+            place = s.len[lead] + at;
+            page = page_of(place, a.div);
+            pg = a.page_table[(size_t)s.item[lead] * a.max_pages + page];
+        }
     }
     // the sequences that begin or go on in these rows: 16 threads each, all at once
     // (16 short prompts one after another took 30 us), and then all threads for
     // each of the few that have many pages
     {
         constexpr int kLong = 64;
-        const int i = tid / (256 / ROWS), b = s.item[i];
-        const bool leads = i < n && s.pos[i] >= 0 && (i == 0 || s.pos[i - 1] < 0 || s.item[i - 1] != b);
-        if (leads) {
+        const int i = tid / (256 / ROWS);
+        if (s.leads >> i & 1) {
             if (!page_range(a, s.len[i], s.count[i], &first, &last))
                 s.bad[i] = 1;
             else if (last - first >= kLong)
                 s.is_long[i] = 1;
-            else if (pages_bad(a, b, first + tid % (256 / ROWS), last, 256 / ROWS))
+            else if (pages_bad(a, s.item[i], first + tid % (256 / ROWS), last, 256 / ROWS))
                 s.bad[i] = 1;
         }
         lds_barrier();
@@ -262,9 +269,7 @@ __device__ __forceinline__ bool find_places(const CacheWriteArgs& a, int r0, int
         }
     }
     if (tid < n) {
-        int j = tid;  // the first of this sequence's rows here
-        while (j > 0 && s.pos[j] >= 0 && s.item[j - 1] == s.item[tid] && s.pos[j - 1] >= 0) --j;
-        if (s.bad[j]) place = -1;
+        if (s.bad[lead]) place = -1;
         s.place[tid] = place;
         s.dst[tid] = place >= 0 ? (long long)pg * a.Hk * a.page_size + (place - page * a.page_size) : -1;
     }
