@@ -323,7 +323,7 @@ tsv_status tree_attn_rope(const tsv_attn_shape* s, const tsv_rope* r, const void
     if (st == TSV_OK) st = check_rope(s, r);
     if (st != TSV_OK) return st;
     const long long rows = (long long)s->batch * s->n_nodes;
-    if (rows > kMaxRows || tsv::rope_blocks((int)rows, 0) > kMaxBlocks) return TSV_E_UNSUPPORTED;
+    if (rows > kMaxRows || tsv::rope_blocks((int)rows, false, 0) > kMaxBlocks) return TSV_E_UNSUPPORTED;
     if (rows == 0) return TSV_OK;
     if ((!q && !k) || (q && !q_out) || (k && !k_out) || !position || (r->rot_dim > 0 && !inv_freq)) return TSV_E_NULL;
     if ((q && !stride_ok(r->q_stride, s->n_heads, s->head_dim)) || (k && !stride_ok(r->k_stride, s->n_kv_heads, s->head_dim)))
@@ -341,7 +341,7 @@ tsv_status tree_attn_append_rope(const tsv_attn_shape* s, const tsv_rope* r, con
     tsv_status st = check_attn(s, false);
     if (st == TSV_OK) st = check_rope(s, r);
     if (st != TSV_OK) return st;
-    if (s->n_nodes > kMaxRows || s->batch > kMaxRows || tsv::rope_blocks(s->n_nodes, s->batch) > kMaxBlocks) return TSV_E_UNSUPPORTED;
+    if (s->n_nodes > kMaxRows || s->batch > kMaxRows || tsv::rope_blocks(s->n_nodes, true, s->batch) > kMaxBlocks) return TSV_E_UNSUPPORTED;
     if (s->batch == 0) return TSV_OK;
     if (!seq_start || !cache_len || (r->rot_dim > 0 && !inv_freq)) return TSV_E_NULL;
     if (s->n_nodes > 0 && (!k || !v || (q && !q_out))) return TSV_E_NULL;

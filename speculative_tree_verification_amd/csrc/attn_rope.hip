@@ -7,18 +7,24 @@
 // for the R / 2 pairs (a, b) = (i, i + R/2), or (2 i, 2 i + 1), of a head; the other
 // elements stay z.
 //
-// Bound by the rows' traffic. A lane has eight pairs of a head, so that both elements of a
-// pair are its own and only the sum of squares leaves it: a head of D has D / 16 lanes
-// (rounded up to a power of two), two 16-byte pieces each in bf16. The angles of a row are
-// the same for all of its heads: the work-group forms them once, in LDS. An angle is a
-// product in 64 bits, in revolutions, of which the whole ones are dropped before it is
-// rounded to 32: at position 10^6 a product in 32 bits would be off by 0.06.
+// Bound by the rows' traffic, and in 8 bits by the vector unit beside it: 32 trees of 63 nodes,
+// 32 query and 8 key heads of 128 in bf16, 41 MB, 9.7 us in the kernel (12.6 a call, the host's
+// time); 16 prompts of 1 to 2047 tokens into an e4m3 cache, 370 MB, 80.1 us (4.6 TB/s; a large
+// copy reaches 5.1); one token 3.8 us.
+//
+// A lane has eight pairs of a head, so that both elements of a pair are its own and only the
+// sum of squares leaves it: a head of D has D / 16 lanes (rounded up to a power of two), two
+// 16-byte pieces each in bf16, with the next head's on their way (two heads ahead gained
+// nothing). The angles of a row are the same for all of its heads: the work-group forms them
+// once, in LDS. An angle is a product in 64 bits, in revolutions, of which the whole ones are
+// dropped before it is rounded to 32: at position 10^6 a product in 32 bits would be off by
+// 0.06.
 #include "attn_cache.hpp"
 
 namespace tsv {
 namespace {
 
-constexpr int kRopeRows = 16;  // most rows of a work-group
+constexpr int kRopeRows = 4;  // most rows of a work-group
 
 // How a lane has its eight pairs:
 //   kHalves       pairs 8 j + i of (i, i + R / 2), as two pieces of eight neighbours; past the
@@ -264,6 +270,13 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, CacheWriteArgs c,
     }
 }
 
+// One row each while there are few, so that all compute units have one; of many, the weights' way
+// into LDS and the search for the rows' sequences are paid by four (one row a work-group and four,
+// in the kernel: 64 rows into the cache 6.4 and 9.6 us, 1024 rows 9.4 and 11.3, 2048 rows 14.9 and
+// 13.8, 16000 rows 106 and 85; without a cache 992 rows 6.7 and 8.8, 2016 rows 9.7 and 10.9, 8160
+// rows 29.2 and 27.7)
+int rope_rows(int rows, bool append) { return rows <= (append ? 1024 : 2048) ? 1 : kRopeRows; }
+
 template <typename TIO, int LPH, Pairing P>
 void launch_one(const RopeArgs& a, const CacheWriteArgs* c, bool e4m3, int rb, int blocks, int all, hipStream_t stream) {
     if (!c)
@@ -286,7 +299,8 @@ void launch_pairing(const RopeArgs& a, const CacheWriteArgs* c, bool e4m3, int r
 
 template <typename TIO>
 hipError_t launch_type(const RopeArgs& a, const CacheWriteArgs* c, bool e4m3, hipStream_t stream) {
-    const int rb = rope_rows(a.rows), blocks = (int)rope_blocks(a.rows, 0), all = (int)rope_blocks(a.rows, c && c->status ? c->batch : 0);
+    const int rb = rope_rows(a.rows, c != nullptr), blocks = (int)rope_blocks(a.rows, c != nullptr, 0);
+    const int all = blocks + (c && c->status ? c->batch : 0);
     if (all == 0) return hipSuccess;
     // eight elements at a time where heads, strides and pointers allow it
     uintptr_t bits = (uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.q_out | (uintptr_t)a.k_out;
@@ -304,8 +318,7 @@ hipError_t launch_type(const RopeArgs& a, const CacheWriteArgs* c, bool e4m3, hi
 
 }  // namespace
 
-int rope_rows(int rows) { return rows <= 1024 ? 1 : rows <= 8192 ? 4 : kRopeRows; }
-long long rope_blocks(int rows, int items) { return ((long long)rows + rope_rows(rows) - 1) / rope_rows(rows) + items; }
+long long rope_blocks(int rows, bool append, int items) { return ((long long)rows + rope_rows(rows, append) - 1) / rope_rows(rows, append) + items; }
 
 hipError_t launch_rope(const RopeArgs& a, const CacheWriteArgs* c, bool bf16, bool e4m3, hipStream_t stream) {
     return bf16 ? launch_type<uint16_t>(a, c, e4m3, stream) : launch_type<float>(a, c, e4m3, stream);

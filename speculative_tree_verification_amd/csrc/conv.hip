@@ -7,7 +7,8 @@
 // one on, and t - k is node t's k-th ancestor in a tree.
 //
 // Bound by the rows' traffic: every input is read once and every output written once for
-// 2 W operations. A lane has 16 bytes of neighbouring channels, whose taps stay in
+// 2 W operations (32 prompts of 1 to 1531 tokens, 5120 channels in bf16, 504 MB: 118 us, 4.3
+// TB/s; a large copy reaches 5.1). A lane has 16 bytes of neighbouring channels, whose taps stay in
 // registers; a wave goes down a strip of a sequence's rows with the last W - 1 of them in
 // registers, so that only a strip's first rows are read twice. Waves work by themselves
 // (no barrier): each finds its sequence from seq_start. A sequence's first strip alone
@@ -390,7 +391,8 @@ int strip_of(int rows, int chunks) {
     return all >= 65536 ? 32 : all >= 32768 ? 16 : all >= 16384 ? 8 : 4;
 }
 
-// Nodes of a wave (16 trees of 31 nodes: 8.6 us with 4, 9.2 with 2, 9.0 with 8)
+// Nodes of a wave (16 trees of 31 nodes, 5376 channels, 11 MB: 8.6 us in the kernel with 4, 9.2
+// with 2, 9.0 with 8: the latency of the launch, the parents, the taps and the inputs)
 int nodes_of(int n, int T, int chunks) { return min(T, (long long)n * T * chunks >= 65536 ? 32 : 4); }
 
 // Waves of a launch

@@ -84,8 +84,7 @@ struct RopeArgs {
     float eps;
     PageDiv heads, key_heads;  // by a row's heads of q and k, and by those of k
 };
-int rope_rows(int rows);                        // rows of a work-group
-long long rope_blocks(int rows, int items);     // work-groups, with the items' status
+long long rope_blocks(int rows, bool append, int items);  // work-groups, with the items' status
 // c: into the cache; NULL: to k_out
 hipError_t launch_rope(const RopeArgs& a, const CacheWriteArgs* c, bool bf16, bool e4m3, hipStream_t stream);
 

@@ -116,9 +116,8 @@ def test_grids_past_32_bits_of_threads_are_refused():
     assert conv_prefill(seq(n_seqs=2 ** 30, n_tokens=2 ** 30, **one), c) == UNSUPPORTED
     assert rope(attn(batch=1, n_nodes=2 ** 31 - 1), rot()) == UNSUPPORTED
     assert rope(attn(batch=2 ** 16, n_nodes=2 ** 16), rot()) == UNSUPPORTED
-    # (16 rows a work-group)
-    assert rope(attn(batch=1, n_nodes=16 * MOST + 1), rot()) == UNSUPPORTED
-    assert append(attn(n_nodes=16 * MOST + 1), rot()) == UNSUPPORTED
+    assert rope(attn(batch=1, n_nodes=4 * MOST + 1), rot()) == UNSUPPORTED
+    assert append(attn(n_nodes=4 * MOST + 1), rot()) == UNSUPPORTED
     assert append(attn(batch=MOST, n_nodes=64), rot()) == UNSUPPORTED
     assert chunk(attn(n_nodes=2 ** 31 - 1)) == UNSUPPORTED
     assert chunk(attn(batch=MOST, n_nodes=MOST, n_heads=8, n_kv_heads=8)) == UNSUPPORTED
