@@ -391,9 +391,14 @@ int strip_of(int rows, int chunks) {
     return all >= 65536 ? 32 : all >= 32768 ? 16 : all >= 16384 ? 8 : 4;
 }
 
-// Nodes of a wave (16 trees of 31 nodes, 5376 channels, 11 MB: 8.6 us in the kernel with 4, 9.2
-// with 2, 9.0 with 8: the latency of the launch, the parents, the taps and the inputs)
-int nodes_of(int n, int T, int chunks) { return min(T, (long long)n * T * chunks >= 65536 ? 32 : 4); }
+// Nodes of a wave, in the kernel with 4, 8 and 32 of them (us; 5376 or 5120 channels): 16 trees of 31
+// nodes 8.4, 8.8, 20 (the latency of the launch, the parents, the taps and the inputs), 8 of 255
+// 17.8, 15.7, 22, 64 of 63 27.8, 26, 33, 64 of 255 135, 114, 103 (336 MB; every input comes W times,
+// from the L2 after the first)
+int nodes_of(int n, int T, int chunks) {
+    const long long all = (long long)n * T * chunks;
+    return min(T, all >= 65536 ? 32 : all >= 16384 ? 8 : 4);
+}
 
 // Waves of a launch
 long long units_of(ConvKind kind, int n, int rows, int chunks) {
