@@ -17,7 +17,12 @@
 namespace tsv {
 
 struct ChunkPlan {
-    int rows;      // rows of a block
+    int rows;      // rows of a block, a power of two
+    int shift;     // its logarithm
+    int g;         // rows of a token
+    int tokens;    // most of a block
+    PageDiv by_g;  // n / g
+    float share;   // above Hk / want, by more than the sum of the work is rounded
     int want;      // work-groups wanted
     int min_keys;  // smallest part
     bool split;    // whether a block may have more than one part
@@ -85,11 +90,24 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkArgs& a, const ChunkPla
     s.n = hi - lo;
     s.fits = s.old >= 0 && s.old <= a.room && s.n <= a.room - s.old;
     if (!s.fits || s.n == 0) return s;
-    const int g = a.H / a.Hk;
-    s.blocks = (s.n * g + plan.rows - 1) / plan.rows;
-    const int tokens = min(s.n, (plan.rows + g - 2) / g + 1);  // of a block
-    s.longest = (int)min((long long)s.old + s.n, (long long)a.window + tokens - 1 + a.sinks);
+    s.blocks = (s.n * plan.g + plan.rows - 1) >> plan.shift;
+    s.longest = (int)min((long long)s.old + s.n, (long long)a.window + min(s.n, plan.tokens) - 1 + a.sinks);
     return s;
+}
+
+// Sums over the lanes up to this one
+template <typename T>
+__device__ __forceinline__ T lanes_before(T v) {
+    static_assert(sizeof(T) == 4, "a word of a lane");
+#define TSV_ADD_DPP(ctrl, rows) v += __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl, rows, 0xf, false))
+    TSV_ADD_DPP(0x111, 0xf);  // row_shr:1, of 16 lanes
+    TSV_ADD_DPP(0x112, 0xf);
+    TSV_ADD_DPP(0x114, 0xf);
+    TSV_ADD_DPP(0x118, 0xf);
+    TSV_ADD_DPP(0x142, 0xa);  // row_bcast:15, into the second and fourth row
+    TSV_ADD_DPP(0x143, 0xc);  // row_bcast:31, into the upper half
+#undef TSV_ADD_DPP
+    return v;
 }
 
 // The unit whose turn is `want`, or with JOIN the cut block whose turn it is. The same in
@@ -110,25 +128,17 @@ __device__ __forceinline__ ChunkUnit find_unit(const ChunkArgs& a, const ChunkPl
     if (u.bad) return u;
     int keys = 0x7fffffc0;  // above any length
     if (plan.split) {
-#pragma unroll
-        for (int m = 1; m < kWave; m <<= 1) work += __shfl_xor(work, m, kWave);
-        const unsigned long long per = (work * a.Hk + plan.want - 1) / plan.want;
-        keys = max((int)min((per + 63) / 64 * 64, 0x7fffffc0ull), plan.min_keys);
+        // (rounded to 24 bits once and in six sums: `share` has 2^-20 more)
+        const int total = __builtin_amdgcn_readlane(__float_as_int(lanes_before((float)work)), kWave - 1);
+        const int per = (int)fminf(__int_as_float(total) * plan.share + 1.f, 2147483520.f);
+        keys = max((per + 63) / 64 * 64, plan.min_keys);
     }
     int run = 0, slots = 0;
     for (int q0 = 0; q0 < a.batch; q0 += kWave) {
         if (q0) s = chunk_seq(a, plan, q0 + lane);
         const int parts = s.blocks ? (int)(((uint32_t)s.longest + keys - 1) / keys) : 0;
         const int cut = parts > 1 ? s.blocks * parts : 0, cnt = JOIN ? (parts > 1 ? s.blocks : 0) : s.blocks * parts;
-        int upto = cnt, cuts = cut;
-#pragma unroll
-        for (int m = 1; m < kWave; m <<= 1) {
-            const int x = __shfl_up(upto, m, kWave), y = __shfl_up(cuts, m, kWave);
-            if (lane >= m) {
-                upto += x;
-                cuts += y;
-            }
-        }
+        const int upto = lanes_before(cnt), cuts = lanes_before(cut);
         const int at = want - run;
         int from = upto - cnt;
         if (!JOIN && plan.sorted) {
@@ -149,8 +159,9 @@ __device__ __forceinline__ ChunkUnit find_unit(const ChunkArgs& a, const ChunkPl
             u.old = __builtin_amdgcn_readlane(s.old, src);
             u.parts = __builtin_amdgcn_readlane(parts, src);
             const int blocks = __builtin_amdgcn_readlane(s.blocks, src);
-            u.block = blocks - 1 - (JOIN ? turn : turn / u.parts);
-            u.part = JOIN ? 0 : turn % u.parts;
+            const int done = JOIN || u.parts == 1 ? turn : turn / u.parts;
+            u.block = blocks - 1 - done;
+            u.part = JOIN ? 0 : turn - done * u.parts;
             u.slot = slots + __builtin_amdgcn_readlane(cuts - cut, src) + (JOIN ? turn * u.parts : turn);
             u.lead = turn == 0;
             return u;
@@ -167,13 +178,13 @@ struct ChunkKeys {
     int k0, k1;  // this part's virtual positions
 };
 __device__ __forceinline__ ChunkKeys chunk_keys(const ChunkArgs& a, const ChunkPlan& plan, const ChunkUnit& u) {
-    const int g = a.H / a.Hk, row0 = u.block * plan.rows, row1 = min(u.n * g, row0 + plan.rows) - 1;
+    const int row0 = u.block * plan.rows, row1 = min(u.n * plan.g, row0 + plan.rows) - 1;
     ChunkKeys k;
-    const int hi = u.old + row1 / g + 1;
-    k.lo = (int)max(0LL, (long long)u.old + row0 / g - a.window + 1);
+    const int hi = u.old + page_of(row1, plan.by_g) + 1;
+    k.lo = (int)max(0LL, (long long)u.old + page_of(row0, plan.by_g) - a.window + 1);
     k.sinks = min(a.sinks, k.lo);
     k.keys = k.sinks + hi - k.lo;
-    const int per = ((k.keys + u.parts - 1) / u.parts + 63) / 64 * 64;
+    const int per = u.parts == 1 ? k.keys : ((k.keys + u.parts - 1) / u.parts + 63) / 64 * 64;
     k.k0 = (int)min((long long)u.part * per, (long long)k.keys);
     k.k1 = (int)min((long long)k.k0 + per, (long long)k.keys);
     return k;

@@ -48,13 +48,13 @@ __global__ __launch_bounds__(256, 2) void chunk_f32_kernel(ChunkArgs a, ChunkPla
     if (blockIdx.x == 0 && w == 0) chunk_status(a, plan, u.bad);
     if (!u.ok) return;
     const ChunkKeys kk = chunk_keys(a, plan, u);
-    const int H = a.H, g = H / a.Hk, R = u.n * g, row0 = u.block * M;
+    const int H = a.H, g = plan.g, R = u.n * g, row0 = u.block * M;
     const int32_t* table = a.page_table + (size_t)u.seq * a.max_pages;
 
     // this lane's row
-    const int row = min(row0 + 16 * wr + l16, R - 1), token = row / g, own = u.old + token;
+    const int row = min(row0 + 16 * wr + l16, R - 1), token = page_of(row, plan.by_g), own = u.old + token;
     const size_t at = ((size_t)u.start + token) * H + hk * g + (row - token * g);  // in q and o
-    const int own_min = u.old + row0 / g, own_max = u.old + (min(R, row0 + M) - 1) / g;
+    const int own_min = u.old + page_of(row0, plan.by_g), own_max = u.old + page_of(min(R, row0 + M) - 1, plan.by_g);
     const bool active = row0 + 16 * wr < R;
     float4 q[D / 16];
     {
@@ -283,7 +283,7 @@ __global__ __launch_bounds__(256, 2) void chunk_f32_kernel(ChunkArgs a, ChunkPla
                     ws.ml[slot * 2 + 1] = sum;
                 }
             } else {
-                const int tk = (row0 + r) / g;
+                const int tk = page_of(row0 + r, plan.by_g);
                 gstore((float4*)((float*)a.o + (((size_t)u.start + tk) * H + hk * g + (row0 + r - tk * g)) * D + d),
                        make_float4(v.x / sum, v.y / sum, v.z / sum, v.w / sum));
             }

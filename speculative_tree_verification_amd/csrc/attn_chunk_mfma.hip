@@ -63,12 +63,12 @@ __global__ __launch_bounds__(256, 3) void chunk_rows_kernel(ChunkArgs a, ChunkPl
     if (blockIdx.x == 0 && w == 0) chunk_status(a, plan, u.bad);
     if (!u.ok) return;
     const ChunkKeys kk = chunk_keys(a, plan, u);
-    const int H = a.H, g = H / a.Hk, R = u.n * g, row0 = u.block * M;
+    const int H = a.H, g = plan.g, R = u.n * g, row0 = u.block * M;
     const int32_t* table = a.page_table + (size_t)u.seq * a.max_pages;
 
     // this lane's row: k-slot e of step 2 j + h is d = 64 j + 16 lg + 8 h + e
-    const int row = min(row0 + l16, R - 1), token = row / g, own = u.old + token;
-    const int own_min = u.old + row0 / g, own_max = u.old + (min(R, row0 + M) - 1) / g;
+    const int row = min(row0 + l16, R - 1), token = page_of(row, plan.by_g), own = u.old + token;
+    const int own_min = u.old + page_of(row0, plan.by_g), own_max = u.old + page_of(min(R, row0 + M) - 1, plan.by_g);
     bf16x8 q[ND];
     {
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(256, 3) void chunk_rows_kernel(ChunkArgs a, ChunkPl
             }
         } else {
             const float lr = s_l[r];
-            const int tk = (row0 + r) / g;
+            const int tk = page_of(row0 + r, plan.by_g);
             gstore((uint2*)((uint16_t*)a.o + (((size_t)u.start + tk) * H + hk * g + (row0 + r - tk * g)) * D + d),
                    make_uint2(pack_bf16x2(v[0] / lr, v[1] / lr), pack_bf16x2(v[2] / lr, v[3] / lr)));
         }
@@ -347,13 +347,13 @@ __global__ __launch_bounds__(256, ND == 2 ? 3 : 2) void chunk_tiles_kernel(Chunk
     if (!u.ok) return;
     if (chunk_check<256>(a, u, hk, ws)) return;
     const ChunkKeys kk = chunk_keys(a, plan, u);
-    const int H = a.H, g = H / a.Hk, R = u.n * g, row0 = u.block * M;
+    const int H = a.H, g = plan.g, R = u.n * g, row0 = u.block * M;
     const int32_t* table = a.page_table + (size_t)u.seq * a.max_pages;
     const int n = (kk.k1 - kk.k0 + kSub - 1) / kSub;  // steps
     const bool active = row0 + 32 * w < R;
 
     // this lane's rows: their positions and queries (with the sign of the scores' factor)
-    const int row = min(row0 + 32 * w + lr, R - 1), token = row / g, own = u.old + token;
+    const int row = min(row0 + 32 * w + lr, R - 1), token = page_of(row, plan.by_g), own = u.old + token;
     const size_t at = ((size_t)u.start + token) * H + hk * g + (row - token * g);  // in q and o
     bf16x8 q[NK];
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
@@ -362,7 +362,7 @@ __global__ __launch_bounds__(256, ND == 2 ? 3 : 2) void chunk_tiles_kernel(Chunk
         const uint4 v = gload((const uint4*)((const uint16_t*)a.q + at * D + 8 * lg + 16 * i));
         q[i] = as_operand(make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip));
     }
-    const int own_min = u.old + row0 / g, own_max = u.old + (min(R, row0 + M) - 1) / g;
+    const int own_min = u.old + page_of(row0, plan.by_g), own_max = u.old + page_of(min(R, row0 + M) - 1, plan.by_g);
     const float c = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);  // (0 becomes the smallest normal: a masked score of -inf stays one)
 
     // The steps whose keys every row of the block sees: those of the sinks, and [whole0, whole1)

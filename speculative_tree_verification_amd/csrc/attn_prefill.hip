@@ -39,7 +39,7 @@ __global__ __launch_bounds__(256) void chunk_plain_kernel(ChunkArgs a, ChunkPlan
     if (!u.ok) return;
     if (chunk_check<256>(a, u, hk, ws)) return;
     const ChunkKeys kk = chunk_keys(a, plan, u);
-    const int D = a.D, g = a.H / a.Hk, R = u.n * g, row0 = u.block * kRows;
+    const int D = a.D, g = plan.g, R = u.n * g, row0 = u.block * kRows;
     for (int i = tid; i < kRows * D; i += 256) {
         const int r = row0 + i / D;
         s_q[i / D][i % D] = r < R ? Elem<TIO>::ld((const TIO*)a.q, (((size_t)u.start + r / g) * a.H + hk * g + r % g) * D + i % D) : 0.f;
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(256) void chunk_join_kernel(ChunkArgs a, ChunkPlan 
     const int tid = threadIdx.x, unit = blockIdx.x / groups, hk = unit % a.Hk, grp = tid / LPR, d = tid % LPR * 4;
     const ChunkUnit u = find_unit<true>(a, plan, unit / a.Hk);
     if (!u.ok || ws.bad[(size_t)u.slot * a.Hk + hk]) return;
-    const int D = a.D, g = a.H / a.Hk, row0 = u.block * plan.rows, rows = min(u.n * g - row0, plan.rows);
+    const int D = a.D, g = plan.g, row0 = u.block * plan.rows, rows = min(u.n * g - row0, plan.rows);
     int share = 1;  // groups of a row
     while (2 * share * min(per, rows) <= kAt) share *= 2;
     const int first = blockIdx.x % groups * per;
@@ -243,8 +243,8 @@ __global__ __launch_bounds__(256) void chunk_join_kernel(ChunkArgs a, ChunkPlan 
             }
         }
         if (d >= D || grp % share || r0 + grp / share >= min(rows, first + per)) continue;
-        const int row = row0 + r;
-        TIO* to = (TIO*)a.o + (((size_t)u.start + row / g) * a.H + hk * g + row % g) * D + d;
+        const int row = row0 + r, token = page_of(row, plan.by_g);
+        TIO* to = (TIO*)a.o + (((size_t)u.start + token) * a.H + hk * g + (row - token * g)) * D + d;
         const float f[4] = {o.x / l, o.y / l, o.z / l, o.w / l};
         if (whole) {
             if constexpr (sizeof(TIO) == 4)
@@ -320,6 +320,11 @@ ChunkPlan plan_of(const tsv_attn_shape* s, bool matrix, int window, int sinks) {
     p.rows = !matrix ? kRows : rows <= 16LL * s->batch ? 16 : s->in_dtype == TSV_F32 ? 64 : 128;
     p.want = !matrix ? 1024 : p.rows > 16 || x <= 128 ? 512 : x >= 512 ? 2048 : (int)(4 * x);
     p.min_keys = 256;
+    for (p.shift = 0; 1 << p.shift < p.rows;) ++p.shift;
+    p.g = g;
+    p.by_g = page_div(g);
+    p.tokens = (p.rows + g - 2) / g + 1;
+    p.share = (float)s->n_kv_heads / (float)p.want * (1.f + 0x1p-20f);
     const long long blocks = rows / p.rows > items ? rows / p.rows : items;
     long long longest = (long long)s->max_pages * s->page_size;
     if (window > 0 && longest > (long long)window + sinks + p.rows) longest = (long long)window + sinks + p.rows;
