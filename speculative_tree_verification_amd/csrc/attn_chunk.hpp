@@ -192,6 +192,19 @@ __device__ __forceinline__ ChunkKeys chunk_keys(const ChunkArgs& a, const ChunkP
 // Position of virtual position v
 __device__ __forceinline__ int chunk_pos(const ChunkKeys& k, int v) { return v < k.sinks ? v : v - k.sinks + k.lo; }
 
+// The virtual positions v that the row at position `own` sees: v < hi and (v >= lo or v < a.sinks).
+// (The sinks' own, below k.sinks, all rows see, and a.sinks is k.sinks unless the sinks go on
+// behind k.lo, where virtual positions are positions.)
+struct ChunkSeen {
+    int lo, hi;
+};
+__device__ __forceinline__ ChunkSeen chunk_seen(const ChunkArgs& a, const ChunkKeys& k, int own) {
+    ChunkSeen s;
+    s.lo = max(0, own - a.window + 1 - k.lo + k.sinks);
+    s.hi = min(k.k1, own - k.lo + k.sinks + 1);
+    return s;
+}
+
 // Whether some page that the sequence's rows use is none of the pool's: threads of a
 // work-group of NT look at different ones.
 template <int NT>

@@ -71,7 +71,8 @@ __global__ __launch_bounds__(256, 2) void chunk_f32_kernel(ChunkArgs a, ChunkPla
     f32x4 o[D / 16];
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto sees = [&](int pos) { return pos <= own && (own - pos < a.window || pos < a.sinks); };
+    const ChunkSeen seen = chunk_seen(a, kk, own);
+    auto sees = [&](int v) { return v < seen.hi && (v >= seen.lo || v < a.sinks); };  // virtual position v
 
     // One tile of keys in LDS, from virtual position t on
     auto take = [&](int t, bool whole) {
@@ -94,7 +95,7 @@ __global__ __launch_bounds__(256, 2) void chunk_f32_kernel(ChunkArgs a, ChunkPla
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int v = t + 16 * (x + wk) + 4 * lg + r;
-                    s[x][r] = v < kk.k1 && sees(chunk_pos(kk, v)) ? s[x][r] : -INFINITY;
+                    s[x][r] = sees(v) ? s[x][r] : -INFINITY;
                 }
         }
         float mx = max3(max3(s[0][0], s[0][1], s[0][2]), s[0][3], s[0][3]);
@@ -143,12 +144,12 @@ __global__ __launch_bounds__(256, 2) void chunk_f32_kernel(ChunkArgs a, ChunkPla
                 const int key = 32 * half + __builtin_ctz(left), pos = chunk_pos(kk, t + key), page = page_of(pos, a.div);
                 if (WK == 4 && key / 16 != wk) continue;
                 const size_t row = ((size_t)table[page] * a.Hk + hk) * a.page_size + (pos - page * a.page_size);
-                const bool seen = sees(pos);
+                const bool here = sees(t + key);
 #pragma unroll
                 for (int i = 0; i < D / 4; ++i) {
                     const size_t d = row * D + 64 * (i / 16) + 16 * lg + i % 16;
                     const float f = E4M3 ? e4m3_ld((const uint8_t*)a.v_cache + d) : gload((const float*)a.v_cache + d);
-                    if (seen && odd_value(f)) o[4 * (i / 16) + i % 4][i % 16 / 4] += f;
+                    if (here && odd_value(f)) o[4 * (i / 16) + i % 4][i % 16 / 4] += f;
                     if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
                 }
             }
