@@ -13,10 +13,10 @@
 // same 16 rows, a quarter of the keys each, which meet at the end.
 //
 // Many rows are bound by the fp32 matrix unit, which waits for LDS and the softmax of its own
-// step: 2 chunks of 500 tokens behind 1000 positions, 32 query and 8 key heads of 128, 228 us
-// (90 TFLOP/s; a large fp32 product reaches 154); 3 prompts of 130 to 777 tokens in a window of
-// 255, 24 and 3 heads of 64, 34.6 us, the unit busy in 45% of the cycles. Few rows are bound by
-// the cache's bytes: 32 tokens over 2200 positions, 578 MB, 121 us (4.8 TB/s). Weights stay in fp32.
+// step: 2 chunks of 500 tokens behind 1000 positions, 32 query and 8 key heads of 128, 230 us
+// (89 TFLOP/s; a large fp32 product reaches 154); 3 prompts of 130 to 777 tokens in a window of
+// 255, 24 and 3 heads of 64, 32.4 us, the unit busy in 40% of the cycles. Few rows are bound by
+// the cache's bytes: 32 tokens over 2200 positions, 578 MB, 118 us (4.9 TB/s). Weights stay in fp32.
 #include <cfloat>
 
 #include "attn_chunk.hpp"
@@ -196,7 +196,7 @@ __global__ __launch_bounds__(256, 2) void chunk_f32_kernel(ChunkArgs a, ChunkPla
         }
     };
     // the pages are checked while the queries and the first keys' pages are on their way (the
-    // three windowed prompts above: 35.1 us with the check first)
+    // three windowed prompts above: 34.6 us, 35.1 with the check first)
     look_up(kk.k0);
     if (chunk_check<256>(a, u, hk, ws)) return;
     if (kk.k1 > kk.k0) {

@@ -47,8 +47,8 @@ __device__ __forceinline__ uint32_t chunk_row(const ChunkArgs& a, int page, int 
 // each in turn and meet at the end; K goes from memory into the operand registers, V through
 // LDS. The weights enter the product with V as two bf16 parts: free here, since the kernel
 // is bound by the cache's bytes (32 query and 8 key heads of 128: one token over 65532
-// positions, 268 MB, 54.5 us with the join, 4.9 TB/s; 64 tokens with windows of 1021, 251 MB,
-// 51.6 us; 64 over e4m3 caches of up to 8190 positions 124 us, 4.5 TB/s).
+// positions, 268 MB, 53.1 us with the join, 5.1 TB/s; 64 tokens with windows of 1021, 251 MB,
+// 50.5 us; 64 over e4m3 caches of 17 to 8190 positions 116 to 123 us, 4.7 TB/s).
 template <int ND, bool E4M3>
 __global__ __launch_bounds__(256, 3) void chunk_rows_kernel(ChunkArgs a, ChunkPlan plan, ChunkWorkspace ws) {
     constexpr int D = ND * 32, M = 16, kVs = D + 16, kOs = D + 4;
@@ -323,14 +323,15 @@ __global__ __launch_bounds__(256, 3) void chunk_rows_kernel(ChunkArgs a, ChunkPl
 // 0.0024 of their size on average, of which their own rounding is 0.0017.
 //
 // Bound by the matrix and the vector unit of two waves a SIMD, and by the clock that the card's
-// power leaves them (2.0 GHz): 4096 tokens, 32 query and 8 key heads of 128, 166 us, 825
-// TFLOP/s, the matrix unit busy in 40% of the cycles and the vector unit issuing in 43%; 509
-// tokens behind 33258 positions 305 us, 900 TFLOP/s. Slower were 64 rows a wave, with the
+// power leaves them (2.0 GHz): 4096 tokens, 32 query and 8 key heads of 128, 156.5 us, 878
+// TFLOP/s, the matrix unit busy in 41% of the cycles and the vector unit issuing in 42%; 509
+// tokens behind 32749 positions 297 us, 927 TFLOP/s. At an earlier step (177 and 319 us) slower were 64 rows a wave, with the
 // operands read for twice the rows but one wave a SIMD (207 and 344 us), and all scores of a
 // step before the product with V (182 and 321). D 64 forms as many weights for half of the
-// products: 122 us for 4096 tokens (560 TFLOP/s). e4m3 steps pay for their conversion: 16 chunks
-// of 1 to 701 tokens behind 0 to 4099 positions 305 us, 700 TFLOP/s; LDS bank conflicts of the
-// converted pieces (9% of its cycles) cost nothing: without them 308 us.
+// products: 115 us for 4096 tokens (597 TFLOP/s). e4m3 steps pay for their conversion: 16 chunks
+// of 1 to 701 tokens behind 0 to 4099 positions 287 us, 748 TFLOP/s; LDS bank conflicts of the
+// converted pieces (9% of its cycles) cost nothing (306 us, without
+// them 309).
 template <int ND, bool E4M3>
 __global__ __launch_bounds__(256, ND == 2 ? 3 : 2) void chunk_tiles_kernel(ChunkArgs a, ChunkPlan plan, ChunkWorkspace ws) {
     constexpr int D = ND * 32, M = 128, NK = D / 16, NO = D / 32;
@@ -583,7 +584,7 @@ __global__ __launch_bounds__(256, ND == 2 ? 3 : 2) void chunk_tiles_kernel(Chunk
             else
                 o[j / 2 % NO] = mma(f[j % (AHEAD + 1)], p[j / 2 / NO], o[j / 2 % NO]);
             // pair y of weights: its arguments, a slot later its exponentials, and another one later
-            // the rest, so that no instruction waits for the one before it (166 us; all in one slot 172)
+            // the rest, so that no instruction waits for the one before it (168 us, all in one slot 172)
             if (j % EVERY == 0) {
                 const int y = j / EVERY;
                 x[y % 3][0] = fmaf(t[2 * y], c, -base);

@@ -11,8 +11,8 @@
 // waves take 64 keys each in turn. Scores: a lane per key, the rows' q from LDS (the same
 // for all lanes). Values: lanes over the head_dim, weights from LDS. Bound by the vector
 // ALU and the LDS broadcasts (4 D operations per row and key): 512
-// tokens, 32 query and 8 key heads of 80, 133 us (10 TFLOP/s), 16 and 4 heads of 256 166 us; 32
-// single tokens over 2200 positions each, heads of 80, 224 us.
+// tokens, 32 query and 8 key heads of 80, 127 us (11 TFLOP/s), 16 and 4 heads of 256 162 us; 32
+// single tokens over 2200 positions each, heads of 80, 226 us.
 #include "attn_chunk.hpp"
 
 namespace tsv {
