@@ -302,22 +302,28 @@ bool matrix_shape(const tsv_attn_shape* s) {
            (long long)s->n_pages * s->n_kv_heads * s->page_size < (1LL << 32);
 }
 
-// Rows of a block: 16 (chunk_rows_kernel) where the sequences have no more on average, as
-// single tokens do, 128 (chunk_tiles_kernel), or 8 (plain). Work-groups wanted, for x of
-// them that would run without any cut:
+// Rows of a block, by those that the sequences have of a key head on average:
+//   bf16   16 (chunk_rows_kernel) up to 16, as single tokens do, otherwise 128
+//          (chunk_tiles_kernel). 8 single tokens over 1000 positions 17.4 us, 22.5 in blocks of
+//          128; 32 chains of 8 tokens, 32 rows, over 4096 117 us, 130 in blocks of 16
+//   fp32   16 up to 32 rows, otherwise 64. 32 single tokens over 4096 positions 205 us, 238 in
+//          blocks of 64; 32 chains of 8 tokens 266 and 316
+//   plain  8
+// Work-groups wanted, for x of them that would run without any cut:
 //   tiles  one round of two a compute unit (a chunk of 509 over 33258 positions: 316 us, 388
 //          for half as many, 339 for twice)
 //   rows   few parts while they fill one round, small ones where many items of different
 //          lengths share the GPU (us for half as many, as here, and twice: 1 token over 65532
 //          positions 54, 55, 59; 8 over 4000 32, 32, 35; 64 over 17 to 8190 in e4m3 124, 123, 131)
-// No block is cut that has no more than 512 keys, nor where a window bounds every block and
+// (at earlier steps of the kernels.) No block is cut that has no more than 512 keys, nor where a window bounds every block and
 // blocks fill the GPU (64 tokens, windows of 1021: 55 us, 65 with a second launch that finds
 // nothing to join).
 ChunkPlan plan_of(const tsv_attn_shape* s, bool matrix, int window, int sinks) {
     ChunkPlan p;
     const int g = s->n_heads / s->n_kv_heads;
     const long long T = s->n_nodes, rows = T * g, items = s->batch < T ? s->batch : T, x = items * s->n_kv_heads;
-    p.rows = !matrix ? kRows : rows <= 16LL * s->batch ? 16 : s->in_dtype == TSV_F32 ? 64 : 128;
+    const bool f32 = s->in_dtype == TSV_F32;
+    p.rows = !matrix ? kRows : rows <= (f32 ? 32LL : 16LL) * s->batch ? 16 : f32 ? 64 : 128;
     p.want = !matrix ? 1024 : p.rows > 16 || x <= 128 ? 512 : x >= 512 ? 2048 : (int)(4 * x);
     p.min_keys = 256;
     for (p.shift = 0; 1 << p.shift < p.rows;) ++p.shift;

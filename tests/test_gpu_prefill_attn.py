@@ -105,6 +105,36 @@ def test_single_tokens(bnd, dtype, cdtype, H, Hk, D, window, sinks):
     check(bnd, queries(6, 12, H, D, dtype), [1] * 12, old, c, f"tokens {dtype} {cdtype} H={H}/{Hk} D={D} window {window}", window, sinks)
 
 
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+@pytest.mark.parametrize("H,Hk,D", [(8, 2, 128), (4, 2, 64)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (20, 3)])
+def test_short_chains(bnd, dtype, cdtype, H, Hk, D, window, sinks):
+    """A few tokens of some items beside single tokens of the others: sequences of several of the smallest blocks."""
+    lens, old = [7, 1, 1, 0, 1, 13, 1, 2, 1, 1, 1, 1], [0, 700, 31, 5, 64, 1100, 1, 63, 255, 2000, 17, 9]
+    c = case(17, lens, old, Hk, D, 16, dtype, cdtype)
+    check(bnd, queries(18, sum(lens) + 2, H, D, dtype), lens, old, c, f"chains {dtype} {cdtype} H={H}/{Hk} D={D} window {window}", window, sinks, first=1)
+
+
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+@pytest.mark.parametrize("D", [128, 40])
+def test_windows_past_everything(bnd, dtype, cdtype, D):
+    """The largest window, and the most first positions, leave nothing out."""
+    lens, old = [70, 1, 300], [40, 900, 0]
+    c = case(19, lens, old, 2, D, 16, dtype, cdtype)
+    q = queries(20, sum(lens), 4, D, dtype)
+    whole = check(bnd, q, lens, old, c, f"whole {dtype} {cdtype} D={D}", rows=some)
+    most = 2 ** 31 - 1
+    for window, sinks in ((most, 0), (most, most), (most - 1, 7), (1, most), (64, 1300)):
+        o = torch.full_like(q, 7.0)
+        args, scales = U.cache_args(c)
+        bnd.attn_prefill(q, V.starts(lens), *args, **scales, window=window, sinks=sinks, o=o)
+        torch.cuda.synchronize()
+        err = (o.double() - whole.double()).abs().max().item()
+        # two computations of the same sums, each within its bound: outputs of unit size differ by four roundings of
+        # the type at most in what the matrix kernels' weights and outputs lose (bf16), or by the sums' own (fp32)
+        assert err <= (4 * 2.0 ** -8 if dtype == BF else 1e-4) * max(1.0, whole.double().abs().max().item()), (window, sinks, err)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("H,Hk,D", [(4, 1, 128), (2, 2, 64)])
 @pytest.mark.parametrize("n,old", [(1, 0), (63, 1), (129, 63), (520, 0), (777, 333)])
