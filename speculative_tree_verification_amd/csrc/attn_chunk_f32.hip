@@ -15,9 +15,10 @@
 // Many rows are bound by the fp32 matrix unit, which waits for LDS and the softmax of its own
 // step: 2 chunks of 500 tokens behind 1000 positions, 32 query and 8 key heads of 128, 230 us
 // (89 TFLOP/s; a large fp32 product reaches 154); 3 prompts of 130 to 777 tokens in a window of
-// 255, 24 and 3 heads of 64, 32.4 us, the unit busy in 40% of the cycles. Few rows are bound by
+// 255, 24 and 3 heads of 64, 30.3 us, the unit busy in 40% of the cycles. Few rows are bound by
 // the cache's bytes: 32 tokens over 2200 positions, 578 MB, 118 us (4.9 TB/s). Weights stay in fp32.
 #include <cfloat>
+#include <type_traits>
 
 #include "attn_chunk.hpp"
 #include "attn_lanes.hpp"
@@ -74,24 +75,25 @@ __global__ __launch_bounds__(256, 2) void chunk_f32_kernel(ChunkArgs a, ChunkPla
     const ChunkSeen seen = chunk_seen(a, kk, own);
     auto sees = [&](int v) { return v < seen.hi && (v >= seen.lo || v < a.sinks); };  // virtual position v
 
-    // One tile of keys in LDS, from virtual position t on
-    auto take = [&](int t, bool whole) {
-        f32x4 s[NX];
+    // One tile of keys in LDS, from virtual position t on, or the first `keys` of it
+    auto take = [&](int t, bool whole, auto keys) {
+        constexpr int NK = decltype(keys)::value / 16 < NX ? decltype(keys)::value / 16 : NX;  // products of 16 keys
+        f32x4 s[NK];
 #pragma unroll
-        for (int x = 0; x < NX; ++x) s[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int x = 0; x < NK; ++x) s[x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
 #pragma unroll
-            for (int x = 0; x < NX; ++x) s[x] = mma4(*(const float4*)&s_K[(16 * (x + wk) + l16) * kS + 16 * j + 4 * lg], q[j], s[x]);
+            for (int x = 0; x < NK; ++x) s[x] = mma4(*(const float4*)&s_K[(16 * (x + wk) + l16) * kS + 16 * j + 4 * lg], q[j], s[x]);
             if (j % 2) __builtin_amdgcn_sched_barrier(0);
         }
         if (E4M3) {
 #pragma unroll
-            for (int x = 0; x < NX; ++x) s[x] *= *(const f32x4*)&s_ks[16 * (x + wk) + 4 * lg];
+            for (int x = 0; x < NK; ++x) s[x] *= *(const f32x4*)&s_ks[16 * (x + wk) + 4 * lg];
         }
         if (!whole) {
 #pragma unroll
-            for (int x = 0; x < NX; ++x)
+            for (int x = 0; x < NK; ++x)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int v = t + 16 * (x + wk) + 4 * lg + r;
@@ -100,7 +102,7 @@ __global__ __launch_bounds__(256, 2) void chunk_f32_kernel(ChunkArgs a, ChunkPla
         }
         float mx = max3(max3(s[0][0], s[0][1], s[0][2]), s[0][3], s[0][3]);
 #pragma unroll
-        for (int x = 1; x < NX; ++x) mx = max3(max3(mx, s[x][0], s[x][1]), s[x][2], s[x][3]);
+        for (int x = 1; x < NK; ++x) mx = max3(max3(mx, s[x][0], s[x][1]), s[x][2], s[x][3]);
         if (__ballot(fmaf(mx, c, -base) > kSlack)) {
             const float top = row_max(mx);  // a row moves by its own scores alone: its bits do not follow from its neighbours'
             const float to = fmaf(top, c, -base) > kSlack ? top * c : base, al = __builtin_amdgcn_exp2f(base - to);
@@ -110,7 +112,7 @@ __global__ __launch_bounds__(256, 2) void chunk_f32_kernel(ChunkArgs a, ChunkPla
             base = to;
         }
 #pragma unroll
-        for (int x = 0; x < NX; ++x) {
+        for (int x = 0; x < NK; ++x) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 s[x][r] = __builtin_amdgcn_exp2f(fmaf(s[x][r], c, -base));
@@ -246,7 +248,12 @@ __global__ __launch_bounds__(256, 2) void chunk_f32_kernel(ChunkArgs a, ChunkPla
                 request(set ^ 1);
             }
             if (!active) continue;
-            take(t, whole);
+            // the last tile's second half may have no keys (the windowed prompts above: 30.3 us, 32.4
+            // with its products)
+            if (NX > 2 && t + kTileKeys / 2 >= kk.k1)
+                take(t, false, std::integral_constant<int, kTileKeys / 2>());
+            else
+                take(t, whole, std::integral_constant<int, kTileKeys>());
             if (!whole) add_odd(t, s_odd[set]);
         }
     }
