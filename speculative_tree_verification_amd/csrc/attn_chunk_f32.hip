@@ -15,7 +15,7 @@
 // Many rows are bound by the fp32 matrix unit, which waits for LDS and the softmax of its own
 // step: 2 chunks of 500 tokens behind 1000 positions, 32 query and 8 key heads of 128, 230 us
 // (89 TFLOP/s; a large fp32 product reaches 154); 3 prompts of 130 to 777 tokens in a window of
-// 255, 24 and 3 heads of 64, 30.3 us, the unit busy in 40% of the cycles. Few rows are bound by
+// 255, 24 and 3 heads of 64, 29.3 us, the unit busy in 40% of the cycles. Few rows are bound by
 // the cache's bytes: 32 tokens over 2200 positions, 578 MB, 118 us (4.9 TB/s). Weights stay in fp32.
 #include <cfloat>
 #include <type_traits>
@@ -248,9 +248,11 @@ __global__ __launch_bounds__(256, 2) void chunk_f32_kernel(ChunkArgs a, ChunkPla
                 request(set ^ 1);
             }
             if (!active) continue;
-            // the last tile's second half may have no keys (the windowed prompts above: 30.3 us, 32.4
-            // with its products)
-            if (NX > 2 && t + kTileKeys / 2 >= kk.k1)
+            // the last tile may have few keys (the windowed prompts above: 29.3 us, 30.2 without the
+            // quarter, 32.4 with all products)
+            if (NX > 2 && t + kTileKeys / 4 >= kk.k1)
+                take(t, false, std::integral_constant<int, kTileKeys / 4>());
+            else if (NX > 2 && t + kTileKeys / 2 >= kk.k1)
                 take(t, false, std::integral_constant<int, kTileKeys / 2>());
             else
                 take(t, whole, std::integral_constant<int, kTileKeys>());

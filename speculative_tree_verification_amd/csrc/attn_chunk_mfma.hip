@@ -21,7 +21,7 @@ constexpr int kSub = 32;  // keys of a step
 
 // Most steps whose keys not all of a block's 128 rows see: up to 127 positions at the windows'
 // start, behind the sinks' last step's others, and up to 127 at the end, each with what is
-// left of its steps, and the step that makes their number even
+// left of its steps
 constexpr int kOddSteps = 12;
 
 __device__ __forceinline__ bool nonfinite(float v) { return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u; }
@@ -651,14 +651,18 @@ __global__ __launch_bounds__(256, ND == 2 ? 3 : 2) void chunk_tiles_kernel(Chunk
                 }
                 if (!active) continue;
                 step(s + slot, slot, sa, sb, pa, pb);
+                if (s + slot + 1 >= n) {  // an odd number of steps
+                    pa[0] = pb[0];
+                    pa[1] = pb[1];
+                    break;
+                }
                 step(s + slot + 1, slot + 1, sb, sa, pb, pa);
             }
         }
-        // (an odd number of steps ends with one past the last key: its weights are 0)
         lds_barrier();
         if (active) {
             rescale();
-            product((n + 1) / 2 * 2 - 1, pa);
+            product(n - 1, pa);
             for (int i = 0; i < kOddSteps; ++i) {
                 const int s = i < whole0 - sink_steps ? sink_steps + i : whole1 + i - (whole0 - sink_steps);
                 for (uint32_t odd = s_odd[i]; odd; odd &= odd - 1) add_odd(kSub * s + __builtin_ctz(odd));
