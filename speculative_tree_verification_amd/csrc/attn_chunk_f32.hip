@@ -15,7 +15,7 @@
 // Many rows are bound by the fp32 matrix unit, which waits for LDS and the softmax of its own
 // step: 2 chunks of 500 tokens behind 1000 positions, 32 query and 8 key heads of 128, 230 us
 // (89 TFLOP/s; a large fp32 product reaches 154); 3 prompts of 130 to 777 tokens in a window of
-// 255, 24 and 3 heads of 64, 29.3 us, the unit busy in 40% of the cycles. Few rows are bound by
+// 255, 24 and 3 heads of 64, 29.3 us, the unit busy in 35% of the cycles. Few rows are bound by
 // the cache's bytes: 32 tokens over 2200 positions, 578 MB, 118 us (4.9 TB/s). Weights stay in fp32.
 #include <cfloat>
 #include <type_traits>

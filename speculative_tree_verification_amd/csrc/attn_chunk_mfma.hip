@@ -323,13 +323,13 @@ __global__ __launch_bounds__(256, 3) void chunk_rows_kernel(ChunkArgs a, ChunkPl
 // 0.0024 of their size on average, of which their own rounding is 0.0017.
 //
 // Bound by the matrix and the vector unit of two waves a SIMD, and by the clock that the card's
-// power leaves them (2.0 GHz): 4096 tokens, 32 query and 8 key heads of 128, 156.5 us, 878
+// power leaves them (2.0 GHz): 4096 tokens, 32 query and 8 key heads of 128, 155 us, 889
 // TFLOP/s, the matrix unit busy in 41% of the cycles and the vector unit issuing in 42%; 509
-// tokens behind 32749 positions 297 us, 927 TFLOP/s. At an earlier step (177 and 319 us) slower
+// tokens behind 32749 positions 294 us, 938 TFLOP/s. At an earlier step (177 and 319 us) slower
 // were 64 rows a wave, with operands read for twice the rows but one wave a SIMD (207 and 344),
 // and all scores of a step before the product with V (182 and 321). D 64 forms as many weights
-// for half of the products: 115 us for 4096 tokens (597 TFLOP/s). e4m3 steps pay for their
-// conversion: 16 chunks of 1 to 701 tokens behind 0 to 4099 positions 287 us, 748 TFLOP/s; the
+// for half of the products: 110 us for 4096 tokens (625 TFLOP/s). e4m3 steps pay for their
+// conversion: 16 chunks of 1 to 701 tokens behind 0 to 4099 positions 286 us, 750 TFLOP/s; the
 // LDS bank conflicts of the converted pieces (9% of its cycles) cost nothing (306 us, 309 without).
 template <int ND, bool E4M3>
 __global__ __launch_bounds__(256, ND == 2 ? 3 : 2) void chunk_tiles_kernel(ChunkArgs a, ChunkPlan plan, ChunkWorkspace ws) {
