@@ -1320,10 +1320,17 @@ def attn_rope(q, k, position, inv_freq, q_weight=None, k_weight=None, eps: float
     shape = _attn_shape(1, position.numel(), H or Hk, Hk or 1, D, 0, 1, 0, code, code, 0, 1.0)
 
     def body(s):
-        qo = q_out if q is None or q_out is not None else q.new_empty(q.shape)
-        ko = k_out if k is None or k_out is not None else k.new_empty(k.shape)
-        rc = lib.tree_attn_rope(shape, rope, _opt(q), _opt(k), position.data_ptr(), inv_freq.data_ptr(), _opt(q_weight),
-                                _opt(k_weight), _opt(qo), _opt(ko), s)
+        qo, ko, qp, qop, kp, kop = q_out, k_out, None, None, None, None
+        if q is not None:
+            if qo is None:
+                qo = torch.empty_like(q, memory_format=torch.contiguous_format)
+            qp, qop = q.data_ptr(), qo.data_ptr()
+        if k is not None:
+            if ko is None:
+                ko = torch.empty_like(k, memory_format=torch.contiguous_format)
+            kp, kop = k.data_ptr(), ko.data_ptr()
+        rc = lib.tree_attn_rope(shape, rope, qp, kp, position.data_ptr(), inv_freq.data_ptr(), _opt(q_weight),
+                                _opt(k_weight), qop, kop, s)
         if rc != 0:
             raise TreeSSDError(rc, "tree_attn_rope")
         return qo, ko
@@ -1358,10 +1365,14 @@ def attn_append_rope(q, k, v, seq_start, inv_freq, k_cache, v_cache, page_table,
     fields = _attn_fields(k, k_cache, v_cache, k_scale, v_scale, page_table, cache_len, Bt, L, H, 1.0, False)
 
     def body(s):
-        qo = q_out if q is None or q_out is not None else q.new_empty((L, H, D))
-        rc = lib.tree_attn_append_rope(_attn_shape(*fields), rope, _opt(q), k.data_ptr(), v.data_ptr(),
+        qo, qp, qop = q_out, None, None
+        if q is not None:
+            if qo is None:
+                qo = torch.empty_like(q, memory_format=torch.contiguous_format)
+            qp, qop = q.data_ptr(), qo.data_ptr()
+        rc = lib.tree_attn_append_rope(_attn_shape(*fields), rope, qp, k.data_ptr(), v.data_ptr(),
                                        seq_start.data_ptr(), inv_freq.data_ptr(), _opt(q_weight), _opt(k_weight),
-                                       page_table.data_ptr(), cache_len.data_ptr(), _opt(qo), k_cache.data_ptr(),
+                                       page_table.data_ptr(), cache_len.data_ptr(), qop, k_cache.data_ptr(),
                                        v_cache.data_ptr(), _opt(k_scale), _opt(v_scale), _opt(seq_status), s)
         if rc != 0:
             raise TreeSSDError(rc, "tree_attn_append_rope")

@@ -8,7 +8,7 @@
 // elements stay z.
 //
 // Bound by the rows' traffic, and in 8 bits by the vector unit beside it: 32 trees of 63 nodes,
-// 32 query and 8 key heads of 128 in bf16, 41 MB, 10 us in the kernel (12.7 a call, the host's
+// 32 query and 8 key heads of 128 in bf16, 41 MB, 10 us in the kernel (11.5 a call, the host's
 // time); 16 prompts of 1 to 2047 tokens into an e4m3 cache, 370 MB, 80 us (4.6 TB/s; a large
 // copy reaches 5.1); one token 3.8 us.
 //
