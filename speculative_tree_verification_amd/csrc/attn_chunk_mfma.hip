@@ -421,11 +421,12 @@ __global__ __launch_bounds__(256, ND == 2 ? 3 : 2) void chunk_tiles_kernel(Chunk
             }
         }
         if (E4M3 && w == 0) {
-            // a value row's scale that is not finite: as its elements (below)
-            const int s = 2 * m - 1 + lane / kSub;
+            // a value row's scale that is not finite: as its elements (below). Past the last key its
+            // row was read again: a key there has no position, and is none of those
+            const int s = 2 * m - 1 + lane / kSub, k = kSub * (2 * m - 1) + lane;
             float vs = rk.vs;
             if (nonfinite(vs) && !full(s)) {
-                if (s >= 0 && s < n) atomicOr(&s_odd[odd_of(s)], 1u << (lane % kSub));
+                if (k >= 0 && k < kk.k1 - kk.k0) atomicOr(&s_odd[odd_of(s)], 1u << (lane % kSub));
                 vs = 0.f;
             }
             s_ks[s & 7][lane % kSub] = rk.ks;
@@ -603,6 +604,7 @@ __global__ __launch_bounds__(256, ND == 2 ? 3 : 2) void chunk_tiles_kernel(Chunk
     // the elements of a key's value that are not finite, to the rows that see it
     auto add_odd = [&](int i) TSV_INLINE {
         const int v = kk.k0 + i, pos = chunk_pos(kk, v);
+        if (v >= kk.k1) return;  // no key of this part: its page is not one that was checked
         const uint32_t at = chunk_row(a, table[page_of(pos, a.div)], hk, pos);
         const bool sees = v < seen.hi && (v >= seen.lo || v < a.sinks), scaled = !E4M3 || !nonfinite(gload(a.v_scale + at));
 #pragma unroll

@@ -545,3 +545,55 @@ def test_layer_calls_in_a_graph(bnd):
         torch.cuda.synchronize()
         for a, b in zip(everything + caches, want):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), lens
+
+
+def few_rows(bnd, lens, H, Hk, D, dtype, cdtype=None):
+    """Whether the call's blocks are those of few rows (16; 64 or 128 otherwise): by what a table that is cut needs."""
+    need = bnd.attn_prefill_workspace_bytes(len(lens), sum(lens), H, Hk, D, 16, 4096, dtype, cdtype)
+    return need / (2 * 512 * 4 * (D + 2)) < 32
+
+
+# kernel, new tokens of the one item: blocks of few rows, of many, and the plain kernel
+KERNELS = [("few", 1), ("few", 4), ("many", 21), ("many", 150), ("plain", 4), ("plain", 21)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("kernel,n", KERNELS)
+@pytest.mark.parametrize("old", [0, 38, 1210])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (30, 2)])
+def test_last_scale_that_is_not_finite(bnd, dtype, value, kernel, n, old, window, sinks):
+    """The newest position's scale or byte is a NaN, as appended from a row that is not finite: it reaches the last
+    token's rows alone, and positions behind it (whose rows of the pool are finite here, and pages of the pool) none."""
+    c = case(41, [n], [old], 2, 64, 16, dtype, E4)
+    c["page_table"].clamp_(min=0)
+    for m in ("k_scale", "v_scale"):
+        c[m].nan_to_num_(nan=1.0)
+    for m in ("k_cache", "v_cache"):
+        u = c[m].view(torch.uint8)
+        u[u == 0x7f] = 0x30
+    q = queries(42, n, 8, 64, dtype)
+    assert kernel == "plain" or few_rows(bnd, [n], 8, 2, 64, dtype, E4) == (kernel == "few")
+    args, scales = U.cache_args(c)
+    run = lambda: bnd.attn_prefill(q, V.starts([n]), *args, **scales, window=window, sinks=sinks, force_generic=kernel == "plain")
+    clean = run()
+    p = old + n - 1
+    page, slot = int(c["page_table"][0, p // 16]), p % 16
+    for m in ("k_scale", "v_scale", "v_cache"):
+        t = c[m] if m != "v_cache" else c[m].view(torch.uint8)
+        keep = t.clone()
+        if m == "v_cache":
+            t[page, 1, slot, 7] = 0x7f
+        else:
+            t[page, 1, slot] = value
+        say(f"[last] {m} {value} {kernel} {dtype} {n} after {old} window {window}+{sinks}")
+        o = run()
+        assert torch.equal(o[:-1], clean[:-1]), m
+        assert torch.equal(o[:, :4], clean[:, :4]), "the other key head"
+        if m == "v_cache":
+            assert torch.isnan(o[-1, 4:, 7].float()).all()
+        elif m == "v_scale":
+            assert not torch.isfinite(o[-1, 4:].float()).any()
+        elif value != value:
+            assert torch.isnan(o[-1, 4:].float()).all()
+        t.copy_(keep)
