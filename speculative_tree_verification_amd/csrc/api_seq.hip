@@ -130,7 +130,8 @@ tsv::RopeArgs rope_args(const tsv_attn_shape* s, const tsv_rope* r, const void* 
     a.qs = q ? r->q_stride : 0; a.ks = k ? r->k_stride : 0; a.vs = v ? r->v_stride : 0;
     a.rows = rows; a.H = s->n_heads; a.Hk = s->n_kv_heads; a.D = s->head_dim;
     a.R = r->rot_dim; a.interleaved = r->interleaved; a.eps = r->eps;
-    a.heads = tsv::page_div((q ? s->n_heads : 0) + (k ? s->n_kv_heads : 0));
+    const int heads = (q ? s->n_heads : 0) + (k ? s->n_kv_heads : 0);
+    a.heads = tsv::page_div(heads > 0 ? heads : 1);  // (a call without rows may have neither: nothing is divided then)
     a.key_heads = tsv::page_div(s->n_kv_heads);
     return a;
 }

@@ -250,3 +250,22 @@ def test_values_that_are_not_finite_in_8_bits(bnd):
     got = [x[:6, 0] for x in V.cached(c, 0, 6)]
     for g, t, row in ((got[0], k, 2), (got[1], v, 4)):
         assert np.isnan(g[row]).all() and np.isfinite(np.delete(g, row, 0)).all()
+
+
+@pytest.mark.parametrize("dtype,cdtype", [(BF, BF), (F32, E4)])
+@pytest.mark.parametrize("with_q", [False, True])
+def test_append_of_no_rows(bnd, dtype, cdtype, with_q):
+    """A call without rows writes the status of its empty sequences and nothing else."""
+    c = U.cache(43, 3, [5, 0, 40], 2, 64, 16, dtype, cdtype)
+    c["cache_len"][1] = 10 ** 6  # past its pages
+    args, scales = U.cache_args(c)
+    before = {m: c[m].clone() for m in ("k_cache", "v_cache")}
+    rows = lambda h: torch.empty(0, h, 64, dtype=dtype, device="cuda")
+    st = torch.full((3,), -3, dtype=torch.int32, device="cuda")
+    say(f"[append] no rows, {dtype} {cdtype} q: {with_q}")
+    q = bnd.attn_append_rope(rows(4) if with_q else None, rows(2), rows(2), V.starts([0, 0, 0]), freqs(64), *args, **scales, seq_status=st)
+    bnd.attn_append_rope(None, rows(2), rows(2), V.starts([0, 0, 0]), freqs(64), *args, **scales)
+    torch.cuda.synchronize()
+    assert st.tolist() == [0, 64, 0] and (q.shape == (0, 4, 64) if with_q else q is None)
+    for m, t in before.items():
+        assert torch.equal(c[m].view(torch.uint8), t.view(torch.uint8))

@@ -230,3 +230,10 @@ def test_rows_at_one_distance():
     assert rows(t[1:2, 1:2], (1, 1), (10, 8)) == 80     # one row: its own length
     assert rows(t[0, :, 2:5], (6,), (3, 8)) == 80
     assert rows(t.view(4, 6, 80)[..., 8:24], (4, 6), (16,)) == 80
+
+
+def test_append_of_no_rows():
+    """Rows that are none have no pointers (as an empty tensor's)."""
+    for q in (None, FAKE):
+        assert append(attn(n_nodes=0), rot(), [q, None, None] + [FAKE] * 11) == OK
+    assert append(attn(n_nodes=0, n_pages=0, max_pages=0), rot(), [None] * 3 + [FAKE, FAKE] + [None] * 3 + [FAKE] + [None] * 5) == OK
