@@ -597,3 +597,44 @@ def test_last_scale_that_is_not_finite(bnd, dtype, value, kernel, n, old, window
         elif value != value:
             assert torch.isnan(o[-1, 4:].float()).all()
         t.copy_(keep)
+
+
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+@pytest.mark.parametrize("n", [4, 20])
+@pytest.mark.parametrize("size", [8.0, 2.0 ** 18 + 2.0 ** 16])
+def test_rows_do_not_depend_on_their_neighbours(bnd, dtype, cdtype, n, size):
+    """Rows with the same score at every position, beside rows whose maximum moves at every step: an output is the mean of
+    the values whatever the neighbours do, to the bit."""
+    items, H, Hk, D, old = 6, 8, 2, 64, 490
+    lens, olds = [n] * items, [old] * items
+    c = case(45, lens, olds, Hk, D, 16, dtype, cdtype)
+    ramp = torch.zeros(old + n, D)
+    ramp[:, 0], ramp[:, 1] = 1, torch.arange(old + n) // 16
+    rows = torch.arange(old + n)
+    for b in range(items):
+        pages = c["page_table"][b].cpu()[rows // 16]
+        c["k_cache"][pages.cuda(), :, (rows % 16).cuda()] = ramp.cuda()[:, None].expand(-1, Hk, -1).to(c["k_cache"].dtype)
+        if cdtype == E4:
+            c["k_scale"][pages.cuda(), :, (rows % 16).cuda()] = 1.0
+    assert few_rows(bnd, lens, H, Hk, D, dtype, cdtype) == (n == 4)
+    q = torch.zeros(items, n, H, D, dtype=dtype, device="cuda")
+    q[..., 0] = size
+    args, scales = U.cache_args(c)
+    run = lambda x: bnd.attn_prefill(x.view(-1, H, D), V.starts(lens), *args, **scales).view(items, n, H, D)
+    want = run(q)
+    for b in range(items):
+        _, vc = V.cached(c, b, old + n)
+        for i in (0, 1, n - 1):
+            v = vc[:old + i + 1]
+            mean, oa = v.mean(0), np.abs(v).mean(0)
+            # all scores are one number, so the weights are equal: the sums round, in bf16 the output, and in blocks of many
+            # rows the weight beside its sum
+            half = 2.0 ** -8 if dtype == BF else 0.0
+            bound = (old + 64) * 2.0 ** -24 * oa + half * (np.abs(mean) * 1.01 + (oa if n > 4 else 0)) + 1e-30
+            U.within(U.f64(want[b, i]).reshape(Hk, 4, D), mean[:, None], bound[:, None], f"mean {b} {i}")
+    x = q.clone()
+    x[:, :, 1::2, 1] = 4.0
+    x[:, :2, :, 1] = 2.0
+    got = run(x)
+    assert torch.equal(got[:, 2:, ::2], want[:, 2:, ::2])
+    assert not torch.equal(got[:, :2], want[:, :2])
