@@ -638,3 +638,40 @@ def test_rows_do_not_depend_on_their_neighbours(bnd, dtype, cdtype, n, size):
     got = run(x)
     assert torch.equal(got[:, 2:, ::2], want[:, 2:, ::2])
     assert not torch.equal(got[:, :2], want[:, :2])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("kernel,n", KERNELS[1:])
+@pytest.mark.parametrize("old,back,window,sinks", [(40, -1, 0, 0), (40, 0, 0, 0), (700, -1, 0, 0), (700, 299, 300, 2), (700, 0, 300, 2), (700, 699, 300, 2)])
+def test_positions_that_are_not_finite_in_each_kernel(bnd, dtype, value, kernel, n, old, back, window, sinks):
+    """A key or a value that is not finite, at the newest position (back -1) or `back` before the first new one, in bits: the
+    rows that see it have it, an infinite value as an infinity, the others are as they were."""
+    c = case(48, [n], [old], 2, 64, 16, dtype, dtype)
+    q = queries(49, n, 8, 64, dtype)
+    assert kernel == "plain" or few_rows(bnd, [n], 8, 2, 64, dtype) == (kernel == "few")
+    args, _ = U.cache_args(c)
+    run = lambda: bnd.attn_prefill(q, V.starts([n]), *args, window=window, sinks=sinks, force_generic=kernel == "plain")
+    clean, at = run(), old + n - 1 if back < 0 else old - back
+    see = [i for i in range(n) if Y.sees(old + i, at, window, sinks)]
+    others = [i for i in range(n) if i not in set(see)]
+    assert see
+    page, slot = int(c["page_table"][0, at // 16]), at % 16
+    rest = [d for d in range(64) if d != 5]
+    for m in ("v_cache", "k_cache"):
+        keep = c[m].clone()
+        c[m][page, 1, slot, 5] = value
+        o = run()
+        assert torch.equal(o[others], clean[others]), m
+        assert torch.equal(o[:, :4], clean[:, :4]), "the other key head"
+        if m == "v_cache":
+            hit = o[see][:, 4:, 5]
+            assert torch.isnan(hit.float()).all() if value != value else (hit == value).all(), hit
+            assert torch.equal(o[..., rest], clean[..., rest])
+        elif value != value:
+            assert torch.isnan(o[see][:, 4:].float()).all()
+        else:  # an infinite score: its weight is the only one (NaN), or none
+            up = (q[see][:, 4:, 5].double() * value > 0)[..., None].expand(-1, -1, 64)
+            got = o[see][:, 4:]
+            assert torch.isnan(got[up].float()).all() and torch.isfinite(got[~up].float()).all()
+        c[m].copy_(keep)
