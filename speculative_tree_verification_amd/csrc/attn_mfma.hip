@@ -113,7 +113,7 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
         }
     }
 
-    float m = -INFINITY, l = 0.f;  // in units of the raw scores
+    float base = -FLT_MAX, l = 0.f;  // the row's maximum, c times its largest score, as it is rounded
     f32x4 o[D / 16];
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -122,15 +122,14 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
     // of each value row; V in this wave's LDS
     auto take = [&](const f32x4* s, const f32x4* vs) {
         const float top = max3(max3(s[0][0], s[0][1], s[0][2]), max3(s[0][3], s[1][0], s[1][1]), max3(s[1][1], s[1][2], s[1][3]));
-        const float mn = max3(row_max(top), m, m);
-        const float base = mn == -INFINITY ? 0.f : mn * c;
-        if (__ballot(mn > m)) {  // some row's maximum moved
-            const float al = __builtin_amdgcn_exp2f(fmaf(m, c, -base));
+        const float to = fmaxf(base, row_max(top) * c);
+        if (__ballot(to > base)) {  // some row's maximum moved (the factor of the others is 1)
+            const float al = __builtin_amdgcn_exp2f(base - to);
+            base = to;
             l *= al;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) o[i] *= al;
         }
-        m = mn;
         float p[8], sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -319,22 +318,20 @@ __global__ __launch_bounds__(256, 3) void attn_rows_kernel(AttnArgs a, AttnPlan 
         take_tree();
     }
     l = row_sum(l);
-    m = m == -INFINITY ? m : m * c;
 
     // the four waves
     if (lg == 0) {
-        s_ml[w][l16][0] = m;
+        s_ml[w][l16][0] = base;
         s_ml[w][l16][1] = l;
     }
     st |= __syncthreads_or(bad) ? kStBadCache : 0;
-    float mt = -INFINITY, lt = 0.f;
+    float mt = -FLT_MAX, lt = 0.f;
 #pragma unroll
     for (int x = 0; x < 4; ++x) mt = fmaxf(mt, s_ml[x][l16][0]);
-    const float base = mt == -INFINITY ? 0.f : mt;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) lt += s_ml[x][l16][1] * __builtin_amdgcn_exp2f(s_ml[x][l16][0] - base);
+    for (int x = 0; x < 4; ++x) lt += s_ml[x][l16][1] * __builtin_amdgcn_exp2f(s_ml[x][l16][0] - mt);
     {
-        const float al = __builtin_amdgcn_exp2f(m - base);
+        const float al = __builtin_amdgcn_exp2f(base - mt);
         float* so = (float*)s_V + (w * 16 + l16) * kOs + 4 * lg;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) *(f32x4*)(so + 16 * i) = o[i] * al;

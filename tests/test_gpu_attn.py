@@ -387,6 +387,46 @@ def test_masked_nodes_of_few_rows(bnd, dtype, cdtype, D, value):
             assert torch.isnan(o[0, [1, 2]]).all()
 
 
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+@pytest.mark.parametrize("T", [4, 21])
+@pytest.mark.parametrize("size", [8.0, 2.0 ** 18 + 2.0 ** 16])
+def test_rows_do_not_depend_on_their_neighbours(bnd, dtype, cdtype, T, size):
+    """Rows with the same score at every position, beside rows whose maximum moves at every step: an output is the mean of
+    the values it sees whatever other nodes and heads do, to the bit. 16 rows a key head, and many."""
+    items, H, Hk, D, old = 6, 8, 2, 64, 250
+    c = U.cache(45, items, [old] * items, Hk, D, 16, dtype, cdtype)
+    ramp, rows = torch.zeros(old, D), torch.arange(old)
+    ramp[:, 0], ramp[:, 1] = 1, rows // 16
+    for b in range(items):
+        pages = c["page_table"][b].cpu()[rows // 16].cuda()
+        c["k_cache"][pages, :, (rows % 16).cuda()] = ramp.cuda()[:, None].expand(-1, Hk, -1).to(c["k_cache"].dtype)
+        if cdtype == E4:
+            c["k_scale"][pages, :, (rows % 16).cuda()] = 1.0
+    q, k, v = nodes(46, items, T, H, Hk, D, dtype)
+    q.zero_()
+    k.zero_()
+    q[..., 0], k[..., 0] = size, 1
+    par = U.trees(47, items, T, "star").cuda()
+    args, scales = U.cache_args(c)
+    run = lambda x: bnd.attn_verify(x, k, v, par, *args, **scales)
+    want, page = run(q), c["k_cache"].shape[2]
+    for b in range(items):
+        vc = S.cache_rows(U.np8(c["v_cache"]), U.np8(c["v_scale"]), c["page_table"][b].cpu().numpy(), old, page)
+        for i in (0, 1, T - 1):
+            see = np.concatenate([vc, U.f64(v[b, sorted({0, i})])])
+            mean, oa = see.mean(0), np.abs(see).mean(0)
+            # the weights are equal: the sums round, in bf16 the output, and for many rows the weight beside its sum
+            half = 2.0 ** -8 if dtype == BF else 0.0
+            bound = (old + 64) * 2.0 ** -24 * oa + half * (np.abs(mean) * 1.01 + (oa if T > 4 else 0)) + 1e-30
+            U.within(U.f64(want[b, i]).reshape(Hk, 4, D), mean[:, None], bound[:, None], f"mean {b} {i}")
+    x = q.clone()
+    x[:, :, 1::2, 1] = 4.0
+    x[:, :2, :, 1] = 2.0
+    got = run(x)
+    assert torch.equal(got[:, 2:, ::2], want[:, 2:, ::2])
+    assert not torch.equal(got[:, :2], want[:, :2])
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("T", [1, 3, 33])
