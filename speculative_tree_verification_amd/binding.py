@@ -1194,7 +1194,7 @@ def attn_append(k, v, seq_start, k_cache, v_cache, page_table, cache_len, k_scal
 @functools.lru_cache(maxsize=4096)
 def _attn_prefill_workspace(*fields) -> int:
     need = ctypes.c_uint64()
-    rc = lib.tree_attn_prefill_workspace(ctypes.byref(AttnShape(*fields)), ctypes.byref(need))
+    rc = lib.tree_attn_prefill_workspace(_attn_shape(*fields), ctypes.byref(need))
     if rc != 0:
         raise TreeSSDError(rc, "tree_attn_prefill_workspace")
     return need.value
@@ -1212,6 +1212,8 @@ def attn_prefill(q, seq_start, k_cache, v_cache, page_table, cache_len, k_scale=
     were in a given ``o``, and undefined in one made here."""
     L, H, D = q.shape
     at, io, Bt = q.get_device(), q.dtype, cache_len.shape[0]
+    _fits(window, "window")
+    _fits(sinks, "sinks")
     _need(q, "q", (L, H, D), io, at)
     _need(seq_start, "seq_start", (Bt + 1,), torch.int32, at)
     if seq_status is not None:
@@ -1269,12 +1271,26 @@ def _need_rows(t, name: str, rows, row, dtype, at: int) -> int:
     return _distance(t.shape, t.stride(), len(rows), name)
 
 
-# the structures of a call, by their values: forming one costs a microsecond
-_attn_shape = functools.lru_cache(maxsize=4096)(lambda *fields: AttnShape(*fields))
-_rope_struct = functools.lru_cache(maxsize=4096)(lambda *fields: Rope(*fields))
-_conv_struct = functools.lru_cache(maxsize=4096)(lambda *fields: Conv(*fields))
-_seq_shape = functools.lru_cache(maxsize=4096)(lambda *fields: SeqShape(*fields))
-_tree_shape = functools.lru_cache(maxsize=4096)(lambda *fields: Shape(*fields))
+def _fits(value: int, name: str) -> int:
+    """A number that a 32-bit argument holds (ctypes would cut any other without a word)."""
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name}: {value} does not fit into 32 bits")
+    return value
+
+
+def _struct(cls):
+    """Structures of a call by their values (forming one costs a microsecond), each number as it was given."""
+    def make(*fields):
+        s = cls(*fields)
+        for (name, kind), value in zip(cls._fields_, fields):
+            if kind is ctypes.c_int32:
+                _fits(value, name)
+        return s
+    return functools.lru_cache(maxsize=4096)(make)
+
+
+_attn_shape, _rope_struct, _conv_struct = _struct(AttnShape), _struct(Rope), _struct(Conv)
+_seq_shape, _tree_shape = _struct(SeqShape), _struct(Shape)
 
 
 def _rope_weights(inv_freq, q_weight, k_weight, D, at):
@@ -1470,6 +1486,7 @@ def conv_commit(xbc, state, parent, accepted, accepted_len, n_heads: int, head_d
     _need(accepted_len, "accepted_len", (Bt,), torch.int32, at)
     if tree_status is not None:
         _need(tree_status, "tree_status", (Bt,), torch.int32, at)
+    _fits(Lmax, "accepted")
     conv = _conv_struct(back + 1, _need_rows(xbc, "xbc", (Bt, T), (channels,), io, at), 0)
     shape = _tree_shape(Bt, T, n_heads, head_dim, d_state, n_groups, _dtype_code(xbc), 0, 0)
 

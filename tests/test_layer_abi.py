@@ -237,3 +237,34 @@ def test_append_of_no_rows():
     for q in (None, FAKE):
         assert append(attn(n_nodes=0), rot(), [q, None, None] + [FAKE] * 11) == OK
     assert append(attn(n_nodes=0, n_pages=0, max_pages=0), rot(), [None] * 3 + [FAKE, FAKE] + [None] * 3 + [FAKE] + [None] * 5) == OK
+
+
+def test_numbers_past_32_bits_are_refused():
+    """A number that its argument cannot hold is refused, and not cut to one that it can."""
+    torch = pytest.importorskip("torch")
+    z = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype, device="meta")
+    i32 = torch.int32
+    start, c, table, n = z(2, dtype=i32), z(2, 2, 16, 8), z(1, 1, dtype=i32), z(1, dtype=i32)
+    for big in (2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63 - 1, -2 ** 32 + 5):
+        with pytest.raises(ValueError, match="window"):
+            B.attn_prefill(z(3, 2, 8), start, c, c, table, n, window=big)
+        with pytest.raises(ValueError, match="sinks"):
+            B.attn_prefill(z(3, 2, 8), start, c, c, table, n, window=5, sinks=big)
+    far = torch.empty_strided((3, 16), (2 ** 32 + 16, 1), device="meta")
+    x, b, taps = z(3, 1, 8), z(3, 1, 4), z(16, 4)
+    with pytest.raises(ValueError, match="row_stride"):
+        B.conv_step(far, taps, None, z(3, 3, 16), x, b, b)
+    with pytest.raises(ValueError, match="row_stride"):
+        B.conv_prefill(far, taps, None, z(1, 3, 16), start, x, b, b)
+    one = z(3, 1, dtype=i32)
+    with pytest.raises(ValueError, match="row_stride"):
+        B.conv_verify(far[:, None], taps, None, z(3, 3, 16), one, x[:, None], b[:, None], b[:, None])
+    with pytest.raises(ValueError, match="row_stride"):
+        B.conv_commit(far[:, None], z(3, 3, 16), one, one, z(3, dtype=i32), 1, 8, 1, 4)
+    with pytest.raises(ValueError, match="accepted"):
+        B.conv_commit(z(3, 1, 16), z(3, 3, 16), one, z(3, 2 ** 32 + 1, dtype=i32), z(3, dtype=i32), 1, 8, 1, 4)
+    rows = 2 ** 32 + 3
+    with pytest.raises(ValueError, match="n_nodes"):
+        B.attn_rope(z(rows, 1, 8), None, z(rows, dtype=i32), z(4))
+    with pytest.raises(ValueError, match="n_nodes"):
+        B.attn_prefill_workspace_bytes(1, rows, 2, 2, 64, 16, 4)
