@@ -26,15 +26,6 @@
 namespace tsv {
 namespace {
 
-__device__ __forceinline__ f32x4 mma4(float4 a, float4 b, f32x4 c) {
-    c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x, b.x, c, 0, 0, 0);
-    c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.y, b.y, c, 0, 0, 0);
-    c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.z, b.z, c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x4f32(a.w, b.w, c, 0, 0, 0);
-}
-
-__device__ __forceinline__ bool odd_value(float v) { return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u; }
-
 template <int D, bool E4M3, int WK>
 __global__ __launch_bounds__(256, 2) void chunk_f32_kernel(ChunkArgs a, ChunkPlan plan, ChunkWorkspace ws) {
     constexpr int M = 64 / WK, kS = D + 4, NX = 4 / WK;
@@ -151,7 +142,7 @@ __global__ __launch_bounds__(256, 2) void chunk_f32_kernel(ChunkArgs a, ChunkPla
                 for (int i = 0; i < D / 4; ++i) {
                     const size_t d = row * D + 64 * (i / 16) + 16 * lg + i % 16;
                     const float f = E4M3 ? e4m3_ld((const uint8_t*)a.v_cache + d) : gload((const float*)a.v_cache + d);
-                    if (here && odd_value(f)) o[4 * (i / 16) + i % 4][i % 16 / 4] += f;
+                    if (here && nonfinite(f)) o[4 * (i / 16) + i % 4][i % 16 / 4] += f;
                     if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -227,10 +218,10 @@ __global__ __launch_bounds__(256, 2) void chunk_f32_kernel(ChunkArgs a, ChunkPla
                         // finite enter as 0 and are added for the rows that see them
                         if (t + key >= kk.k1) {
                             f[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        } else if (odd_value(f[e].x) || odd_value(f[e].y) || odd_value(f[e].z) || odd_value(f[e].w)) {
+                        } else if (nonfinite(f[e].x) || nonfinite(f[e].y) || nonfinite(f[e].z) || nonfinite(f[e].w)) {
                             atomicOr(&s_odd[set][key / 32], 1u << (key % 32));
-                            f[e] = make_float4(odd_value(f[e].x) ? 0.f : f[e].x, odd_value(f[e].y) ? 0.f : f[e].y,
-                                               odd_value(f[e].z) ? 0.f : f[e].z, odd_value(f[e].w) ? 0.f : f[e].w);
+                            f[e] = make_float4(nonfinite(f[e].x) ? 0.f : f[e].x, nonfinite(f[e].y) ? 0.f : f[e].y,
+                                               nonfinite(f[e].z) ? 0.f : f[e].z, nonfinite(f[e].w) ? 0.f : f[e].w);
                         }
                     }
                     *(float4*)&s_V[key * kS + pcol / EB + 4 * e] = f[e];

@@ -24,20 +24,6 @@ constexpr int kSub = 32;  // keys of a step
 // left of its steps
 constexpr int kOddSteps = 12;
 
-__device__ __forceinline__ bool nonfinite(float v) { return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u; }
-
-__device__ __forceinline__ bf16x8 as_operand(uint4 u) { return __builtin_bit_cast(bf16x8, u); }
-
-__device__ __forceinline__ uint4 only_finite(uint4 u) {
-    uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
-        if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0x0000ffffu;
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 __device__ __forceinline__ uint32_t chunk_row(const ChunkArgs& a, int page, int hk, int pos) {
     return ((uint32_t)page * a.Hk + hk) * a.page_size + (pos - page_of(pos, a.div) * a.page_size);
 }

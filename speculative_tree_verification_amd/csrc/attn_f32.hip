@@ -24,15 +24,6 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ f32x4 mma4(float4 a, float4 b, f32x4 c) {
-    c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x, b.x, c, 0, 0, 0);
-    c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.y, b.y, c, 0, 0, 0);
-    c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.z, b.z, c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x4f32(a.w, b.w, c, 0, 0, 0);
-}
-
-__device__ __forceinline__ bool odd_value(float v) { return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u; }
-
 template <int D, bool E4M3, int WK>
 __global__ __launch_bounds__(256, 2) void attn_f32_kernel(AttnArgs a, AttnPlan plan, AttnWorkspace ws, int row_blocks) {
     constexpr int M = 64 / WK, kS = D + 4, NX = 4 / WK;
@@ -156,10 +147,10 @@ __global__ __launch_bounds__(256, 2) void attn_f32_kernel(AttnArgs a, AttnPlan p
                     kf = gload((const float4*)(kp + (size_t)(j0 + key) * stride + d));
                     vf = gload((const float4*)(vp + (size_t)(j0 + key) * stride + d));
                 }
-                if (odd_value(vf.x) || odd_value(vf.y) || odd_value(vf.z) || odd_value(vf.w)) {
+                if (nonfinite(vf.x) || nonfinite(vf.y) || nonfinite(vf.z) || nonfinite(vf.w)) {
                     atomicOr(&s_odd[(j0 + key) / 32], 1u << ((j0 + key) % 32));
-                    vf = make_float4(odd_value(vf.x) ? 0.f : vf.x, odd_value(vf.y) ? 0.f : vf.y, odd_value(vf.z) ? 0.f : vf.z,
-                                     odd_value(vf.w) ? 0.f : vf.w);
+                    vf = make_float4(nonfinite(vf.x) ? 0.f : vf.x, nonfinite(vf.y) ? 0.f : vf.y, nonfinite(vf.z) ? 0.f : vf.z,
+                                     nonfinite(vf.w) ? 0.f : vf.w);
                 }
                 *(float4*)&s_K[key * kS + d] = kf;
                 *(float4*)&s_V[key * kS + d] = vf;
@@ -179,7 +170,7 @@ __global__ __launch_bounds__(256, 2) void attn_f32_kernel(AttnArgs a, AttnPlan p
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float f = gload(v + 64 * h + 4 * r + e);
-                            if (odd_value(f)) o[4 * h + e][r] += f;
+                            if (nonfinite(f)) o[4 * h + e][r] += f;
                         }
             }
         }

@@ -45,6 +45,16 @@ __device__ __forceinline__ float row_sum(float v) {
     return q.a + q.b;
 }
 
+// Four k-slots of an fp32 product
+__device__ __forceinline__ f32x4 mma4(float4 a, float4 b, f32x4 c) {
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x, b.x, c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.y, b.y, c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.z, b.z, c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a.w, b.w, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ bool nonfinite(float v) { return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u; }
+
 // Whether `page`, what the table holds, is a page of the pool; and the row index of
 // position `pos`, which lies on it, in the cache's arrays (of another page, or of
 // none: take page 0, whose rows exist, and the item's status bit).

@@ -31,8 +31,6 @@ namespace {
 
 constexpr int kStepKeys = 32;  // keys of a wave's step in the row kernel
 
-__device__ __forceinline__ bf16x8 as_operand(uint4 u) { return __builtin_bit_cast(bf16x8, u); }
-
 // q with the sign of the scores' factor
 __device__ __forceinline__ bf16x8 query_operand(const AttnArgs& a, uint4 u) {
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
@@ -41,16 +39,7 @@ __device__ __forceinline__ bf16x8 query_operand(const AttnArgs& a, uint4 u) {
 
 // A node's value that is not finite may reach the rows that see the node only,
 // but a product would carry it to all rows, at weight 0. So such elements enter
-// the product as 0, and afterwards each row adds those of the nodes it sees.
-__device__ __forceinline__ uint4 only_finite(uint4 u) {
-    uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
-        if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0x0000ffffu;
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
+// the product as 0 (only_finite), and afterwards each row adds those of the nodes it sees.
 // v: the node's values from this lane's first d on; o's element e holds d = e / 4 * STEP + e % 4
 template <int NO, int STEP = 16, class Acc>
 __device__ __forceinline__ void add_nonfinite(const uint16_t* v, Acc* o) {

@@ -54,6 +54,18 @@ __device__ __forceinline__ uint32_t nonfinite_bits(uint4 u) {
            ((u.z & 0x7fff7fffu) + 0x00800080u) | ((u.w & 0x7fff7fffu) + 0x00800080u);
 }
 
+// 8 bf16 values as an operand, and with 0 in place of those that are not finite
+__device__ __forceinline__ bf16x8 as_operand(uint4 u) { return __builtin_bit_cast(bf16x8, u); }
+__device__ __forceinline__ uint4 only_finite(uint4 u) {
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+        if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0x0000ffffu;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // 8 e4m3 bytes as bf16 (exact)
 __device__ __forceinline__ uint4 e4m3_to_bf16(uint2 u) {
     uint32_t r[4];
