@@ -1207,8 +1207,9 @@ def attn_prefill(q, seq_start, k_cache, v_cache, page_table, cache_len, k_scale=
     [Bt+1] int32), over the cache that already holds them behind its cache_len
     positions (tree_attn_prefill): ``attn_append`` or ``attn_append_rope`` first,
     cache_len grows afterwards. ``window`` > 0: a row sees its last ``window``
-    positions, itself included, and the first ``sinks``. Caches, scales, ``scale``
-    and ``workspace`` as for ``attn_verify``. Rows of no sequence are left as they
+    positions, itself included, and the first ``sinks``. A long chunk among many
+    single tokens, or in a batch with many empty items, is faster in a call of its
+    own. Caches, scales, ``scale`` and ``workspace`` as for ``attn_verify``. Rows of no sequence are left as they
     were in a given ``o``, and undefined in one made here."""
     L, H, D = q.shape
     at, io, Bt = q.get_device(), q.dtype, cache_len.shape[0]
@@ -1308,8 +1309,8 @@ def attn_rope(q, k, position, inv_freq, q_weight=None, k_weight=None, eps: float
               q_out=None, k_out=None, stream=None):
     """(q_out, k_out): the heads' norms (where a weight [D] is given) and the
     position rotation of q [...,H,D] and k [...,Hk,D] (tree_attn_rope); either
-    may be None. position [...] int32 (negative: the row is left as it was),
-    inv_freq [rot_dim/2] float32; ``interleaved`` rotates neighbouring elements,
+    may be None. position [...] int32 (negative: the row is left as it was in a
+    given output, and undefined in one made here), inv_freq [rot_dim/2] float32; ``interleaved`` rotates neighbouring elements,
     otherwise (i, i + rot_dim/2). Rows may be slices of a projection's output; a
     contiguous q or k may be its own output."""
     given = q if q is not None else k

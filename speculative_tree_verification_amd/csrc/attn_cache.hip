@@ -12,9 +12,9 @@
 // so that the stored byte is the nearest to row / scale. A work-group first
 // checks everything that its rows' items need (path, lengths, pages), so that
 // an item with a status bit is left whole; in append the rows are on their way
-// meanwhile. 16 prompts, 16378 rows of 8 heads of 128 into e4m3 (102 MB): 30 us,
-// 3.4 TB/s, half of it the vector work (fetching after the search 31.6 us against
-// 30.0, the butterfly through LDS 30.0 against 29.0).
+// meanwhile. 16 prompts, 16378 rows of 8 heads of 128 into e4m3 (102 MB): 27 us,
+// 3.8 TB/s, half of it the vector work (at earlier steps: fetching after the search
+// 31.6 us, 30.0 before it; the butterfly through LDS 30.0, by lane moves 29.0).
 #include "attn_cache.hpp"
 
 namespace tsv {
@@ -74,8 +74,6 @@ template <typename TIO, int LPR, bool E4M3, bool VEC>
 __global__ __launch_bounds__(256) void append_kernel(CacheWriteArgs a, int row_blocks) {
     __shared__ RowPlaces<kRows> places;
     const int tid = threadIdx.x;
-    // the packing, and the sequence of this block's first row: the sequences
-    // that end at or before it
     const int r0 = blockIdx.x * kRows;
     const bool rows = (int)blockIdx.x < row_blocks;
     const int n = rows ? min(kRows, a.T - r0) : 0;

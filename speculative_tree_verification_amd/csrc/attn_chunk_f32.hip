@@ -13,10 +13,11 @@
 // same 16 rows, a quarter of the keys each, which meet at the end.
 //
 // Many rows are bound by the fp32 matrix unit, which waits for LDS and the softmax of its own
-// step: 2 chunks of 500 tokens behind 1000 positions, 32 query and 8 key heads of 128, 230 us
-// (89 TFLOP/s; a large fp32 product reaches 154); 3 prompts of 130 to 777 tokens in a window of
+// step: 2 chunks of 500 tokens behind 1000 positions, 32 query and 8 key heads of 128, 218 us
+// (94 TFLOP/s; a large fp32 product reaches 154; over an e4m3 cache 239 us); 3 prompts of 130 to 777 tokens in a window of
 // 255, 24 and 3 heads of 64, 29.3 us, the unit busy in 35% of the cycles. Few rows are bound by
-// the cache's bytes: 32 tokens over 2200 positions, 578 MB, 118 us (4.9 TB/s). Weights stay in fp32.
+// the cache's bytes: 32 tokens over 2200 positions, 578 MB, 116 us (5.0 TB/s). In e4m3 those are
+// 150 MB, but the products are the same: 84 us. Weights stay in fp32.
 #include <cfloat>
 #include <type_traits>
 

@@ -33,8 +33,9 @@ __device__ __forceinline__ uint32_t chunk_row(const ChunkArgs& a, int page, int 
 // each in turn and meet at the end; K goes from memory into the operand registers, V through
 // LDS. The weights enter the product with V as two bf16 parts: free here, since the kernel
 // is bound by the cache's bytes (32 query and 8 key heads of 128: one token over 65532
-// positions, 268 MB, 53.1 us with the join, 5.1 TB/s; 64 tokens with windows of 1021, 251 MB,
-// 50.5 us; 64 over e4m3 caches of 17 to 8190 positions 116 to 123 us, 4.7 TB/s).
+// positions, 268 MB, 65 us with the join, 4.1 TB/s, and 51 where the last call left most of it in
+// the last-level cache; 64 tokens with windows of 1021, 251 MB, 50.7 us; 64 over e4m3 caches of 17
+// to 8190 positions 116 us, 4.8 TB/s).
 template <int ND, bool E4M3>
 __global__ __launch_bounds__(256, 3) void chunk_rows_kernel(ChunkArgs a, ChunkPlan plan, ChunkWorkspace ws) {
     constexpr int D = ND * 32, M = 16, kVs = D + 16, kOs = D + 4;
@@ -302,16 +303,20 @@ __global__ __launch_bounds__(256, 3) void chunk_rows_kernel(ChunkArgs a, ChunkPl
 //
 // The weights are rounded to bf16 once, relative to a maximum that they pass by a factor of
 // 2^kSlack at most, and the sum is formed before: a second part, as above, would be half of the
-// matrix products again. Each weight is off by 2^-8 of itself at most, and outputs by 0.0021 to
-// 0.0024 of their size on average, of which their own rounding is 0.0017.
+// matrix products again. Each weight is off by e_j, 2^-8 of itself at most, and an output by sum w_j
+// e_j v_j / sum w_j: 0.0021 to 0.0024 of its size on average, of which its own rounding is 0.0017. (The
+// sum of the rounded weights would make it sum w_j e_j (v_j - o) / sum w_j: less where one key has most
+// of the weight, but up to twice as much where values differ in sign.)
 //
-// Bound by the matrix and the vector unit of two waves a SIMD, and by the clock that the card's
-// power leaves them (2.0 GHz): 4096 tokens, 32 query and 8 key heads of 128, 155 us, 889
-// TFLOP/s, the matrix unit busy in 41% of the cycles and the vector unit issuing in 42%; 509
+// Bound by three units that two waves a SIMD keep busy in turn, none of them to the end, and by
+// the clock that the card's power leaves them (2.0 GHz): 4096 tokens, 32 query and 8 key heads of
+// 128, 155 us, 889 TFLOP/s, the matrix unit busy in 41% of the cycles, the vector unit issuing in
+// 42%, and LDS, from which each wave reads all of a step's keys and values for its 32 rows, active
+// in 34% (18.3 MB read and 4.5 written a compute unit: 54% at 128 bytes a cycle); 509
 // tokens behind 32749 positions 294 us, 938 TFLOP/s. At an earlier step (177 and 319 us) slower
 // were 64 rows a wave, with operands read for twice the rows but one wave a SIMD (207 and 344),
 // and all scores of a step before the product with V (182 and 321). D 64 forms as many weights
-// for half of the products: 110 us for 4096 tokens (625 TFLOP/s). e4m3 steps pay for their
+// for half of the products: 104 us for 4096 tokens (660 TFLOP/s). e4m3 steps pay for their
 // conversion: 16 chunks of 1 to 701 tokens behind 0 to 4099 positions 286 us, 750 TFLOP/s; the
 // LDS bank conflicts of the converted pieces (9% of its cycles) cost nothing (306 us, 309 without).
 template <int ND, bool E4M3>

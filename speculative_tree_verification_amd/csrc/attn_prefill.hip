@@ -11,8 +11,8 @@
 // waves take 64 keys each in turn. Scores: a lane per key, the rows' q from LDS (the same
 // for all lanes). Values: lanes over the head_dim, weights from LDS. Bound by the vector
 // ALU and the LDS broadcasts (4 D operations per row and key): 512
-// tokens, 32 query and 8 key heads of 80, 127 us (11 TFLOP/s), 16 and 4 heads of 256 162 us; 32
-// single tokens over 2200 positions each, heads of 80, 226 us.
+// tokens, 32 query and 8 key heads of 80, 123 us (11 TFLOP/s), 16 and 4 heads of 256 201 us; 32
+// single tokens over 2200 positions each, heads of 80, 283 us.
 #include "attn_chunk.hpp"
 
 namespace tsv {
@@ -302,22 +302,28 @@ bool matrix_shape(const tsv_attn_shape* s) {
            (long long)s->n_pages * s->n_kv_heads * s->page_size < (1LL << 32);
 }
 
-// Rows of a block, by those that the sequences have of a key head on average:
+// Rows of a block, by those that the sequences (empty ones among them) have of a key head on
+// average, since the host does not know their lengths:
 //   bf16   16 (chunk_rows_kernel) up to 16, as single tokens do, otherwise 128
-//          (chunk_tiles_kernel). 8 single tokens over 1000 positions 17.4 us, 22.5 in blocks of
-//          128; 32 chains of 8 tokens, 32 rows, over 4096 117 us, 130 in blocks of 16
-//   fp32   16 up to 32 rows, otherwise 64. 32 single tokens over 4096 positions 205 us, 238 in
-//          blocks of 64; 32 chains of 8 tokens 266 and 316
+//          (chunk_tiles_kernel). 8 single tokens over 1000 positions 15.9 us, 22.8 in blocks of
+//          128; 32 chains of 5 tokens, 20 rows, over 4096 114 us, 125 in blocks of 16
+//   fp32   16 up to 32 rows, otherwise 64. 32 single tokens over 4096 positions 201 us, 235 in
+//          blocks of 64; 32 chains of 8 tokens 255 and 319, of 16 tokens 438 in blocks of 16, 331
 //   plain  8
+// So a long chunk beside many single tokens goes in blocks of 16 (512 tokens behind 30000
+// positions and 256 behind 1000: 1268 us, 487 as two calls; beside 64 of them 335 and 346).
 // Work-groups wanted, for x of them that would run without any cut:
-//   tiles  one round of two a compute unit (a chunk of 509 over 33258 positions: 316 us, 388
-//          for half as many, 339 for twice)
+//   tiles  one round of two a compute unit (a chunk of 509 over 33258 positions: 312 us, 362
+//          for half as many, 325 for twice)
 //   rows   few parts while they fill one round, small ones where many items of different
 //          lengths share the GPU (us for half as many, as here, and twice: 1 token over 65532
-//          positions 54, 55, 59; 8 over 4000 32, 32, 35; 64 over 17 to 8190 in e4m3 124, 123, 131)
-// (at earlier steps of the kernels.) No block is cut that has no more than 512 keys, nor where a window bounds every block and
-// blocks fill the GPU (64 tokens, windows of 1021: 55 us, 65 with a second launch that finds
-// nothing to join).
+//          positions 62, 64, 68; 8 over 4000 34, 34, 38; 32 over 2200 62, 65, 69; 64 over 17 to
+//          8190 in e4m3 118, 115, 122)
+// No block is cut that has no more than 512 keys, nor where a window bounds every block and
+// blocks fill the GPU (64 tokens, windows of 1021: 50.6 us, 65.2 cut, most of it a second launch
+// that finds little to join; 4096 tokens in a window of 1024 84 and 88). A window that is longer
+// than most caches bounds little: 63 tokens behind 100 positions and one behind 65000 take 682 us
+// in a window of 65536, 114 without one.
 ChunkPlan plan_of(const tsv_attn_shape* s, bool matrix, int window, int sinks) {
     ChunkPlan p;
     const int g = s->n_heads / s->n_kv_heads;
@@ -335,7 +341,8 @@ ChunkPlan plan_of(const tsv_attn_shape* s, bool matrix, int window, int sinks) {
     long long longest = (long long)s->max_pages * s->page_size;
     if (window > 0 && longest > (long long)window + sinks + p.rows) longest = (long long)window + sinks + p.rows;
     p.split = longest > 2 * p.min_keys && s->n_kv_heads <= p.want && !(window > 0 && blocks * s->n_kv_heads >= 512);
-    // long work-groups should not start last (their order costs each a search of a microsecond)
+    // long work-groups should not start last (their order costs each a search of a microsecond: 16
+    // mixed e4m3 chunks 295 us, 318 in the sequences' order)
     p.sorted = p.rows > 16 && s->batch > 1 && s->batch <= kWave;
     return p;
 }
