@@ -661,8 +661,9 @@ tsv_status tree_attn_append(const tsv_attn_shape* s, const void* k, const void* 
  *   y_t = act(bias + sum_{k < W} weight[W-1-k] u_{t-k}),
  * split into the x, B and C that the SSM calls take. The state holds the last
  * W - 1 inputs of an item, oldest first; an item without a past has zeros. The v,
- * k and q of a gated-delta-rule layer are such x, B and C with G = H: where its
- * projection gives them as q, k, v, its rows, weight and bias change places.
+ * k and q of a gated-delta-rule layer are such x, B and C (G its key heads, which
+ * tree_gdn_verify takes one for each head): where its projection gives them as q,
+ * k, v, the rows of its weight, and weight and bias here, change places.
  *
  *   xbc    rows of C channels, row_stride elements apart   in_dtype
  *   weight [C][W]           float      the tap of the newest input last
